@@ -311,6 +311,184 @@ LA_API size_t la_bwd_workspace_size(int B, int H, int T, int d_k, int d_v, la_dt
                                     unsigned flags);
 
 /*
+ * Queries and keys made ready for retention, in one pass: the norm of every
+ * head's row, the rotation by its token's position, a scale, and the layout
+ * la_chunk_fwd and la_recurrent_step read.
+ *
+ *   n = x r w,  r = (mean(x^2) + eps)^(-1/2)     with LA_QK_NORM, else n = x
+ *   (y_i, y_j) = s (n_i cos - n_j sin, n_i sin + n_j cos),  angle p inv_freq[m],
+ *       for pair m = 0 .. rot/2 - 1 of the first rot entries: (m, m + rot/2), or
+ *       (2m, 2m + 1) with LA_QK_ADJACENT;  y = s n for the other entries
+ *
+ * RetNet rotates its queries and keys by their position before the retention;
+ * decode is the same call with T = 1.
+ *
+ *   q, k      [B][T][Hq][d], [B][T][Hk][d] dtype, rows of d entries dense, the
+ *             other strides free (slices of a packed projection; a stride of 0
+ *             repeats a row).  q_strides, k_strides: HOST arrays of 3 strides
+ *             (batch, token, head) in elements, each >= 0 and a multiple of 16
+ *             bytes, or NULL for the dense layout.  The stride of a dimension of
+ *             size 1 is not read.
+ *   d         a multiple of 16 in [16, 256];  rot a multiple of 16 in [0, d]
+ *   inv_freq  HOST double[rot/2], radians per position (rot > 0); finite
+ *   positions DEVICE int32 [B][T], any values, or NULL: token t stands at pos0 + t,
+ *             0 <= pos0 and pos0 + T - 1 < 2^31.  The angle keeps fp32 accuracy at
+ *             every position (its fraction of a turn is taken in 64-bit integers).
+ *   q_weight, k_weight  DEVICE fp32 [d] or NULL (ones); NULL without LA_QK_NORM
+ *   eps       > 0, finite (with LA_QK_NORM)
+ *   q_scale, k_scale    finite
+ *   flags     LA_QK_NORM | LA_QK_ADJACENT
+ *   q_out, k_out  [B][Hq][T][d], [B][Hk][T][d] dtype, dense; they may overlap no
+ *             input and not each other
+ *
+ * Sums, norms and angles are fp32, rounded once to dtype at the end; the sum of a
+ * row's squares must stay below the fp32 range (|x| below about 1e18).
+ * B or T == 0 is a no-op; Hq, Hk in [1, 65536]; B * T < 2^31.
+ * Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
+ */
+#define LA_QK_NORM 1u
+#define LA_QK_ADJACENT 2u
+LA_API la_status la_qk_rotate_fwd(const void* q, const long long* q_strides, const void* k,
+                                  const long long* k_strides, la_dtype dtype, int B, int T, int Hq,
+                                  int Hk, int d, int rot, const double* inv_freq,
+                                  const int* positions, int pos0, const float* q_weight,
+                                  const float* k_weight, float eps, float q_scale, float k_scale,
+                                  unsigned flags, void* q_out, void* k_out, la_stream_t stream);
+
+/*
+ * Gradients of la_qk_rotate_fwd.
+ *
+ *   q, k .. flags   as the forward call
+ *   dq_out, dk_out  [B][Hq][T][d], [B][Hk][T][d] dtype, dense: the loss's gradient
+ *             with respect to q_out, k_out (la_chunk_bwd's dQ, dK)
+ *   dq, dk    [B][T][Hq][d], [B][T][Hk][d] dtype with strides as q's (they may be
+ *             slices of one packed row); their rows may overlap neither each other
+ *             nor any input
+ *   dq_weight, dk_weight  fp32 [d] or NULL: the weights' gradients, summed over
+ *             batch, tokens and heads in a fixed order; overwritten
+ *   workspace at least la_qk_rotate_bwd_workspace_size(...) bytes when a weight
+ *             gradient is asked for, else may be NULL; overwritten.  Calls that may
+ *             run at the same time need a workspace each.
+ * A row repeated by a stride of 0 gets a gradient for each of its uses: the caller
+ * adds them up.  B or T == 0: the weight gradients are zeroed, nothing else is done.
+ * Errors as la_qk_rotate_fwd.
+ */
+LA_API la_status la_qk_rotate_bwd(const void* q, const long long* q_strides, const void* k,
+                                  const long long* k_strides, const void* dq_out,
+                                  const void* dk_out, la_dtype dtype, int B, int T, int Hq, int Hk,
+                                  int d, int rot, const double* inv_freq, const int* positions,
+                                  int pos0, const float* q_weight, const float* k_weight, float eps,
+                                  float q_scale, float k_scale, unsigned flags, void* dq,
+                                  const long long* dq_strides, void* dk, const long long* dk_strides,
+                                  float* dq_weight, float* dk_weight, void* workspace,
+                                  size_t workspace_bytes, la_stream_t stream);
+LA_API size_t la_qk_rotate_bwd_workspace_size(int B, int T, int Hq, int Hk, int d, la_dtype dtype);
+
+/*
+ * The norm and gate of each head's output, retention's [B][H][T][d] to the layer's
+ * row [B][T][H][d]:
+ *
+ *   n = o r, r = (mean(o^2) + eps)^(-1/2)     (o less its mean with LA_GATE_CENTER)
+ *   y = n w  [ g sigmoid(g) ]
+ *
+ * RetNet's per-head norm and swish gate: raw retention outputs grow with the sum
+ * of the decays.  Decode is the same call with T = 1.
+ *
+ *   o         [B][H][T][d] dtype; o_strides: HOST array of 3 strides (batch, head,
+ *             token) in elements or NULL for dense.  The per-channel recurrence's
+ *             [B][T][H d] is read with strides (T H d, d, H d).
+ *   gate      [B][T][H][d] dtype or NULL; gate_strides (batch, token, head) or NULL
+ *   weight    DEVICE fp32 [H][d] or NULL (ones)
+ *   flags     LA_GATE_CENTER;  eps > 0, finite
+ *   y         [B][T][H][d] dtype, y_strides (batch, token, head) or NULL; its rows
+ *             may overlap neither each other nor any input
+ * Strides as la_qk_rotate_fwd: rows dense, strides >= 0 and multiples of 16 bytes.
+ * d a multiple of 16 in [16, 256], H in [1, 65536], B * T < 2^31; sums in fp32 (as
+ * la_qk_rotate_fwd).  B or T == 0 is a no-op.  Errors: LA_ERR_INVALID_ARG,
+ * LA_ERR_CUDA.
+ */
+#define LA_GATE_CENTER 1u
+LA_API la_status la_head_gate_fwd(const void* o, const long long* o_strides, const void* gate,
+                                  const long long* gate_strides, la_dtype dtype,
+                                  const float* weight, int B, int H, int T, int d, unsigned flags,
+                                  float eps, void* y, const long long* y_strides,
+                                  la_stream_t stream);
+
+/*
+ * Gradients of la_head_gate_fwd.
+ *   o, gate, weight, flags, eps   as the forward call
+ *   dy        [B][T][H][d] dtype, dy_strides (batch, token, head) or NULL
+ *   d_o       [B][H][T][d] dtype, do_strides (batch, head, token) or NULL (dense:
+ *             what la_chunk_bwd reads as dO)
+ *   dgate     [B][T][H][d] dtype, dgate_strides or NULL; NULL exactly when gate is
+ *   dweight   fp32 [H][d] or NULL: summed over batch and tokens in a fixed order;
+ *             overwritten
+ *   workspace at least la_head_gate_bwd_workspace_size(...) bytes when dweight is
+ *             asked for, else may be NULL; one for each call that may run at once
+ * The outputs' rows overlap nothing.  B or T == 0: dweight is zeroed, nothing else
+ * is done.  Errors as la_head_gate_fwd.
+ */
+LA_API la_status la_head_gate_bwd(const void* o, const long long* o_strides, const void* gate,
+                                  const long long* gate_strides, const void* dy,
+                                  const long long* dy_strides, la_dtype dtype, const float* weight,
+                                  int B, int H, int T, int d, unsigned flags, float eps, void* d_o,
+                                  const long long* do_strides, void* dgate,
+                                  const long long* dgate_strides, float* dweight, void* workspace,
+                                  size_t workspace_bytes, la_stream_t stream);
+LA_API size_t la_head_gate_bwd_workspace_size(int B, int H, int T, int d, la_dtype dtype);
+
+/*
+ * The per-channel gated recurrence, the member of the family "decay the old state,
+ * add, read out" ("Linear Attention, RWKV, and RetNet", temporalbook 13.3,
+ * subsection 4) with a decay for each token and channel and a state of one number
+ * a channel:
+ *
+ *   h_t = a_t h_(t-1) + x_t,   a_t = exp(log_a[b][t][c])
+ *
+ *   x       [B][T][D] dtype, dense;  D a multiple of 16
+ *   log_a   DEVICE fp32 [B][T][D], natural logs, <= 0 (not checked).  -inf (and
+ *           any value whose exponential is zero in fp32) restarts the channel at its
+ *           token: h_t = x_t whatever came before, infinities and NaN included.
+ *   h0      [B][D] fp32 initial state or NULL for zero; may be h_out itself
+ *           (in-place continuation), else may not overlap it
+ *   h       [B][T][D] dtype, output; may overlap no input
+ *   h_out   [B][D] fp32 final state h_T, or NULL
+ *
+ * The state is fp32 throughout; h is rounded where it is stored.  T == 0: h_out is
+ * the initial state.  B == 0 is a no-op.  B * D at most 2^33.  No workspace.
+ * Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
+ */
+LA_API la_status la_scan_fwd(const void* x, la_dtype dtype, const float* log_a, int B, int T, int D,
+                             const float* h0, void* h, float* h_out, la_stream_t stream);
+
+/*
+ * Gradients of la_scan_fwd for the loss sum_t dh_t . h_t + <dh_T, h_T>:
+ *
+ *   c_t = a_t (dh_t + c_(t+1)), c_T = dh_T;  dx_t = dh_t + c_(t+1),
+ *   dlog_a_t = c_t h_(t-1),  dh0 = c_0
+ *
+ *   log_a, h0   as the forward call;  h: its output
+ *   dh      [B][T][D] dtype;  dh_T [B][D] fp32 or NULL (zero)
+ *   dx      [B][T][D] dtype, dlog_a [B][T][D] fp32: outputs, overlapping nothing
+ *   dh0     [B][D] fp32 or NULL; may be dh_T itself
+ * dlog_a reads h as it was rounded to dtype.  A restarted token passes nothing to
+ * the tokens before it and has dlog_a = 0.  T == 0: dh0 is dh_T.
+ * Errors as la_scan_fwd.
+ */
+LA_API la_status la_scan_bwd(const float* log_a, const void* h, const void* dh, la_dtype dtype,
+                             int B, int T, int D, const float* h0, const float* dh_T, void* dx,
+                             float* dlog_a, float* dh0, la_stream_t stream);
+
+/*
+ * One token of la_scan_fwd: h_out = exp(log_a) h_in + x, h its rounding to dtype.
+ *   x, h [B][D] dtype;  log_a, h_in, h_out [B][D] fp32.  h_out may be h_in itself
+ *   (in place) and otherwise overlaps nothing; h overlaps nothing.
+ * Errors as la_scan_fwd.
+ */
+LA_API la_status la_scan_step(const void* x, la_dtype dtype, const float* log_a, int B, int D,
+                              const float* h_in, float* h_out, void* h, la_stream_t stream);
+
+/*
  * la_chunk_fwd for callers that cannot allocate device memory.  The source
  * pages have no counterpart to this entry point.
  *

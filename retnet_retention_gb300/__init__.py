@@ -14,10 +14,17 @@ Names follow the C ABI:
   recurrent_step(q, k, v, None, S, z, log_a=)  per-token decay     (la_recurrent_step_gated)
   workspace_size(...)                          scratch bytes       (la_workspace_size)
   chunk_fwd_host(...)                          host buffers, copies included (la_chunk_fwd_host)
+Around them, for a whole layer:
+  qk_rotate_fwd(q, k, ...) / qk_rotate_bwd     norm, rotation, layout  (la_qk_rotate_fwd / _bwd)
+  head_gate_fwd(o, gate, ...) / head_gate_bwd  per-head norm and gate  (la_head_gate_fwd / _bwd)
+  scan_fwd(x, log_a, ...) / scan_bwd           per-channel recurrence  (la_scan_fwd / _bwd)
+  scan_step(x, log_a, h, ...)                  one token of it         (la_scan_step)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -29,6 +36,8 @@ LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CUDA, LA_ERR_TIMEOUT = ran
 LA_DTYPE_F32, LA_DTYPE_BF16 = 0, 1
 LA_PHI_ELU1, LA_NORMALIZE, LA_NONCAUSAL, LA_NORM_FLOOR, LA_GATED, LA_PHI_TAYLOR = 1, 2, 4, 8, 16, 32
 LA_OPT_PATH, LA_OPT_TC_LOCKSTEP, LA_OPT_FORCE_TIMEOUT = 1, 2, 3
+LA_QK_NORM, LA_QK_ADJACENT = 1, 2
+LA_GATE_CENTER = 1
 
 LIBRARY_PATH = _build.LIBRARY
 _LIB = None
@@ -101,6 +110,27 @@ def _load() -> ctypes.CDLL:
     lib.la_chunk_fwd_host.argtypes = [vp, vp, vp, i, vp, i, i, i, i, i, u, f, vp, vp, vp, vp, vp,
                                       i, i, vp, sz, vp, vp]
     lib.la_chunk_fwd_host.restype = i
+    lib.la_qk_rotate_fwd.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, i, vp, vp, f, f, f,
+                                     u, vp, vp, vp]
+    lib.la_qk_rotate_fwd.restype = i
+    lib.la_qk_rotate_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, i, vp, vp,
+                                     f, f, f, u, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.la_qk_rotate_bwd.restype = i
+    lib.la_qk_rotate_bwd_workspace_size.argtypes = [i, i, i, i, i, i]
+    lib.la_qk_rotate_bwd_workspace_size.restype = sz
+    lib.la_head_gate_fwd.argtypes = [vp, vp, vp, vp, i, vp, i, i, i, i, u, f, vp, vp, vp]
+    lib.la_head_gate_fwd.restype = i
+    lib.la_head_gate_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, i, i, i, i, u, f, vp, vp, vp, vp,
+                                     vp, vp, sz, vp]
+    lib.la_head_gate_bwd.restype = i
+    lib.la_head_gate_bwd_workspace_size.argtypes = [i, i, i, i, i]
+    lib.la_head_gate_bwd_workspace_size.restype = sz
+    lib.la_scan_fwd.argtypes = [vp, i, vp, i, i, i, vp, vp, vp, vp]
+    lib.la_scan_fwd.restype = i
+    lib.la_scan_bwd.argtypes = [vp, vp, vp, i, i, i, i, vp, vp, vp, vp, vp, vp]
+    lib.la_scan_bwd.restype = i
+    lib.la_scan_step.argtypes = [vp, i, vp, i, i, vp, vp, vp, vp]
+    lib.la_scan_step.restype = i
     lib.la_debug_set.argtypes = [i, i]
     lib.la_debug_set.restype = i
     lib.la_trace_enable.argtypes = [i]
@@ -543,7 +573,302 @@ def chunk_fwd_host(q, k, v, gamma, *, phi=False, normalize=False, causal=True, e
     return out, S_out, z_out
 
 
-__all__ = ["chunk_fwd", "chunk_bwd", "chunk_fwd_noalloc", "recurrent_step", "state_init", "workspace_size", "chunk_fwd_host",
+@contextlib.contextmanager
+def _launch_on(dev, stream):
+    """The tensors' device and the launch stream made current, so that what a call
+    allocates (outputs, workspace) belongs to the stream its kernels run on."""
+    with _current(dev):
+        if stream is None:
+            yield _stream(None)
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}; the inputs are on {dev}")
+        with torch.cuda.stream(stream):
+            yield _stream(stream)
+
+
+def _rows(t, name: str, shape: tuple, dtype, dev):
+    """Address and host array of the three outer strides of a [.., .., .., d] tensor
+    whose rows of d entries are dense (None passes): what the library's strided
+    arguments take.  Shape, dtype and device are checked here, alignment there."""
+    if t is None:
+        return None, None
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}; {shape} is needed")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}; the inputs are on {dev}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the entries of a row must lie one after another")
+    return t.data_ptr(), (ctypes.c_longlong * 3)(*t.stride()[:3])
+
+
+def _dense(t, name: str, shape: tuple, dtype, dev) -> int | None:
+    """Address of a contiguous tensor of exactly this shape, dtype and device."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}; {shape} is needed")
+    _buffer(t, name, 0, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=64)
+def _frequencies(rot: int, base: float):
+    return tuple(float(base) ** (-2.0 * m / rot) for m in range(rot // 2))
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0) -> list[float]:
+    """base^(-2 m / rot) for the rot / 2 pairs of a rotation: qk_rotate_fwd's inv_freq."""
+    if rot < 0 or rot % 2:
+        raise ValueError(f"rot must be even and not negative, not {rot}")
+    return list(_frequencies(int(rot), float(base)))
+
+
+class _QkCall:
+    """The arguments qk_rotate_fwd and qk_rotate_bwd share, checked."""
+
+    def __init__(self, q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight, k_weight,
+                 eps, q_scale, k_scale):
+        if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+            raise ValueError(f"shape mismatch: q{tuple(q.shape)} k{tuple(k.shape)} are [B,T,heads,d]")
+        if q.dtype != k.dtype:
+            raise TypeError("q and k must share one dtype")
+        B, T, Hq, d = q.shape
+        Hk = k.shape[2]
+        self.dev, self.dtype, self.shape = q.device, q.dtype, (B, T, Hq, Hk, d)
+        self.code = _dtype_code(q)
+        rot = d if rot is None else int(rot)
+        if rot < 0 or rot > d or rot % 16:
+            raise ValueError(f"rot must be a multiple of 16 from 0 to {d}, not {rot}")
+        if isinstance(inv_freq, torch.Tensor):
+            if inv_freq.is_cuda:
+                raise ValueError("inv_freq is read on the host: pass host values")
+            inv_freq = inv_freq.tolist()
+        freq = _frequencies(rot, 10000.0) if inv_freq is None else inv_freq
+        if len(freq) != rot // 2:
+            raise ValueError(f"inv_freq holds {len(freq)} values; rot / 2 = {rot // 2} are needed")
+        self.freq = (ctypes.c_double * max(1, rot // 2))(*freq)
+        if positions is not None and (positions.dtype != torch.int32
+                                      or tuple(positions.shape) != (B, T)):
+            raise ValueError(f"positions must be int32 [B,T] = {(B, T)}")
+        pos0 = int(pos0)
+        if not 0 <= pos0 < 2 ** 31:
+            raise ValueError(f"pos0 must be from 0 to 2^31 - 1, not {pos0}")
+        self.flags = (LA_QK_NORM if norm else 0) | (LA_QK_ADJACENT if interleaved else 0)
+        xq, sq = _rows(q, "q", (B, T, Hq, d), self.dtype, self.dev)
+        xk, sk = _rows(k, "k", (B, T, Hk, d), self.dtype, self.dev)
+        f32 = torch.float32
+        self.keep = (sq, sk)
+        self.inputs = (xq, sq, xk, sk)
+        self.rest = (self.code, B, T, Hq, Hk, d, rot, self.freq,
+                     _dense(positions, "positions", (B, T), torch.int32, self.dev), pos0,
+                     _dense(q_weight, "q_weight", (d,), f32, self.dev),
+                     _dense(k_weight, "k_weight", (d,), f32, self.dev),
+                     float(eps), float(q_scale), float(k_scale), self.flags)
+
+
+def qk_rotate_fwd(q, k, *, positions=None, pos0=0, rot=None, inv_freq=None, interleaved=False,
+                  norm=True, q_weight=None, k_weight=None, eps=1e-6, q_scale=1.0, k_scale=1.0,
+                  q_out=None, k_out=None, stream=None):
+    """Norm, rotation by position, scale and layout of queries and keys in one pass.
+
+    q [B,T,Hq,d] and k [B,T,Hk,d] as the projections leave them (slices of a packed
+    row will do: rows of d entries dense, other strides multiples of 16 bytes).
+    Returns (q [B,Hq,T,d], k [B,Hk,T,d]), dense: what chunk_fwd reads, and for T = 1
+    (squeezed) recurrent_step.  positions: int32 [B,T] device tensor, or token t
+    stands at pos0 + t.  rot: the first entries that turn (None: all d), inv_freq:
+    rot/2 host values, radians per position (None: rotary_frequencies(rot));
+    interleaved: pairs (2m, 2m+1), else (m, m + rot/2).  norm: each row divided by
+    the root of its mean square (plus eps), times q_weight / k_weight (fp32 [d])."""
+    a = _QkCall(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight, k_weight, eps,
+                q_scale, k_scale)
+    B, T, Hq, Hk, d = a.shape
+    with _launch_on(a.dev, stream) as s:
+        if q_out is None:
+            q_out = torch.empty((B, Hq, T, d), dtype=a.dtype, device=a.dev)
+        if k_out is None:
+            k_out = torch.empty((B, Hk, T, d), dtype=a.dtype, device=a.dev)
+        st = _load().la_qk_rotate_fwd(*a.inputs, *a.rest,
+                                      _dense(q_out, "q_out", (B, Hq, T, d), a.dtype, a.dev),
+                                      _dense(k_out, "k_out", (B, Hk, T, d), a.dtype, a.dev), s)
+    _check(st, "la_qk_rotate_fwd")
+    return q_out, k_out
+
+
+def qk_rotate_bwd(q, k, dq_out, dk_out, *, positions=None, pos0=0, rot=None, inv_freq=None,
+                  interleaved=False, norm=True, q_weight=None, k_weight=None, eps=1e-6, q_scale=1.0,
+                  k_scale=1.0, dq=None, dk=None, weight_grads=True, workspace=None, stream=None):
+    """Gradients of qk_rotate_fwd for those of its outputs, dq_out [B,Hq,T,d] and
+    dk_out [B,Hk,T,d] (chunk_bwd's dq and dk).  Returns (dq [B,T,Hq,d], dk [B,T,Hk,d],
+    dq_weight [d], dk_weight [d]); a weight's gradient is None where there is no
+    weight or weight_grads is False.  dq and dk may be given, with strides (slices of
+    one packed gradient)."""
+    a = _QkCall(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight, k_weight, eps,
+                q_scale, k_scale)
+    B, T, Hq, Hk, d = a.shape
+    lib = _load()
+    with _launch_on(a.dev, stream) as s:
+        if dq is None:
+            dq = torch.empty((B, T, Hq, d), dtype=a.dtype, device=a.dev)
+        if dk is None:
+            dk = torch.empty((B, T, Hk, d), dtype=a.dtype, device=a.dev)
+        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=a.dev)
+                    if weight_grads and w is not None else None for w in (q_weight, k_weight))
+        need = 0
+        if dwq is not None or dwk is not None:
+            need = int(lib.la_qk_rotate_bwd_workspace_size(B, T, Hq, Hk, d, a.code))
+            if need and workspace is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=a.dev)
+        ws_bytes = _workspace(workspace, need, a.dev)
+        gq = _dense(dq_out, "dq_out", (B, Hq, T, d), a.dtype, a.dev)
+        gk = _dense(dk_out, "dk_out", (B, Hk, T, d), a.dtype, a.dev)
+        st = lib.la_qk_rotate_bwd(*a.inputs, gq, gk, *a.rest,
+                                  *_rows(dq, "dq", (B, T, Hq, d), a.dtype, a.dev),
+                                  *_rows(dk, "dk", (B, T, Hk, d), a.dtype, a.dev),
+                                  _ptr(dwq), _ptr(dwk), _ptr(workspace), ws_bytes, s)
+    _check(st, "la_qk_rotate_bwd")
+    return dq, dk, dwq, dwk
+
+
+def head_gate_fwd(o, gate=None, *, weight=None, eps=1e-6, center=False, out=None, stream=None):
+    """Norm of each head's output o [B,H,T,d], times weight (fp32 [H,d]), times
+    gate * sigmoid(gate) (gate [B,T,H,d]); returns [B,T,H,d], the layer's row.
+    center: the mean is taken out first.  o, gate and out may have strides (rows
+    dense, the others multiples of 16 bytes): scan_fwd's [B,T,H*d] goes in as
+    h.view(B, T, H, d).permute(0, 2, 1, 3)."""
+    if o.dim() != 4:
+        raise ValueError(f"o is {tuple(o.shape)}; [B,H,T,d] is needed")
+    B, H, T, d = o.shape
+    dev, dt, code = o.device, o.dtype, _dtype_code(o)
+    with _launch_on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((B, T, H, d), dtype=dt, device=dev)
+        st = _load().la_head_gate_fwd(*_rows(o, "o", (B, H, T, d), dt, dev),
+                                      *_rows(gate, "gate", (B, T, H, d), dt, dev), code,
+                                      _dense(weight, "weight", (H, d), torch.float32, dev), B, H, T,
+                                      d, LA_GATE_CENTER if center else 0, float(eps),
+                                      *_rows(out, "out", (B, T, H, d), dt, dev), s)
+    _check(st, "la_head_gate_fwd")
+    return out
+
+
+def head_gate_bwd(o, gate, dy, *, weight=None, eps=1e-6, center=False, d_o=None, dgate=None,
+                  weight_grads=True, workspace=None, stream=None):
+    """Gradients of head_gate_fwd for dy [B,T,H,d]: (d_o [B,H,T,d], dgate [B,T,H,d],
+    dweight [H,d]); dgate is None without a gate, dweight without a weight or with
+    weight_grads False.  d_o takes o's order of dimensions where o is dense (what
+    chunk_bwd reads as dO, or scan_bwd as dh), and the buffer given otherwise."""
+    if o.dim() != 4:
+        raise ValueError(f"o is {tuple(o.shape)}; [B,H,T,d] is needed")
+    B, H, T, d = o.shape
+    dev, dt, code = o.device, o.dtype, _dtype_code(o)
+    lib = _load()
+    if gate is None and dgate is not None:
+        raise ValueError("dgate is given without a gate")
+    with _launch_on(dev, stream) as s:
+        if d_o is None:
+            d_o = torch.empty_like(o)
+        if gate is not None and dgate is None:
+            dgate = torch.empty((B, T, H, d), dtype=dt, device=dev)
+        dw = (torch.empty((H, d), dtype=torch.float32, device=dev)
+              if weight_grads and weight is not None else None)
+        need = 0
+        if dw is not None:
+            need = int(lib.la_head_gate_bwd_workspace_size(B, H, T, d, code))
+            if need and workspace is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = _workspace(workspace, need, dev)
+        st = lib.la_head_gate_bwd(*_rows(o, "o", (B, H, T, d), dt, dev),
+                                  *_rows(gate, "gate", (B, T, H, d), dt, dev),
+                                  *_rows(dy, "dy", (B, T, H, d), dt, dev), code,
+                                  _dense(weight, "weight", (H, d), torch.float32, dev), B, H, T, d,
+                                  LA_GATE_CENTER if center else 0, float(eps),
+                                  *_rows(d_o, "d_o", (B, H, T, d), dt, dev),
+                                  *_rows(dgate, "dgate", (B, T, H, d), dt, dev), _ptr(dw),
+                                  _ptr(workspace), ws_bytes, s)
+    _check(st, "la_head_gate_bwd")
+    return d_o, dgate, dw
+
+
+def scan_fwd(x, log_a, *, h0=None, out=None, h_out=None, return_state=True, stream=None):
+    """The recurrence h_t = exp(log_a_t) h_(t-1) + x_t for every channel of x [B,T,D]
+    (fp32 or bf16), log_a [B,T,D] fp32 (<= 0; -inf restarts its channel), from h0
+    [B,D] fp32 (None: zero).  Returns (h [B,T,D], h_T [B,D] fp32); h_T is None when
+    return_state is False and no h_out was given.  h_out may be h0."""
+    if x.dim() != 3:
+        raise ValueError(f"x is {tuple(x.shape)}; [B,T,D] is needed")
+    B, T, D = x.shape
+    dev, dt, code = x.device, x.dtype, _dtype_code(x)
+    f32 = torch.float32
+    with _launch_on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((B, T, D), dtype=dt, device=dev)
+        if return_state and h_out is None:
+            h_out = torch.empty((B, D), dtype=f32, device=dev)
+        st = _load().la_scan_fwd(_dense(x, "x", (B, T, D), dt, dev), code,
+                                 _dense(log_a, "log_a", (B, T, D), f32, dev), B, T, D,
+                                 _dense(h0, "h0", (B, D), f32, dev),
+                                 _dense(out, "out", (B, T, D), dt, dev),
+                                 _dense(h_out, "h_out", (B, D), f32, dev), s)
+    _check(st, "la_scan_fwd")
+    return out, h_out
+
+
+def scan_bwd(log_a, h, dh, *, h0=None, dh_T=None, dx=None, dlog_a=None, state_grads=True, stream=None):
+    """Gradients of scan_fwd for the loss sum(dh * h) + <dh_T, h_T>, from its output h:
+    (dx [B,T,D], dlog_a [B,T,D] fp32, dh0 [B,D] fp32); dh0 is None when state_grads
+    is False."""
+    if h.dim() != 3:
+        raise ValueError(f"h is {tuple(h.shape)}; [B,T,D] is needed")
+    B, T, D = h.shape
+    dev, dt, code = h.device, h.dtype, _dtype_code(h)
+    f32 = torch.float32
+    with _launch_on(dev, stream) as s:
+        if dx is None:
+            dx = torch.empty((B, T, D), dtype=dt, device=dev)
+        if dlog_a is None:
+            dlog_a = torch.empty((B, T, D), dtype=f32, device=dev)
+        dh0 = torch.empty((B, D), dtype=f32, device=dev) if state_grads else None
+        st = _load().la_scan_bwd(_dense(log_a, "log_a", (B, T, D), f32, dev),
+                                 _dense(h, "h", (B, T, D), dt, dev),
+                                 _dense(dh, "dh", (B, T, D), dt, dev), code, B, T, D,
+                                 _dense(h0, "h0", (B, D), f32, dev),
+                                 _dense(dh_T, "dh_T", (B, D), f32, dev),
+                                 _dense(dx, "dx", (B, T, D), dt, dev),
+                                 _dense(dlog_a, "dlog_a", (B, T, D), f32, dev), _ptr(dh0), s)
+    _check(st, "la_scan_bwd")
+    return dx, dlog_a, dh0
+
+
+def scan_step(x, log_a, h, *, out=None, h_out=None, stream=None):
+    """One token of scan_fwd: the state h [B,D] fp32 becomes exp(log_a) h + x, in place
+    or in h_out; returns its rounding to x's dtype, [B,D]."""
+    if x.dim() != 2:
+        raise ValueError(f"x is {tuple(x.shape)}; [B,D] is needed")
+    B, D = x.shape
+    dev, dt, code = x.device, x.dtype, _dtype_code(x)
+    f32 = torch.float32
+    with _launch_on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((B, D), dtype=dt, device=dev)
+        st = _load().la_scan_step(_dense(x, "x", (B, D), dt, dev), code,
+                                  _dense(log_a, "log_a", (B, D), f32, dev), B, D,
+                                  _dense(h, "h", (B, D), f32, dev),
+                                  _dense(h if h_out is None else h_out, "h_out", (B, D), f32, dev),
+                                  _dense(out, "out", (B, D), dt, dev), s)
+    _check(st, "la_scan_step")
+    return out
+
+
+__all__ = ["qk_rotate_fwd", "qk_rotate_bwd", "rotary_frequencies", "head_gate_fwd", "head_gate_bwd",
+           "scan_fwd", "scan_bwd", "scan_step", "LA_QK_NORM", "LA_QK_ADJACENT", "LA_GATE_CENTER",
+           "chunk_fwd", "chunk_bwd", "chunk_fwd_noalloc", "recurrent_step", "state_init", "workspace_size", "chunk_fwd_host",
            "host_arena_size",
            "trace_enable", "trace_collect", "debug_set", "debug_options",
            "library", "status_string", "abi_version", "LinAttnError", "LA_PHI_ELU1",

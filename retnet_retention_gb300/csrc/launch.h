@@ -100,6 +100,57 @@ struct BwdArgs {
     bool dq_only = false;
 };
 
+// Queries and keys normed, rotated and laid out for retention, or the gradients of
+// that; validated by the ABI layer.  Strides are in elements: batch, token, head.
+struct QkRotateArgs {
+    const void *q, *k;
+    const void *dq_out, *dk_out;        // backward: [B][H][T][d]
+    long long q_strides[3], k_strides[3];
+    void *yq, *yk;                      // forward: [B][H][T][d]; backward: dq, dk
+    long long yq_strides[3], yk_strides[3];  // backward
+    int B, T, Hq, Hk, d, rot;
+    const double* inv_freq;             // host [rot / 2]
+    const int* positions;               // device [B][T] or null: pos0 + t
+    int pos0;
+    const float *q_weight, *k_weight;   // [d] or null
+    float *dq_weight, *dk_weight;       // backward: [d] or null
+    float eps, q_scale, k_scale;
+    bool bf16, norm, halves;
+    void* workspace;
+};
+
+// The norm and gate of each head's output, or its gradients; validated by the ABI
+// layer.  Strides in elements: batch, head, token for o and do, batch, token, head
+// for the rest.
+struct HeadGateArgs {
+    const void *o, *gate, *dy;          // gate may be null
+    long long o_strides[3], gate_strides[3], dy_strides[3];
+    const float* weight;                // [H][d] or null
+    int B, H, T, d;
+    bool bf16, center;
+    float eps;
+    void *y, *d_o, *d_gate;
+    long long y_strides[3], do_strides[3], dgate_strides[3];
+    float* d_weight;                    // [H][d] or null
+    void* workspace;
+};
+
+// The per-channel recurrence h_t = a_t h_(t-1) + x_t over [B][T][D], or its
+// gradients; validated by the ABI layer.
+struct RecurrenceArgs {
+    const void* x;                      // forward
+    const float* log_a;
+    const float* h0;                    // [B][D] or null
+    void* h;                            // forward: output; backward: input
+    float* h_out;                       // forward: [B][D] or null
+    const void* dh;                     // backward
+    const float* dh_T;                  // [B][D] or null
+    void* dx;
+    float *dlog_a, *dh0;                // dh0 may be null
+    int B, T, D;
+    bool bf16;
+};
+
 // The test and diagnostic switches of la_debug_set (abi.cu).
 int opt_path();           // 0 automatic, 1 CUDA cores, 2 tensor cores
 bool opt_tc_lockstep();   // the lockstep kernel instead of the pipelined one
@@ -151,5 +202,21 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, const KernelGammas& g, cudaStrea
 bool taylor_supported(const ChunkArgs& a);
 int taylor_feature_dim(int d);
 cudaError_t launch_chunk_taylor(const ChunkArgs& a, const KernelGammas& g, cudaStream_t s);
+
+// qk_rotate.cu: norm, rotation and layout of queries and keys, and its gradients
+size_t qk_rotate_bwd_workspace_bytes(const QkRotateArgs& a);
+cudaError_t launch_qk_rotate_fwd(const QkRotateArgs& a, cudaStream_t s);
+cudaError_t launch_qk_rotate_bwd(const QkRotateArgs& a, cudaStream_t s);
+
+// head_gate.cu: norm and gate of the heads' outputs, and its gradients
+size_t head_gate_bwd_workspace_bytes(const HeadGateArgs& a);
+cudaError_t launch_head_gate_fwd(const HeadGateArgs& a, cudaStream_t s);
+cudaError_t launch_head_gate_bwd(const HeadGateArgs& a, cudaStream_t s);
+
+// scan.cu: the per-channel recurrence, its gradients and its single step (T = 1 of x,
+// log_a, h0 -> h, h_out)
+cudaError_t launch_scan_fwd(const RecurrenceArgs& a, cudaStream_t s);
+cudaError_t launch_scan_bwd(const RecurrenceArgs& a, cudaStream_t s);
+cudaError_t launch_scan_step(const RecurrenceArgs& a, cudaStream_t s);
 
 }  // namespace la
