@@ -453,13 +453,15 @@ LA_API size_t la_head_gate_bwd_workspace_size(int B, int H, int T, int d, la_dty
  *           (in-place continuation), else may not overlap it
  *   h       [B][T][D] dtype, output; may overlap no input
  *   h_out   [B][D] fp32 final state h_T, or NULL
+ *   dev_status  device int or NULL (see the conventions above)
  *
  * The state is fp32 throughout; h is rounded where it is stored.  T == 0: h_out is
  * the initial state.  B == 0 is a no-op.  B * D at most 2^33.  No workspace.
  * Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
  */
 LA_API la_status la_scan_fwd(const void* x, la_dtype dtype, const float* log_a, int B, int T, int D,
-                             const float* h0, void* h, float* h_out, la_stream_t stream);
+                             const float* h0, void* h, float* h_out, int* dev_status,
+                             la_stream_t stream);
 
 /*
  * Gradients of la_scan_fwd for the loss sum_t dh_t . h_t + <dh_T, h_T>:
@@ -477,7 +479,7 @@ LA_API la_status la_scan_fwd(const void* x, la_dtype dtype, const float* log_a, 
  */
 LA_API la_status la_scan_bwd(const float* log_a, const void* h, const void* dh, la_dtype dtype,
                              int B, int T, int D, const float* h0, const float* dh_T, void* dx,
-                             float* dlog_a, float* dh0, la_stream_t stream);
+                             float* dlog_a, float* dh0, int* dev_status, la_stream_t stream);
 
 /*
  * One token of la_scan_fwd: h_out = exp(log_a) h_in + x, h its rounding to dtype.
@@ -580,6 +582,9 @@ LA_API la_status la_chunk_fwd_host(const void* Q, const void* K, const void* V, 
  *                         LA_ERR_TIMEOUT in dev_status and return without
  *                         computing (the device status path, exercised with
  *                         neither a hang nor a fault).
+ *                         la_scan_fwd and la_scan_bwd on long sequences: the CTAs
+ *                         of a cluster send each other nothing, each waits 1 ms,
+ *                         and the status is recorded.
  *
  * Returns the option's previous value, or -1 (nothing changed) for an unknown
  * option or an out-of-range value.  Set a switch before enqueuing the calls it

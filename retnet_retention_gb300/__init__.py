@@ -125,9 +125,9 @@ def _load() -> ctypes.CDLL:
     lib.la_head_gate_bwd.restype = i
     lib.la_head_gate_bwd_workspace_size.argtypes = [i, i, i, i, i]
     lib.la_head_gate_bwd_workspace_size.restype = sz
-    lib.la_scan_fwd.argtypes = [vp, i, vp, i, i, i, vp, vp, vp, vp]
+    lib.la_scan_fwd.argtypes = [vp, i, vp, i, i, i, vp, vp, vp, vp, vp]
     lib.la_scan_fwd.restype = i
-    lib.la_scan_bwd.argtypes = [vp, vp, vp, i, i, i, i, vp, vp, vp, vp, vp, vp]
+    lib.la_scan_bwd.argtypes = [vp, vp, vp, i, i, i, i, vp, vp, vp, vp, vp, vp, vp]
     lib.la_scan_bwd.restype = i
     lib.la_scan_step.argtypes = [vp, i, vp, i, i, vp, vp, vp, vp]
     lib.la_scan_step.restype = i
@@ -796,7 +796,8 @@ def head_gate_bwd(o, gate, dy, *, weight=None, eps=1e-6, center=False, d_o=None,
     return d_o, dgate, dw
 
 
-def scan_fwd(x, log_a, *, h0=None, out=None, h_out=None, return_state=True, stream=None):
+def scan_fwd(x, log_a, *, h0=None, out=None, h_out=None, return_state=True, dev_status=None,
+             stream=None):
     """The recurrence h_t = exp(log_a_t) h_(t-1) + x_t for every channel of x [B,T,D]
     (fp32 or bf16), log_a [B,T,D] fp32 (<= 0; -inf restarts its channel), from h0
     [B,D] fp32 (None: zero).  Returns (h [B,T,D], h_T [B,D] fp32); h_T is None when
@@ -806,6 +807,7 @@ def scan_fwd(x, log_a, *, h0=None, out=None, h_out=None, return_state=True, stre
     B, T, D = x.shape
     dev, dt, code = x.device, x.dtype, _dtype_code(x)
     f32 = torch.float32
+    _buffer(dev_status, "dev_status", 1, torch.int32, dev)
     with _launch_on(dev, stream) as s:
         if out is None:
             out = torch.empty((B, T, D), dtype=dt, device=dev)
@@ -815,12 +817,13 @@ def scan_fwd(x, log_a, *, h0=None, out=None, h_out=None, return_state=True, stre
                                  _dense(log_a, "log_a", (B, T, D), f32, dev), B, T, D,
                                  _dense(h0, "h0", (B, D), f32, dev),
                                  _dense(out, "out", (B, T, D), dt, dev),
-                                 _dense(h_out, "h_out", (B, D), f32, dev), s)
+                                 _dense(h_out, "h_out", (B, D), f32, dev), _ptr(dev_status), s)
     _check(st, "la_scan_fwd")
     return out, h_out
 
 
-def scan_bwd(log_a, h, dh, *, h0=None, dh_T=None, dx=None, dlog_a=None, state_grads=True, stream=None):
+def scan_bwd(log_a, h, dh, *, h0=None, dh_T=None, dx=None, dlog_a=None, state_grads=True,
+             dev_status=None, stream=None):
     """Gradients of scan_fwd for the loss sum(dh * h) + <dh_T, h_T>, from its output h:
     (dx [B,T,D], dlog_a [B,T,D] fp32, dh0 [B,D] fp32); dh0 is None when state_grads
     is False."""
@@ -829,6 +832,7 @@ def scan_bwd(log_a, h, dh, *, h0=None, dh_T=None, dx=None, dlog_a=None, state_gr
     B, T, D = h.shape
     dev, dt, code = h.device, h.dtype, _dtype_code(h)
     f32 = torch.float32
+    _buffer(dev_status, "dev_status", 1, torch.int32, dev)
     with _launch_on(dev, stream) as s:
         if dx is None:
             dx = torch.empty((B, T, D), dtype=dt, device=dev)
@@ -841,7 +845,8 @@ def scan_bwd(log_a, h, dh, *, h0=None, dh_T=None, dx=None, dlog_a=None, state_gr
                                  _dense(h0, "h0", (B, D), f32, dev),
                                  _dense(dh_T, "dh_T", (B, D), f32, dev),
                                  _dense(dx, "dx", (B, T, D), dt, dev),
-                                 _dense(dlog_a, "dlog_a", (B, T, D), f32, dev), _ptr(dh0), s)
+                                 _dense(dlog_a, "dlog_a", (B, T, D), f32, dev), _ptr(dh0),
+                                 _ptr(dev_status), s)
     _check(st, "la_scan_bwd")
     return dx, dlog_a, dh0
 

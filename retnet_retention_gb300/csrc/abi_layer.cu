@@ -385,7 +385,8 @@ la_status la_head_gate_bwd(const void* o, const long long* o_strides, const void
 }
 
 la_status la_scan_fwd(const void* x, la_dtype dtype, const float* log_a, int B, int T, int D,
-                      const float* h0, void* h, float* h_out, la_stream_t stream) {
+                      const float* h0, void* h, float* h_out, int* dev_status,
+                      la_stream_t stream) {
     if (!scan_shape_ok(B, T, D, dtype)) return LA_ERR_INVALID_ARG;
     if (any_misaligned({x, log_a, h0, h, h_out})) return LA_ERR_INVALID_ARG;
     if (B == 0) return LA_OK;
@@ -404,6 +405,7 @@ la_status la_scan_fwd(const void* x, la_dtype dtype, const float* log_a, int B, 
     RecurrenceArgs a;
     std::memset(&a, 0, sizeof(a));
     a.x = x; a.log_a = log_a; a.h0 = h0; a.h = h; a.h_out = h_out;
+    a.dev_status = dev_status;
     a.B = B; a.T = T; a.D = D;
     a.bf16 = dtype == LA_DTYPE_BF16;
     return cuda_status(launch_scan_fwd(a, s));
@@ -411,7 +413,7 @@ la_status la_scan_fwd(const void* x, la_dtype dtype, const float* log_a, int B, 
 
 la_status la_scan_bwd(const float* log_a, const void* h, const void* dh, la_dtype dtype, int B, int T,
                       int D, const float* h0, const float* dh_T, void* dx, float* dlog_a, float* dh0,
-                      la_stream_t stream) {
+                      int* dev_status, la_stream_t stream) {
     if (!scan_shape_ok(B, T, D, dtype)) return LA_ERR_INVALID_ARG;
     if (any_misaligned({log_a, h, dh, h0, dh_T, dx, dlog_a, dh0})) return LA_ERR_INVALID_ARG;
     if (B == 0) return LA_OK;
@@ -433,6 +435,7 @@ la_status la_scan_bwd(const float* log_a, const void* h, const void* dh, la_dtyp
     std::memset(&a, 0, sizeof(a));
     a.log_a = log_a; a.h = const_cast<void*>(h); a.dh = dh; a.h0 = h0; a.dh_T = dh_T;
     a.dx = dx; a.dlog_a = dlog_a; a.dh0 = dh0;
+    a.dev_status = dev_status;
     a.B = B; a.T = T; a.D = D;
     a.bf16 = dtype == LA_DTYPE_BF16;
     return cuda_status(launch_scan_bwd(a, s));

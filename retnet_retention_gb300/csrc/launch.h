@@ -149,6 +149,7 @@ struct RecurrenceArgs {
     float *dlog_a, *dh0;                // dh0 may be null
     int B, T, D;
     bool bf16;
+    int* dev_status;                    // or null
 };
 
 // The test and diagnostic switches of la_debug_set (abi.cu).

@@ -10,10 +10,9 @@
 // over the warps of a CTA and the CTAs of a cluster: every thread composes the rows
 // it holds in registers, the runs' (A, b) are composed across warps (shared memory)
 // and across the cluster's CTAs (each pushes its own into the others' shared
-// memory, one cluster barrier a round), and every thread then replays its rows from
-// the state that enters them.  x and log_a are read once and h written once; no
-// workspace, no atomics, no waits on memory, and the order of all sums is fixed by
-// the launch shape.
+// memory), and every thread then replays its rows from the state that enters them.
+// x and log_a are read once and h written once; no workspace, no atomics, no waits on
+// global memory, and the order of all sums is fixed by the launch shape.
 //
 // A decay of exactly zero (log_a = -inf) restarts its channel: the old state is
 // dropped by a selection, not multiplied by zero, so that an infinity or a NaN in
@@ -22,16 +21,18 @@
 // Bound by HBM: log_a 4, x 2, h 2 bytes an entry (bf16).  State, products and sums
 // are fp32; h is rounded where it is stored, never the state that is carried on.
 #include <algorithm>
+#include <type_traits>
 
 #include "rows.cuh"
+#include "tc_ptx.cuh"
 #include "trace.h"
 
 namespace la {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+using namespace tc;
+
 constexpr int kMaxCluster = 8;
 
 struct ScanParams {
@@ -44,6 +45,9 @@ struct ScanParams {
     float* dlog_a;       // backward
     float* s_out;        // the state after the walk (h_T, or dh0), or null
     int T, D, tiles;     // tiles: channel tiles of a sequence
+    int* dev_status;     // or null
+    uint64_t limit_ns;   // of a wait for the cluster's runs
+    bool mute;           // test switch: push nothing, so that the waits run out
 };
 
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -65,14 +69,46 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }
-// Write v to the same shared address in CTA `rank` of the cluster.
-__device__ __forceinline__ void push(const float2* at, unsigned rank, float2 v) {
-    const uint32_t a = (uint32_t)__cvta_generic_to_shared(at);
+// Write v to the same shared address in CTA `rank` of the cluster and count its bytes
+// on that CTA's barrier: unlike a cluster barrier this waits for nothing else, in
+// particular not for the round's stores of h.
+__device__ __forceinline__ void push(const float2* at, const uint64_t* bar, unsigned rank, float2 v) {
     asm volatile(
-        "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, %1;\n\t"
-        "st.shared::cluster.v2.f32 [r], {%2, %3};\n\t}" ::"r"(a),
-        "r"(rank), "f"(v.x), "f"(v.y)
+        "{\n\t.reg .b32 ra, rb;\n\tmapa.shared::cluster.u32 ra, %0, %2;\n\t"
+        "mapa.shared::cluster.u32 rb, %1, %2;\n\t"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [ra], {%3, %4}, [rb];\n\t}" ::"r"(
+            smem_addr(at)),
+        "r"(smem_addr(bar)), "r"(rank), "f"(v.x), "f"(v.y)
         : "memory");
+}
+__device__ __forceinline__ bool arrived(const uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+// Wait for the cluster's runs of a round.  The CTAs of a cluster run at the same time,
+// so this ends within microseconds; after the limit it gives up, and so do the
+// CTA's other warps and later rounds, which then run on without the runs.
+__device__ __noinline__ void wait_long(const uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                       volatile int* gave_up) {
+    const uint64_t t0 = global_timer_ns();
+    while (!arrived(bar, parity)) {
+        if (*gave_up) return;
+        if (global_timer_ns() - t0 > limit_ns) {
+            *gave_up = 1;
+            return;
+        }
+    }
+}
+__device__ __forceinline__ void wait_runs(const uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                          volatile int* gave_up) {
+    if (!arrived(bar, parity)) wait_long(bar, parity, limit_ns, gave_up);
 }
 
 // The state s after a run (A, b).
@@ -80,39 +116,44 @@ __device__ __forceinline__ float after(float A, float b, float s) {
     return A == 0.f ? b : fmaf(A, s, b);
 }
 
-template <int V>
-struct Pack;
-template <>
-struct Pack<1> {
-    using F = float;
-    using H = uint16_t;
-};
-template <>
-struct Pack<2> {
-    using F = float2;
-    using H = uint32_t;
-};
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void copy16(void* to, const void* from, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     smem_addr(to)),
+                 "l"(from), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
+// V neighbouring entries of a row in shared memory, as fp32.
 template <int V>
-__device__ __forceinline__ void load_row(const float* p, float (&v)[V]) {
-    const typename Pack<V>::F r = __ldg(reinterpret_cast<const typename Pack<V>::F*>(p));
-    const float* f = reinterpret_cast<const float*>(&r);
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = f[j];
+__device__ __forceinline__ void row_floats(const float* p, float (&v)[V]) {
+    if (V == 2) {
+        const float2 r = *reinterpret_cast<const float2*>(p);
+        v[0] = r.x;
+        v[V - 1] = r.y;
+    } else {
+        v[0] = *p;
+    }
 }
 template <int V>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&v)[V]) {
-    const typename Pack<V>::H r = __ldg(reinterpret_cast<const typename Pack<V>::H*>(p));
-    v[0] = __uint_as_float((uint32_t)r << 16);
-    if (V == 2) v[V - 1] = __uint_as_float((uint32_t)r & 0xffff0000u);
+__device__ __forceinline__ void row_floats(const __nv_bfloat16* p, float (&v)[V]) {
+    if (V == 2) {
+        const uint32_t r = *reinterpret_cast<const uint32_t*>(p);
+        v[0] = __uint_as_float(r << 16);
+        v[V - 1] = __uint_as_float(r & 0xffff0000u);
+    } else {
+        v[0] = __bfloat162float(*p);
+    }
 }
 template <int V>
 __device__ __forceinline__ void store_row(float* p, const float (&v)[V]) {
-    typename Pack<V>::F r;
-    float* f = reinterpret_cast<float*>(&r);
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = v[j];
-    *reinterpret_cast<typename Pack<V>::F*>(p) = r;
+    if (V == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[V - 1]);
+    else *p = v[0];
 }
 template <int V>
 __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&v)[V]) {
@@ -120,53 +161,135 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&v)[V])
     else *p = __float2bfloat16_rn(v[0]);
 }
 
-// One cluster walks one tile of 32 V channels of one sequence, R rows a thread and
-// round; backward, it walks from the last token to the first.
-template <typename T, int V, int R, bool BWD>
-__global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant__ ScanParams p) {
-    constexpr int C = 32 * V, kRun = kWarps * R;
-    __shared__ float2 warp_run[2][kWarps][C];
-    __shared__ float2 cta_run[2][kMaxCluster][C];
+// One kernel's shape: V channels a lane (a tile has C = 32 V), R rows a thread and
+// round, W warps, S rounds of rows in the ring.
+template <typename T, int V_, int R_, int W_, int S_, bool BWD_>
+struct Shape {
+    using Elem = T;
+    static constexpr int V = V_, R = R_, W = W_, S = S_, C = 32 * V_;
+    static constexpr bool BWD = BWD_;
+    static constexpr int kRun = W * R;  // rows a CTA takes a round
+    static constexpr size_t kLog = (size_t)kRun * C * sizeof(float);
+    static constexpr size_t kX = (size_t)kRun * C * sizeof(T);
+    static constexpr size_t kStage = kLog + kX * (BWD ? 2 : 1);
+    static constexpr size_t kRuns = 2 * (size_t)(W + kMaxCluster) * C * sizeof(float2);
+    static constexpr size_t kShared = S * kStage + kRuns;
+};
+
+// One cluster walks one tile of channels of one sequence; backward, it walks from the
+// last token to the first.  A warp copies the rows it works on itself, a ring of S
+// rounds ahead, so that the ring needs no barrier beyond the warp's own.
+template <typename K>
+__global__ void __launch_bounds__(K::W * 32, K::W > 8 ? 1 : 2) scan_kernel(const __grid_constant__ ScanParams p) {
+    using T = typename K::Elem;
+    constexpr int V = K::V, R = K::R, W = K::W, S = K::S, C = K::C;
+    constexpr bool BWD = K::BWD;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ __align__(8) uint64_t bars[2];  // the cluster's runs of even and odd rounds
+    __shared__ int gave_up;
+    float2* warp_run = reinterpret_cast<float2*>(smem + S * K::kStage);  // [2][W][C]
+    float2* cta_run = warp_run + 2 * W * C;                              // [2][kMaxCluster][C]
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const unsigned rank = cluster_rank(), n = cluster_size(), unit = cluster_id();
     const unsigned b = unit / (unsigned)p.tiles, tile = unit - b * (unsigned)p.tiles;
-    const int c0 = (int)tile * C + lane * V;
+    const int first = (int)tile * C, c0 = first + lane * V;
     const bool on = c0 < p.D;
-    const size_t seq = (size_t)b * p.T * p.D + c0;
-    const T* x = (const T*)p.x + seq;
-    const T* h_in = (const T*)p.h_in + seq;
-    const float* log_a = p.log_a + seq;
-    T* y = (T*)p.y + seq;
+    // Rows are counted in walking order: row u is token u, or T - 1 - u backward.
+    const long long step = BWD ? -(long long)p.D : (long long)p.D, seq = (long long)b * p.T * p.D;
+    const long long origin = seq + (BWD ? (p.T - 1ll) * p.D : 0);  // row 0
+    const long long mine = (long long)rank * K::kRun + w * R, leap = (long long)n * K::kRun;
 
+    // A warp copies 16-byte pieces: of log_a (kLogRows rows at a time), of x (dh), and
+    // backward of h one token earlier.  A lane's piece keeps its column.
+    constexpr int kLogRows = 32 / (C / 4), kElems = 16 / (int)sizeof(T), kRows = 32 / (C / kElems);
+    static_assert(R % kLogRows == 0 && R % kRows == 0, "whole passes");
+    const int log_row = lane / (C / 4), log_c = first + lane % (C / 4) * 4;
+    const int x_row = lane / (C / kElems), x_c = first + lane % (C / kElems) * kElems;
+    const bool log_on = log_c < p.D, x_on = x_c < p.D;
+    const float* log_src = p.log_a + origin + (mine + log_row) * step + (log_on ? log_c : 0);
+    const T* x_src = (const T*)p.x + origin + (mine + x_row) * step + (x_on ? x_c : 0);
+    const T* h_src = (const T*)p.h_in + origin + (mine + x_row + 1) * step + (x_on ? x_c : 0);
+    long long u_src = mine;  // the warp's first row of the next round to copy
+    unsigned char* const slot = smem + (size_t)w * R * C * sizeof(float) + lane * 16;
+    unsigned char* const x_slot = smem + K::kLog + (size_t)w * R * C * sizeof(T) + lane * 16;
+    // Copy the next round's rows into stage s.  Rows past the end arrive as zeros:
+    // log_a 0, x 0 leave the state as it is.
+    auto fetch = [&](int s) {
+        unsigned char* const to = slot + s * K::kStage;
+        unsigned char* const x_to = x_slot + s * K::kStage;
+        auto pieces = [&](auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;  // all rows inside, the last token not among them
+#pragma unroll
+            for (int i = 0; i < R / kLogRows; ++i) {
+                const bool valid = log_on && (kWhole || u_src + i * kLogRows + log_row < p.T);
+                copy16(to + i * 512, kWhole || valid ? log_src + i * kLogRows * step : p.log_a, valid);
+            }
+#pragma unroll
+            for (int i = 0; i < R / kRows; ++i) {
+                const long long u = u_src + i * kRows + x_row;
+                const bool valid = x_on && (kWhole || u < p.T), before = x_on && (kWhole || u + 1 < p.T);
+                copy16(x_to + i * 512, kWhole || valid ? x_src + i * kRows * step : (const T*)p.x, valid);
+                if (BWD)
+                    copy16(x_to + K::kX + i * 512,
+                           kWhole || before ? h_src + i * kRows * step : (const T*)p.h_in, before);
+            }
+        };
+        if (u_src + R < p.T) pieces(std::true_type());
+        else pieces(std::false_type());
+        u_src += leap;
+        log_src += leap * step;
+        x_src += leap * step;
+        h_src += leap * step;
+    };
+
+    const uint32_t runs_bytes = n * C * sizeof(float2);
+    if (n > 1 && threadIdx.x == 0) {
+        gave_up = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[i], 1);
+            mbar_arrive_expect_tx(&bars[i], runs_bytes);
+        }
+        fence_mbar_init();
+    }
+    const int rounds = (int)(((long long)p.T + (long long)K::kRun * n - 1) / ((long long)K::kRun * n));
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        if (s < rounds) fetch(s);
+        copies_commit();
+    }
     float state[V];
 #pragma unroll
     for (int j = 0; j < V; ++j)
         state[j] = on && p.s0 ? p.s0[(size_t)b * p.D + c0 + j] : 0.f;
-    if (n > 1) cluster_barrier();  // every CTA of the cluster runs before any is written to
+    if (n > 1) cluster_barrier();  // every CTA of the cluster runs, its barriers set up, before any is written to
 
-    const int rounds = (int)(((long long)p.T + (long long)kRun * n - 1) / ((long long)kRun * n));
-    for (int round = 0; round < rounds; ++round) {
-        const int par = round & 1;
-        const long long u0 = ((long long)round * n + rank) * kRun + w * R;  // first row, in walking order
+    const float* const log_run = reinterpret_cast<const float*>(smem) + w * R * C + lane * V;
+    const T* const x_run = reinterpret_cast<const T*>(smem + K::kLog) + w * R * C + lane * V;
+    T* y = (T*)p.y + origin + mine * step + (on ? c0 : 0);
+    float* dlog_a = BWD ? p.dlog_a + origin + mine * step + (on ? c0 : 0) : nullptr;
+    long long u0 = mine;
+    for (int round = 0, stage = 0; round < rounds; ++round, stage = stage + 1 == S ? 0 : stage + 1) {
+        const int par = round & 1;  // the round's half of the exchange buffers
         float a[R][V], v[R][V], hp[BWD ? R : 1][V];
+        copies_wait<S - 1>();
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const long long u = u0 + i;
+            row_floats<V>(log_run + stage * (K::kStage / sizeof(float)) + i * C, a[i]);
+            row_floats<V>(x_run + stage * (K::kStage / sizeof(T)) + i * C, v[i]);
+            if (BWD)
+                row_floats<V>(x_run + stage * (K::kStage / sizeof(T)) + K::kX / sizeof(T) + i * C,
+                              hp[BWD ? i : 0]);
+        }
+        __syncwarp();
+        if (round + S < rounds) fetch(stage);
+        copies_commit();
+        if (BWD && p.h0 && u0 < p.T && u0 + R >= p.T && on) {  // token 0 follows h0
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                a[i][j] = 0.f;
-                v[i][j] = 0.f;
-                if (BWD) hp[BWD ? i : 0][j] = 0.f;
-            }
-            if (on && u < p.T) {
-                const size_t t = BWD ? (size_t)(p.T - 1 - u) : (size_t)u;
-                load_row<V>(log_a + t * p.D, a[i]);
-                load_row<V>(x + t * p.D, v[i]);
-                if (BWD) {
-                    if (t > 0) load_row<V>(h_in + (t - 1) * p.D, hp[BWD ? i : 0]);
-                    else if (p.h0) load_row<V>(p.h0 + (size_t)b * p.D + c0, hp[BWD ? i : 0]);
-                }
-            }
+            for (int i = 0; i < R; ++i)
+                if (u0 + i == p.T - 1)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) hp[BWD ? i : 0][j] = p.h0[(size_t)b * p.D + c0 + j];
         }
         float A[V], bb[V];
 #pragma unroll
@@ -175,45 +298,72 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                a[i][j] = expf(a[i][j]);  // rows past the end: log_a 0, x 0 keep the state
-                if (BWD) bb[j] = a[i][j] == 0.f ? 0.f : a[i][j] * (v[i][j] + bb[j]);
-                else bb[j] = after(a[i][j], v[i][j], bb[j]);
+                a[i][j] = expf(a[i][j]);
+                bb[j] = BWD ? a[i][j] * (v[i][j] + bb[j]) : fmaf(a[i][j], bb[j], v[i][j]);
                 A[j] *= a[i][j];
             }
+        // a zero among the decays makes the product zero: only then (or after an
+        // underflow) do the restarts' selections run, for the whole warp
+        bool zero = false;
 #pragma unroll
-        for (int j = 0; j < V; ++j) warp_run[par][w][lane * V + j] = make_float2(A[j], bb[j]);
+        for (int j = 0; j < V; ++j) zero |= A[j] == 0.f;
+        const bool cut = __any_sync(0xffffffffu, zero);
+        if (cut) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) bb[j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    bb[j] = BWD ? (a[i][j] == 0.f ? 0.f : a[i][j] * (v[i][j] + bb[j]))
+                                : after(a[i][j], v[i][j], bb[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            warp_run[(par * W + w) * C + lane * V + j] = make_float2(A[j], bb[j]);
         __syncthreads();
         // the run before this warp's in the CTA, and the whole CTA's
         float pA[V], pb[V], tA[V], tb[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) tA[j] = 1.f, tb[j] = 0.f, pA[j] = 1.f, pb[j] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i)
+        for (int i = 0; i < W; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float2 r = warp_run[par][i][lane * V + j];
+                const float2 r = warp_run[(par * W + i) * C + lane * V + j];
                 if (i == w) pA[j] = tA[j], pb[j] = tb[j];
                 tb[j] = after(r.x, r.y, tb[j]);
                 tA[j] *= r.x;
             }
         float s[V];
         if (n > 1) {
-            for (unsigned to = w; to < n; to += kWarps)
+            // A slot and its barrier are used again two rounds later.  A CTA pushes its
+            // run of round r + 2 only when it has all runs of round r + 1, and a CTA pushes
+            // that one behind the __syncthreads that all its warps reach with round r read.
+            for (unsigned to = p.mute ? n : w; to < n; to += W)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    push(&cta_run[par][rank][lane * V + j], to, make_float2(tA[j], tb[j]));
-            cluster_barrier();
-            for (unsigned r = 0; r < n; ++r) {
-                if (r == rank) {
+                    push(&cta_run[(par * kMaxCluster + rank) * C + lane * V + j], &bars[par], to,
+                         make_float2(tA[j], tb[j]));
+            wait_runs(&bars[par], (round >> 1) & 1, p.limit_ns, &gave_up);
+            float2 g[kMaxCluster][V];
 #pragma unroll
-                    for (int j = 0; j < V; ++j) s[j] = after(pA[j], pb[j], state[j]);
-                }
+            for (int r = 0; r < kMaxCluster; ++r)
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float2 g = cta_run[par][r][lane * V + j];
-                    state[j] = after(g.x, g.y, state[j]);
+                for (int j = 0; j < V; ++j)
+                    if (r < n) g[r][j] = cta_run[(par * kMaxCluster + r) * C + lane * V + j];
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                if (r < n) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        if (r == rank) s[j] = after(pA[j], pb[j], state[j]);
+                        state[j] = after(g[r][j].x, g[r][j].y, state[j]);
+                    }
                 }
             }
+            if (threadIdx.x == 0 && !*(volatile int*)&gave_up)
+                mbar_arrive_expect_tx(&bars[par], runs_bytes);  // for round + 2
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -221,27 +371,37 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
                 state[j] = after(tA[j], tb[j], state[j]);
             }
         }
+        auto replay = [&](auto select, auto whole) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const long long u = u0 + i;
-            float out[V], dla[V];
+            for (int i = 0; i < R; ++i) {
+                float out[V], dla[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (BWD) {
-                    out[j] = v[i][j] + s[j];
-                    s[j] = a[i][j] == 0.f ? 0.f : a[i][j] * out[j];
-                    dla[j] = a[i][j] == 0.f ? 0.f : s[j] * hp[BWD ? i : 0][j];
-                } else {
-                    s[j] = after(a[i][j], v[i][j], s[j]);
-                    out[j] = s[j];
+                for (int j = 0; j < V; ++j) {
+                    const bool drop = decltype(select)::value && a[i][j] == 0.f;
+                    if (BWD) {
+                        out[j] = v[i][j] + s[j];
+                        s[j] = drop ? 0.f : a[i][j] * out[j];
+                        dla[j] = drop ? 0.f : s[j] * hp[BWD ? i : 0][j];
+                    } else {
+                        s[j] = drop ? v[i][j] : fmaf(a[i][j], s[j], v[i][j]);
+                        out[j] = s[j];
+                    }
+                }
+                if (on && (decltype(whole)::value || u0 + i < p.T)) {
+                    store_row<V>(y + i * step, out);
+                    if (BWD) store_row<V>(dlog_a + i * step, dla);
                 }
             }
-            if (on && u < p.T) {
-                const size_t t = BWD ? (size_t)(p.T - 1 - u) : (size_t)u;
-                store_row<V>(y + t * p.D, out);
-                if (BWD) store_row<V>(p.dlog_a + seq + t * p.D, dla);
-            }
-        }
+        };
+        if (cut || u0 + R > p.T) replay(std::true_type(), std::false_type());
+        else replay(std::false_type(), std::true_type());
+        u0 += leap;
+        y += leap * step;
+        if (BWD) dlog_a += leap * step;
+    }
+    if (n > 1) {
+        cluster_barrier();  // no CTA ends while another may still write to it
+        if (gave_up && threadIdx.x == 0 && p.dev_status) *p.dev_status = LA_ERR_TIMEOUT;
     }
     if (p.s_out && on && rank == 0 && w == 0) {
 #pragma unroll
@@ -272,36 +432,41 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const T* __restrict__ x,
     }
 }
 
-template <typename T, int V, int R, bool BWD>
+template <typename K>
 cudaError_t launch(const ScanParams& p, int B, int cluster, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(scan_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)K::kShared);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    const long long ctas = (long long)B * p.tiles * cluster;
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)((long long)B * p.tiles * cluster));
+    cfg.blockDim = dim3(K::W * 32);
+    cfg.dynamicSmemBytes = K::kShared;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, scan_kernel<T, V, R, BWD>, p);
+    return cudaLaunchKernelEx(&cfg, scan_kernel<K>, p);
 }
 
-// Tiles of 64 channels where there are enough of them, of 32 otherwise, and CTAs of a
-// cluster until the card is full or a CTA has a single round.
-template <typename T, int R, bool BWD>
-cudaError_t launch(ScanParams p, int B, cudaStream_t s) {
-    const long long want = sm_count() * 2LL;
-    const long long tiles2 = (p.D + 63) / 64, tiles1 = (p.D + 31) / 32;
-    const bool wide = tiles2 * B * kMaxCluster >= want && p.D % 64 == 0;
-    p.tiles = (int)(wide ? tiles2 : tiles1);
+// CTAs of a cluster until the card is full or a CTA has a single round.
+template <typename K>
+cudaError_t plan(ScanParams p, int B, cudaStream_t s) {
+    p.tiles = (p.D + K::C - 1) / K::C;
+    p.mute = opt_force_timeout();
+    p.limit_ns = p.mute ? 1000000ull : 2000000000ull;
+    const long long want = sm_count() * 2LL, units = (long long)B * p.tiles;
     int cluster = 1;
-    while (cluster < kMaxCluster && (long long)p.tiles * B * cluster < want &&
-           (long long)cluster * kWarps * R < p.T)
+    while (cluster < kMaxCluster && units * cluster * 2 <= want && (long long)cluster * K::kRun < p.T)
         cluster *= 2;
-    return wide ? launch<T, 2, R, BWD>(p, B, cluster, s) : launch<T, 1, R, BWD>(p, B, cluster, s);
+    return launch<K>(p, B, cluster, s);
+}
+
+template <typename T, bool BWD>
+cudaError_t launch(const ScanParams& p, int B, cudaStream_t s) {
+    return plan<Shape<T, 1, 16, 8, 2, BWD>>(p, B, s);
 }
 
 }  // namespace
@@ -309,10 +474,10 @@ cudaError_t launch(ScanParams p, int B, cudaStream_t s) {
 cudaError_t launch_scan_fwd(const RecurrenceArgs& a, cudaStream_t s) {
     ScanParams p = {};
     p.x = a.x; p.log_a = a.log_a; p.s0 = a.h0; p.y = a.h; p.s_out = a.h_out;
-    p.T = a.T; p.D = a.D;
+    p.T = a.T; p.D = a.D; p.dev_status = a.dev_status;
     TraceScope trace("scan_kernel", s);
-    const cudaError_t e = a.bf16 ? launch<__nv_bfloat16, 16, false>(p, a.B, s)
-                                 : launch<float, 16, false>(p, a.B, s);
+    const cudaError_t e = a.bf16 ? launch<__nv_bfloat16, false>(p, a.B, s)
+                                 : launch<float, false>(p, a.B, s);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -320,10 +485,10 @@ cudaError_t launch_scan_bwd(const RecurrenceArgs& a, cudaStream_t s) {
     ScanParams p = {};
     p.x = a.dh; p.log_a = a.log_a; p.s0 = a.dh_T; p.h_in = a.h; p.h0 = a.h0;
     p.y = a.dx; p.dlog_a = a.dlog_a; p.s_out = a.dh0;
-    p.T = a.T; p.D = a.D;
+    p.T = a.T; p.D = a.D; p.dev_status = a.dev_status;
     TraceScope trace("scan_bwd_kernel", s);
-    const cudaError_t e = a.bf16 ? launch<__nv_bfloat16, 8, true>(p, a.B, s)
-                                 : launch<float, 8, true>(p, a.B, s);
+    const cudaError_t e = a.bf16 ? launch<__nv_bfloat16, true>(p, a.B, s)
+                                 : launch<float, true>(p, a.B, s);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

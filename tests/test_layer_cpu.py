@@ -231,10 +231,11 @@ def scan_call(lib, kind, **over):
              dh0=FAKE + 9 * MB)
     a.update(over)
     if kind == "fwd":
-        return lib.la_scan_fwd(a["x"], a["dt"], a["la"], a["B"], a["T"], a["D"], a["h0"], a["h"], a["hT"], None)
+        return lib.la_scan_fwd(a["x"], a["dt"], a["la"], a["B"], a["T"], a["D"], a["h0"], a["h"], a["hT"], None,
+                               None)
     if kind == "bwd":
         return lib.la_scan_bwd(a["la"], a["h"], a["dh"], a["dt"], a["B"], a["T"], a["D"], a["h0"], a["dT"],
-                               a["dx"], a["dla"], a["dh0"], None)
+                               a["dx"], a["dla"], a["dh0"], None, None)
     return lib.la_scan_step(a["x"], a["dt"], a["la"], a["B"], a["D"], a["h0"], a["hT"], a["h"], None)
 
 

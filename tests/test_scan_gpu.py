@@ -216,3 +216,24 @@ def test_offsets_past_2_31_elements():
     assert float((dh0.double() - c).abs().max()) <= 2.0 ** -13 * c
     want = np.exp(-rate) * h[:, -2].double()  # the last token: c = a dh
     assert float(((dla[:, -1].double() - want).abs() / want).max()) <= 2.0 ** -20
+
+
+def test_a_wait_that_runs_out_is_reported(opts):
+    """The cluster's exchange, muted: both walks return after their limit of 1 ms with
+    the status set, and the next calls are whole again."""
+    x, log_a, h0, _, _ = inputs((1, 5003, 48, "f32", True, True))
+    want, _ = la.scan_fwd(x, log_a, h0=h0)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for call in (lambda: la.scan_fwd(x, log_a, h0=h0, dev_status=status),
+                 lambda: la.scan_bwd(log_a, want, x, h0=h0, dev_status=status)):
+        opts.force_timeout()
+        status.zero_()
+        call()
+        torch.cuda.synchronize()
+        assert int(status) == la.LA_ERR_TIMEOUT
+        opts.force_timeout(False)
+        status.zero_()
+        call()
+        got, _ = la.scan_fwd(x, log_a, h0=h0, dev_status=status)
+        torch.cuda.synchronize()
+        assert int(status) == 0 and torch.equal(got, want)
