@@ -22,6 +22,7 @@ Around them, for a whole layer:
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import functools
@@ -573,46 +574,74 @@ def chunk_fwd_host(q, k, v, gamma, *, phi=False, normalize=False, causal=True, e
     return out, S_out, z_out
 
 
-@contextlib.contextmanager
-def _launch_on(dev, stream):
+class _launch_on:
     """The tensors' device and the launch stream made current, so that what a call
-    allocates (outputs, workspace) belongs to the stream its kernels run on."""
-    with _current(dev):
-        if stream is None:
-            yield _stream(None)
-            return
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        if stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}; the inputs are on {dev}")
-        with torch.cuda.stream(stream):
-            yield _stream(stream)
+    allocates (outputs, workspace) belongs to the stream its kernels run on; enters to
+    the stream's handle.  Nothing is switched where both are current already, the usual
+    case: a decode step's cost on the host is as long as its kernels'."""
+
+    __slots__ = ("dev", "stream", "switched")
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.switched = dev, stream, None
+
+    def __enter__(self):
+        dev, stream = self.dev, self.stream
+        if dev.type != "cuda":
+            raise ValueError("liblinattn takes CUDA device tensors (use chunk_fwd_host for host data)")
+        if stream is None and torch._C._cuda_getDevice() == dev.index:
+            return torch._C._cuda_getCurrentRawStream(dev.index) or None
+        with contextlib.ExitStack() as switched:
+            switched.enter_context(torch.cuda.device(dev))
+            if stream is not None:
+                if not isinstance(stream, torch.cuda.Stream):
+                    stream = torch.cuda.ExternalStream(int(stream), device=dev)
+                if stream.device != dev:
+                    raise ValueError(f"the stream is on {stream.device}; the inputs are on {dev}")
+                switched.enter_context(torch.cuda.stream(stream))
+            self.switched = switched.pop_all()
+        return _stream(stream)
+
+    def __exit__(self, *exc):
+        if self.switched is not None:
+            return self.switched.__exit__(*exc)
+        return False
+
+
+_Strides = ctypes.c_longlong * 3
+
+
+def _refuse(t, name: str, shape, dtype, dev):
+    if t.shape != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}; {tuple(shape)} is needed")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    raise ValueError(f"{name} is on {t.device}; the inputs are on {dev}")
 
 
 def _rows(t, name: str, shape: tuple, dtype, dev):
-    """Address and host array of the three outer strides of a [.., .., .., d] tensor
-    whose rows of d entries are dense (None passes): what the library's strided
-    arguments take.  Shape, dtype and device are checked here, alignment there."""
+    """Address and host array of the three outer strides (None: dense) of a
+    [.., .., .., d] tensor whose rows of d entries are dense (None passes): what the
+    library's strided arguments take.  Shape, dtype and device are checked here,
+    alignment there."""
     if t is None:
         return None, None
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} is {tuple(t.shape)}; {shape} is needed")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}; the inputs are on {dev}")
-    if t.stride(3) != 1:
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        _refuse(t, name, shape, dtype, dev)
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1:
         raise ValueError(f"{name}: the entries of a row must lie one after another")
-    return t.data_ptr(), (ctypes.c_longlong * 3)(*t.stride()[:3])
+    return t.data_ptr(), _Strides(s0, s1, s2)
 
 
 def _dense(t, name: str, shape: tuple, dtype, dev) -> int | None:
     """Address of a contiguous tensor of exactly this shape, dtype and device."""
     if t is None:
         return None
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} is {tuple(t.shape)}; {shape} is needed")
-    _buffer(t, name, 0, dtype, dev)
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        _refuse(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -630,47 +659,44 @@ def rotary_frequencies(rot: int, base: float = 10000.0) -> list[float]:
     return list(_frequencies(int(rot), float(base)))
 
 
-class _QkCall:
-    """The arguments qk_rotate_fwd and qk_rotate_bwd share, checked."""
-
-    def __init__(self, q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight, k_weight,
-                 eps, q_scale, k_scale):
-        if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
-            raise ValueError(f"shape mismatch: q{tuple(q.shape)} k{tuple(k.shape)} are [B,T,heads,d]")
-        if q.dtype != k.dtype:
-            raise TypeError("q and k must share one dtype")
-        B, T, Hq, d = q.shape
-        Hk = k.shape[2]
-        self.dev, self.dtype, self.shape = q.device, q.dtype, (B, T, Hq, Hk, d)
-        self.code = _dtype_code(q)
-        rot = d if rot is None else int(rot)
-        if rot < 0 or rot > d or rot % 16:
-            raise ValueError(f"rot must be a multiple of 16 from 0 to {d}, not {rot}")
-        if isinstance(inv_freq, torch.Tensor):
-            if inv_freq.is_cuda:
-                raise ValueError("inv_freq is read on the host: pass host values")
-            inv_freq = inv_freq.tolist()
-        freq = _frequencies(rot, 10000.0) if inv_freq is None else inv_freq
-        if len(freq) != rot // 2:
-            raise ValueError(f"inv_freq holds {len(freq)} values; rot / 2 = {rot // 2} are needed")
-        self.freq = (ctypes.c_double * max(1, rot // 2))(*freq)
-        if positions is not None and (positions.dtype != torch.int32
-                                      or tuple(positions.shape) != (B, T)):
-            raise ValueError(f"positions must be int32 [B,T] = {(B, T)}")
-        pos0 = int(pos0)
-        if not 0 <= pos0 < 2 ** 31:
-            raise ValueError(f"pos0 must be from 0 to 2^31 - 1, not {pos0}")
-        self.flags = (LA_QK_NORM if norm else 0) | (LA_QK_ADJACENT if interleaved else 0)
-        xq, sq = _rows(q, "q", (B, T, Hq, d), self.dtype, self.dev)
-        xk, sk = _rows(k, "k", (B, T, Hk, d), self.dtype, self.dev)
-        f32 = torch.float32
-        self.keep = (sq, sk)
-        self.inputs = (xq, sq, xk, sk)
-        self.rest = (self.code, B, T, Hq, Hk, d, rot, self.freq,
-                     _dense(positions, "positions", (B, T), torch.int32, self.dev), pos0,
-                     _dense(q_weight, "q_weight", (d,), f32, self.dev),
-                     _dense(k_weight, "k_weight", (d,), f32, self.dev),
-                     float(eps), float(q_scale), float(k_scale), self.flags)
+def _qk_args(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight, k_weight, eps, q_scale,
+             k_scale):
+    """The arguments qk_rotate_fwd and qk_rotate_bwd share, checked: (q and k with their
+    strides, the rest, what has to outlive the call)."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"shape mismatch: q{tuple(q.shape)} k{tuple(k.shape)} are [B,T,heads,d]")
+    dt, dev = q.dtype, q.device
+    if k.dtype != dt:
+        raise TypeError("q and k must share one dtype")
+    B, T, Hq, d = q.shape
+    Bk, Tk, Hk, dk = k.shape
+    if Bk != B or Tk != T or dk != d:
+        raise ValueError(f"shape mismatch: q{tuple(q.shape)} k{tuple(k.shape)} are [B,T,heads,d]")
+    rot = d if rot is None else int(rot)
+    if rot < 0 or rot > d or rot % 16:
+        raise ValueError(f"rot must be a multiple of 16 from 0 to {d}, not {rot}")
+    if inv_freq is None:
+        inv_freq = _frequencies(rot, 10000.0)
+    elif isinstance(inv_freq, torch.Tensor):
+        if inv_freq.is_cuda:
+            raise ValueError("inv_freq is read on the host: pass host values")
+        inv_freq = inv_freq.tolist()
+    freq = array.array("d", inv_freq)
+    if len(freq) != rot // 2:
+        raise ValueError(f"inv_freq holds {len(freq)} values; rot / 2 = {rot // 2} are needed")
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (B, T)):
+        raise ValueError(f"positions must be int32 [B,T] = {(B, T)}")
+    pos0 = int(pos0)
+    if not 0 <= pos0 < 2 ** 31:
+        raise ValueError(f"pos0 must be from 0 to 2^31 - 1, not {pos0}")
+    f32 = torch.float32
+    inputs = _rows(q, "q", (B, T, Hq, d), dt, dev) + _rows(k, "k", (B, T, Hk, d), dt, dev)
+    rest = (_dtype_code(q), B, T, Hq, Hk, d, rot, freq.buffer_info()[0] if rot else None,
+            _dense(positions, "positions", (B, T), torch.int32, dev), pos0,
+            _dense(q_weight, "q_weight", (d,), f32, dev), _dense(k_weight, "k_weight", (d,), f32, dev),
+            float(eps), float(q_scale), float(k_scale),
+            (LA_QK_NORM if norm else 0) | (LA_QK_ADJACENT if interleaved else 0))
+    return inputs, rest, freq
 
 
 def qk_rotate_fwd(q, k, *, positions=None, pos0=0, rot=None, inv_freq=None, interleaved=False,
@@ -686,17 +712,16 @@ def qk_rotate_fwd(q, k, *, positions=None, pos0=0, rot=None, inv_freq=None, inte
     rot/2 host values, radians per position (None: rotary_frequencies(rot));
     interleaved: pairs (2m, 2m+1), else (m, m + rot/2).  norm: each row divided by
     the root of its mean square (plus eps), times q_weight / k_weight (fp32 [d])."""
-    a = _QkCall(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight, k_weight, eps,
-                q_scale, k_scale)
-    B, T, Hq, Hk, d = a.shape
-    with _launch_on(a.dev, stream) as s:
+    inputs, rest, freq = _qk_args(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight,
+                                  k_weight, eps, q_scale, k_scale)
+    (B, T, Hq, d), Hk, dt, dev = q.shape, k.shape[2], q.dtype, q.device
+    with _launch_on(dev, stream) as s:
         if q_out is None:
-            q_out = torch.empty((B, Hq, T, d), dtype=a.dtype, device=a.dev)
+            q_out = torch.empty((B, Hq, T, d), dtype=dt, device=dev)
         if k_out is None:
-            k_out = torch.empty((B, Hk, T, d), dtype=a.dtype, device=a.dev)
-        st = _load().la_qk_rotate_fwd(*a.inputs, *a.rest,
-                                      _dense(q_out, "q_out", (B, Hq, T, d), a.dtype, a.dev),
-                                      _dense(k_out, "k_out", (B, Hk, T, d), a.dtype, a.dev), s)
+            k_out = torch.empty((B, Hk, T, d), dtype=dt, device=dev)
+        st = _load().la_qk_rotate_fwd(*inputs, *rest, _dense(q_out, "q_out", (B, Hq, T, d), dt, dev),
+                                      _dense(k_out, "k_out", (B, Hk, T, d), dt, dev), s)
     _check(st, "la_qk_rotate_fwd")
     return q_out, k_out
 
@@ -709,28 +734,27 @@ def qk_rotate_bwd(q, k, dq_out, dk_out, *, positions=None, pos0=0, rot=None, inv
     dq_weight [d], dk_weight [d]); a weight's gradient is None where there is no
     weight or weight_grads is False.  dq and dk may be given, with strides (slices of
     one packed gradient)."""
-    a = _QkCall(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight, k_weight, eps,
-                q_scale, k_scale)
-    B, T, Hq, Hk, d = a.shape
+    inputs, rest, freq = _qk_args(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight,
+                                  k_weight, eps, q_scale, k_scale)
+    (B, T, Hq, d), Hk, dt, dev = q.shape, k.shape[2], q.dtype, q.device
     lib = _load()
-    with _launch_on(a.dev, stream) as s:
+    with _launch_on(dev, stream) as s:
         if dq is None:
-            dq = torch.empty((B, T, Hq, d), dtype=a.dtype, device=a.dev)
+            dq = torch.empty((B, T, Hq, d), dtype=dt, device=dev)
         if dk is None:
-            dk = torch.empty((B, T, Hk, d), dtype=a.dtype, device=a.dev)
-        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=a.dev)
+            dk = torch.empty((B, T, Hk, d), dtype=dt, device=dev)
+        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=dev)
                     if weight_grads and w is not None else None for w in (q_weight, k_weight))
         need = 0
         if dwq is not None or dwk is not None:
-            need = int(lib.la_qk_rotate_bwd_workspace_size(B, T, Hq, Hk, d, a.code))
+            need = int(lib.la_qk_rotate_bwd_workspace_size(B, T, Hq, Hk, d, rest[0]))
             if need and workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=a.dev)
-        ws_bytes = _workspace(workspace, need, a.dev)
-        gq = _dense(dq_out, "dq_out", (B, Hq, T, d), a.dtype, a.dev)
-        gk = _dense(dk_out, "dk_out", (B, Hk, T, d), a.dtype, a.dev)
-        st = lib.la_qk_rotate_bwd(*a.inputs, gq, gk, *a.rest,
-                                  *_rows(dq, "dq", (B, T, Hq, d), a.dtype, a.dev),
-                                  *_rows(dk, "dk", (B, T, Hk, d), a.dtype, a.dev),
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = _workspace(workspace, need, dev)
+        st = lib.la_qk_rotate_bwd(*inputs, _dense(dq_out, "dq_out", (B, Hq, T, d), dt, dev),
+                                  _dense(dk_out, "dk_out", (B, Hk, T, d), dt, dev), *rest,
+                                  *_rows(dq, "dq", (B, T, Hq, d), dt, dev),
+                                  *_rows(dk, "dk", (B, T, Hk, d), dt, dev),
                                   _ptr(dwq), _ptr(dwk), _ptr(workspace), ws_bytes, s)
     _check(st, "la_qk_rotate_bwd")
     return dq, dk, dwq, dwk
