@@ -16,155 +16,171 @@
 #include <algorithm>
 
 #include "rows.cuh"
+#include "tc_ptx.cuh"
 #include "trace.h"
 
 namespace la {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kRingBytes = 8;  // rows of the ring: kRingBytes / sizeof(T)
 
 struct GateParams {
     const void *o, *gate, *dy;
     void *y, *d_o, *d_gate;
     const float* w;
     float* part;  // [tokens' blocks][H][d] or null
-    long long o_sb, o_sh, o_st, g_sb, g_st, g_sh, dy_sb, dy_st, dy_sh;
-    long long y_sb, y_st, y_sh, do_sb, do_sh, do_st, dg_sb, dg_st, dg_sh;
+    long long o_b, o_h, o_t, g_b, g_t, g_h, dy_b, dy_t, dy_h;
+    long long y_b, y_t, y_h, do_b, do_h, do_t, dg_b, dg_t, dg_h;
+    Divide by_T;
     unsigned tokens;  // B T
-    int T, H, d, center;
+    int H, d, center;
     float eps;
 };
 
-// sigma(g), with no overflow turned into a NaN: e^-g = inf gives 0.
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + expf(-g)); }
+// sigma(g) to a few ulp: e^-g may overflow to infinity, whose reciprocal is 0.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + expf(-g)); }
 
 // x <- its normed row, returns r.  Lanes past the row hold zeros and keep them.
 template <int G>
-__device__ __forceinline__ float norm_row(float (&x)[8], bool on, int center, float inv_d, float eps) {
+__device__ __forceinline__ float norm_row(float2 (&x)[4], bool on, int center, float inv_d, float eps) {
     if (center) {
-        float sum = 0.f;
+        const float2 sum = __fadd2_rn(__fadd2_rn(x[0], x[1]), __fadd2_rn(x[2], x[3]));
+        float mean = group_sum<G>(sum.x + sum.y) * inv_d;
+        if (!on) mean = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += x[j];
-        const float mean = group_sum<G>(sum) * inv_d;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = on ? x[j] - mean : 0.f;
+        for (int j = 0; j < 4; ++j) x[j] = __fadd2_rn(x[j], both(-mean));
     }
-    float ss = 0.f;
+    const float r = rsqrtf(group_sum<G>(dot8(x, x)) * inv_d + eps);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
-    const float r = rsqrtf(group_sum<G>(ss) * inv_d + eps);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= r;
+    for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], both(r));
     return r;
 }
 
 // Grid: (heads, blocks of tokens).
-template <typename T, int G>
-__global__ void __launch_bounds__(kThreads) head_gate_fwd_kernel(const __grid_constant__ GateParams p) {
-    constexpr int kGroups = kThreads / G;
+template <typename T, int G, bool BWD>
+__global__ void __launch_bounds__(kThreads, 6) head_gate_kernel(const __grid_constant__ GateParams p) {
+    constexpr int kGroups = kThreads / G, kRing = kRingBytes / (int)sizeof(T), kSlot = 8 * G;
+    __shared__ __align__(16) T ring[kRing][BWD ? 3 : 2][kGroups * kSlot];  // o, gate, dy
+    if (BWD) tc::griddep_launch_dependents();  // the sums' kernel may be scheduled (it waits itself)
     const int lane = threadIdx.x % G, grp = threadIdx.x / G, e = lane * 8, h = blockIdx.x;
     const bool on = e < p.d;
     const float inv_d = 1.f / (float)p.d;
-    float w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = p.w && on ? __ldg(p.w + (size_t)h * p.d + e + j) : 1.f;
-    for (unsigned base = blockIdx.y * kGroups; base < p.tokens; base += gridDim.y * kGroups) {
-        const unsigned m = base + grp;
-        const bool row_on = on && m < p.tokens;
-        const int b = (int)(m / (unsigned)p.T), t = (int)(m - (unsigned)b * (unsigned)p.T);
-        Raw8<T> ro = zero_raw8<T>(), rg = zero_raw8<T>();
-        if (row_on) {
-            ro = load_raw8<true>((const T*)p.o + b * p.o_sb + h * p.o_sh + t * p.o_st, e, e + 4);
-            if (p.gate)
-                rg = load_raw8<true>((const T*)p.gate + b * p.g_sb + t * p.g_st + h * p.g_sh, e, e + 4);
-        }
-        float x[8], g[8];
-        floats8(ro, x);
-        floats8(rg, g);
-        norm_row<G>(x, on, p.center, inv_d, p.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] *= w[j];
-            if (p.gate) x[j] *= g[j] * sigmoid(g[j]);
-        }
-        if (row_on)
-            store8<true>((T*)p.y + b * p.y_sb + t * p.y_st + h * p.y_sh, e, e + 4, x);
-    }
-}
+    const T* o = (const T*)p.o + h * p.o_h;
+    const T* gate = p.gate ? (const T*)p.gate + h * p.g_h : nullptr;
+    const T* dy = BWD ? (const T*)p.dy + h * p.dy_h : nullptr;
+    const unsigned leap = gridDim.y * kGroups;
 
-template <typename T, int G>
-__global__ void __launch_bounds__(kThreads) head_gate_bwd_kernel(const __grid_constant__ GateParams p) {
-    constexpr int kGroups = kThreads / G;
-    __shared__ float red[kThreads * 8];
-    const int lane = threadIdx.x % G, grp = threadIdx.x / G, e = lane * 8, h = blockIdx.x;
-    const bool on = e < p.d;
-    const float inv_d = 1.f / (float)p.d;
-    float w[8], dw[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        w[j] = p.w && on ? __ldg(p.w + (size_t)h * p.d + e + j) : 1.f;
-        dw[j] = 0.f;
-    }
-    for (unsigned base = blockIdx.y * kGroups; base < p.tokens; base += gridDim.y * kGroups) {
-        const unsigned m = base + grp;
-        const bool row_on = on && m < p.tokens;
-        const int b = (int)(m / (unsigned)p.T), t = (int)(m - (unsigned)b * (unsigned)p.T);
-        Raw8<T> ro = zero_raw8<T>(), rg = zero_raw8<T>(), rd = zero_raw8<T>();
-        if (row_on) {
-            ro = load_raw8<true>((const T*)p.o + b * p.o_sb + h * p.o_sh + t * p.o_st, e, e + 4);
-            rd = load_raw8<true>((const T*)p.dy + b * p.dy_sb + t * p.dy_st + h * p.dy_sh, e, e + 4);
-            if (p.gate)
-                rg = load_raw8<true>((const T*)p.gate + b * p.g_sb + t * p.g_st + h * p.g_sh, e, e + 4);
+    unsigned f_base = blockIdx.y * kGroups;
+    int f_slot = 0;
+    auto fetch = [&]() {
+        if (f_base < p.tokens) {
+            const bool there = f_base + grp < p.tokens;
+            unsigned b, t;
+            p.by_T(there ? f_base + grp : 0, &b, &t);
+            copy_row<T, G>(&ring[f_slot][0][grp * kSlot], o + b * p.o_b + t * p.o_t, lane, p.d, there);
+            if (gate)
+                copy_row<T, G>(&ring[f_slot][1][grp * kSlot], gate + b * p.g_b + t * p.g_t, lane, p.d, there);
+            if (BWD)
+                copy_row<T, G>(&ring[f_slot][BWD ? 2 : 0][grp * kSlot], dy + b * p.dy_b + t * p.dy_t, lane, p.d,
+                               there);
+            f_base += leap;
         }
-        float n[8], g[8], du[8];
-        floats8(ro, n);
-        floats8(rd, du);
-        floats8(rg, g);
+        copies_commit();
+        f_slot = f_slot + 1 == kRing ? 0 : f_slot + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) fetch();
+
+    float2 w[4], dw[4];
+    row_weights<false>(p.w ? p.w + (size_t)h * p.d : nullptr, on, e, e + 4, w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[j] = make_float2(0.f, 0.f);
+    int slot = 0;
+    for (unsigned base = blockIdx.y * kGroups; base < p.tokens; base += leap) {
+        const bool row_on = on && base + grp < p.tokens;
+        copies_wait<kRing - 1>();
+        __syncwarp();
+        float2 n[4], g[4], du[4];
+        floats8<false>(raw8<true>(&ring[slot][0][grp * kSlot], e, e + 4), n);
+        if (gate) floats8<false>(raw8<true>(&ring[slot][1][grp * kSlot], e, e + 4), g);
+        if (BWD) floats8<false>(raw8<true>(&ring[slot][BWD ? 2 : 0][grp * kSlot], e, e + 4), du);
+        __syncwarp();
+        fetch();
+        slot = slot + 1 == kRing ? 0 : slot + 1;
+        unsigned b, t;
+        p.by_T(base + grp, &b, &t);
         const float r = norm_row<G>(n, on, p.center, inv_d, p.eps);
-        float dot = 0.f, mean = 0.f;
+        if (!BWD) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (p.gate) {
-                const float sg = sigmoid(g[j]), d = du[j];
-                du[j] = d * (g[j] * sg);
-                g[j] = d * n[j] * w[j] * (sg * (1.f + g[j] * (1.f - sg)));
+            for (int j = 0; j < 4; ++j) n[j] = __fmul2_rn(n[j], w[j]);
+            if (gate) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    n[j] = __fmul2_rn(n[j], __fmul2_rn(g[j], make_float2(sigmoid(g[j].x), sigmoid(g[j].y))));
             }
-            if (row_on) dw[j] += du[j] * n[j];
-            du[j] *= w[j];
-            dot += du[j] * n[j];
-            mean += du[j];
-        }
-        dot = group_sum<G>(dot) * inv_d;
-        mean = p.center ? group_sum<G>(mean) * inv_d : 0.f;
+            if (row_on)
+                store8<true, false>((T*)p.y + h * p.y_h + b * p.y_b + t * p.y_t, e, e + 4, n);
+        } else {
+            if (gate) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) du[j] = r * (du[j] - mean - n[j] * dot);
-        if (row_on) {
-            store8<true>((T*)p.d_o + b * p.do_sb + h * p.do_sh + t * p.do_st, e, e + 4, du);
-            if (p.gate)
-                store8<true>((T*)p.d_gate + b * p.dg_sb + t * p.dg_st + h * p.dg_sh, e, e + 4, g);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 sg = make_float2(sigmoid(g[j].x), sigmoid(g[j].y));
+                    // slope: sigma (1 + g (1 - sigma))
+                    const float2 slope = __fmul2_rn(
+                        sg, __ffma2_rn(g[j], __fadd2_rn(both(1.f), make_float2(-sg.x, -sg.y)), both(1.f)));
+                    const float2 act = __fmul2_rn(g[j], sg);
+                    g[j] = __fmul2_rn(__fmul2_rn(du[j], __fmul2_rn(n[j], w[j])), slope);
+                    du[j] = __fmul2_rn(du[j], act);
+                }
+                if (row_on)
+                    store8<true, false>((T*)p.d_gate + h * p.dg_h + b * p.dg_b + t * p.dg_t, e, e + 4, g);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // rows that are not there hold zeros and add none
+                dw[j] = __ffma2_rn(du[j], n[j], dw[j]);
+                du[j] = __fmul2_rn(du[j], w[j]);
+            }
+            const float along = -group_sum<G>(dot8(du, n)) * inv_d;
+            float mean = 0.f;
+            if (p.center) {
+                const float2 sum = __fadd2_rn(__fadd2_rn(du[0], du[1]), __fadd2_rn(du[2], du[3]));
+                mean = -group_sum<G>(sum.x + sum.y) * inv_d;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                du[j] = __fmul2_rn(both(r), __ffma2_rn(n[j], both(along), __fadd2_rn(du[j], both(mean))));
+            if (row_on) store8<true, false>((T*)p.d_o + h * p.do_h + b * p.do_b + t * p.do_t, e, e + 4, du);
         }
     }
-    if (!p.part) return;
+    if (!BWD || !p.part) return;
+    float* red = reinterpret_cast<float*>(&ring[0][0][0]);
+    static_assert(sizeof(ring) >= kThreads * 8 * sizeof(float), "a thread's eight sums fit the ring");
+    copies_wait<0>();
+    __syncthreads();
+    if (on) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (on) red[grp * G * 8 + e + j] = dw[j];
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&red[grp * kSlot + e + 2 * j]) = dw[j];
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < p.d; c += kThreads) {
         float sum = 0.f;
-        for (int i = 0; i < kGroups; ++i) sum += red[i * G * 8 + c];
+        for (int i = 0; i < kGroups; ++i) sum += red[i * kSlot + c];
         p.part[((size_t)blockIdx.y * p.H + h) * p.d + c] = sum;
     }
 }
 
-// Blocks of tokens a head's CTAs share: enough CTAs to fill the card a few times.
-unsigned token_blocks(const HeadGateArgs& a, int per_sm) {
-    const long long groups = kThreads / group_lanes(a.d), tokens = (long long)a.B * a.T;
-    const long long want = ((long long)sm_count() * per_sm + a.H - 1) / a.H;
-    return (unsigned)std::min<long long>(std::min<long long>((tokens + groups - 1) / groups, want), 65535);
-}
+// CTAs a head's tokens are shared out to: a few CTAs per SM in all; backward each
+// leaves one row of partial sums.
+constexpr int kFwdPerSm = 32, kBwdPerSm = 12;
 
-constexpr int kFwdPerSm = 32, kBwdPerSm = 8;
+unsigned token_blocks(const HeadGateArgs& a, bool bwd) {
+    const long long groups = kThreads / group_lanes(a.d);
+    const long long turns = ((long long)a.B * a.T + groups - 1) / groups;
+    const long long most = ((long long)sm_count() * (bwd ? kBwdPerSm : kFwdPerSm) + a.H - 1) / a.H;
+    return (unsigned)std::min(turns, std::min(most, 65535ll));
+}
 
 GateParams params(const HeadGateArgs& a) {
     GateParams p;
@@ -172,22 +188,23 @@ GateParams params(const HeadGateArgs& a) {
     p.y = a.y; p.d_o = a.d_o; p.d_gate = a.d_gate;
     p.w = a.weight;
     p.part = a.d_weight ? (float*)a.workspace : nullptr;
-    p.o_sb = a.o_strides[0]; p.o_sh = a.o_strides[1]; p.o_st = a.o_strides[2];
-    p.g_sb = a.gate_strides[0]; p.g_st = a.gate_strides[1]; p.g_sh = a.gate_strides[2];
-    p.dy_sb = a.dy_strides[0]; p.dy_st = a.dy_strides[1]; p.dy_sh = a.dy_strides[2];
-    p.y_sb = a.y_strides[0]; p.y_st = a.y_strides[1]; p.y_sh = a.y_strides[2];
-    p.do_sb = a.do_strides[0]; p.do_sh = a.do_strides[1]; p.do_st = a.do_strides[2];
-    p.dg_sb = a.dgate_strides[0]; p.dg_st = a.dgate_strides[1]; p.dg_sh = a.dgate_strides[2];
+    p.o_b = a.o_strides[0]; p.o_h = a.o_strides[1]; p.o_t = a.o_strides[2];
+    p.g_b = a.gate_strides[0]; p.g_t = a.gate_strides[1]; p.g_h = a.gate_strides[2];
+    p.dy_b = a.dy_strides[0]; p.dy_t = a.dy_strides[1]; p.dy_h = a.dy_strides[2];
+    p.y_b = a.y_strides[0]; p.y_t = a.y_strides[1]; p.y_h = a.y_strides[2];
+    p.do_b = a.do_strides[0]; p.do_h = a.do_strides[1]; p.do_t = a.do_strides[2];
+    p.dg_b = a.dgate_strides[0]; p.dg_t = a.dgate_strides[1]; p.dg_h = a.dgate_strides[2];
     p.tokens = (unsigned)((long long)a.B * a.T);
-    p.T = a.T; p.H = a.H; p.d = a.d; p.center = a.center;
+    p.by_T = Divide::by(a.T);
+    p.H = a.H; p.d = a.d; p.center = a.center;
     p.eps = a.eps;
     return p;
 }
 
 template <typename T, int G>
 void launch(const GateParams& p, bool bwd, dim3 grid, cudaStream_t s) {
-    if (bwd) head_gate_bwd_kernel<T, G><<<grid, kThreads, 0, s>>>(p);
-    else head_gate_fwd_kernel<T, G><<<grid, kThreads, 0, s>>>(p);
+    if (bwd) head_gate_kernel<T, G, true><<<grid, kThreads, 0, s>>>(p);
+    else head_gate_kernel<T, G, false><<<grid, kThreads, 0, s>>>(p);
 }
 
 template <typename T>
@@ -204,12 +221,12 @@ void launch(const GateParams& p, bool bwd, dim3 grid, cudaStream_t s) {
 }  // namespace
 
 size_t head_gate_bwd_workspace_bytes(const HeadGateArgs& a) {
-    return (size_t)token_blocks(a, kBwdPerSm) * a.H * a.d * sizeof(float);
+    return (size_t)token_blocks(a, true) * a.H * a.d * sizeof(float);
 }
 
 cudaError_t launch_head_gate_fwd(const HeadGateArgs& a, cudaStream_t s) {
     const GateParams p = params(a);
-    const dim3 grid(a.H, token_blocks(a, kFwdPerSm));
+    const dim3 grid(a.H, token_blocks(a, false));
     TraceScope trace("head_gate_fwd_kernel", s);
     if (a.bf16) launch<__nv_bfloat16>(p, false, grid, s);
     else launch<float>(p, false, grid, s);
@@ -218,7 +235,7 @@ cudaError_t launch_head_gate_fwd(const HeadGateArgs& a, cudaStream_t s) {
 
 cudaError_t launch_head_gate_bwd(const HeadGateArgs& a, cudaStream_t s) {
     const GateParams p = params(a);
-    const dim3 grid(a.H, token_blocks(a, kBwdPerSm));
+    const dim3 grid(a.H, token_blocks(a, true));
     {
         TraceScope trace("head_gate_bwd_kernel", s);
         if (a.bf16) launch<__nv_bfloat16>(p, true, grid, s);
@@ -226,7 +243,7 @@ cudaError_t launch_head_gate_bwd(const HeadGateArgs& a, cudaStream_t s) {
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.part) return e;
-    return launch_partial_sum(p.part, (int)grid.y, a.d_weight, a.H * a.d, nullptr, 0, s);
+    return launch_partial_sum(p.part, (int)grid.y, a.d_weight, nullptr, 0, nullptr, a.H * a.d, s);
 }
 
 }  // namespace la

@@ -16,60 +16,99 @@
 // Bound by HBM: 2 bytes in and 2 out an entry (bf16), about 10 operations.  A
 // group of d / 8 lanes holds one row.  With split halves a lane holds four entries
 // of the first half and the four they pair with, so that the rotation needs no
-// exchange between lanes.  A group keeps its token and walks heads: the four angles
-// of a lane are computed once for a block of heads.
+// exchange between lanes.  A group keeps its token and walks heads of q or of k: the
+// four angles of a lane are computed once for a block of heads, and a CTA works on
+// one of the two tensors, so that a lane keeps one set of weights (and of their
+// gradients' sums).
 #include <algorithm>
 #include <cmath>
 
 #include "rows.cuh"
+#include "tc_ptx.cuh"
 #include "trace.h"
 
 namespace la {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 4;  // rows (heads) whose loads are in flight together
+constexpr int kThreads = 128;
+constexpr int kFwdRows = 4;    // rows (heads) whose loads are in flight together
+constexpr int kRingBytes = 16; // backward: the ring's rows are kRingBytes / sizeof(T)
+
+// q or k.
+struct Side {
+    const void* x;            // raw projection
+    const void* g;            // backward: the gradient of its output [B][H][T][d]
+    void* y;                  // output, or the projection's gradient
+    const float* w;           // norm weights [d] or null
+    float* part;              // backward: per-CTA weight gradients [CTA][d] or null
+    long long x_b, x_t, x_h;  // strides, elements
+    long long y_b, y_t, y_h;
+    int H, hb, nhb;           // heads, heads a group walks at a stretch, such blocks of heads
+    unsigned items, ctas;     // B nhb T: what the groups share out; this side's CTAs
+    float scale;
+};
 
 struct QkParams {
-    const void *q, *k;            // raw projections
-    const void *gq, *gk;          // backward: gradients of the outputs [B][H][T][d]
-    void *yq, *yk;                // outputs, or the projections' gradients
-    const float *wq, *wk;         // norm weights [d] or null
-    float* part;                  // backward: per-CTA weight gradients [CTA][2][d] or null
-    long long q_sb, q_st, q_sh, k_sb, k_st, k_sh;      // elements
-    long long yq_sb, yq_st, yq_sh, yk_sb, yk_st, yk_sh;
+    Side side[2];  // q's CTAs first
     const int* positions;         // [B][T] or null: pos0 + t
-    int pos0, B, T, Hq, Hk, d, rot, norm;
-    int hb, nhb;                  // heads a group walks, blocks of heads
-    unsigned items;               // B nhb T: what the groups share out
-    float eps, q_scale, k_scale;
-    unsigned long long freq[128]; // turns per position, units of 2^-64
+    Divide tokens;                // by T
+    int pos0, d, rot, norm;
+    bool both;                    // forward: a group takes its token's q and k
+    float eps;
+    uint2 freq[128];              // turns per position: x 2^-64 + y 2^-32
+};
 
-    // Neighbouring groups take neighbouring tokens: their output rows touch.
-    __device__ __forceinline__ void place(unsigned item, int* t, int* hblk, int* b) const {
-        const unsigned row = item / (unsigned)T;
-        *t = (int)(item - row * (unsigned)T);
-        *b = (int)(row / (unsigned)nhb);
-        *hblk = (int)(row - (unsigned)*b * (unsigned)nhb);
+// Where a group stands: an item is a token and a block of heads of one side.
+// Neighbouring groups take neighbouring tokens: their output rows touch.
+struct Place {
+    int b, t, h0, heads;  // heads 0: no such item (its group keeps the shuffles company)
+
+    __device__ __forceinline__ Place(const QkParams& p, const Side& a, unsigned item) {
+        const bool live = item < a.items;
+        unsigned row, tt, bb, hblk = 0;
+        p.tokens(live ? item : 0, &row, &tt);
+        bb = row;
+        if (a.nhb > 1) {
+            bb = row / (unsigned)a.nhb;
+            hblk = row - bb * (unsigned)a.nhb;
+        }
+        b = (int)bb;
+        t = (int)tt;
+        h0 = (int)hblk * a.hb;
+        heads = live ? min(a.hb, a.H - h0) : 0;
     }
 };
 
-// cos and sin of p F turns: the nearest quarter turn apart, the rest (at most an
-// eighth of a turn) to fp32.
-__device__ __forceinline__ void turn(unsigned long long frac, float* c, float* s) {
-    const unsigned quarter = (unsigned)((frac + (1ull << 61)) >> 62);
-    const int rest = (int)((frac - ((unsigned long long)quarter << 62)) >> 32);
-    float s0, c0;
-    sincospif((float)rest * 4.656612873077393e-10f, &s0, &c0);  // 2^-31: half turns
-    const float cc = (quarter & 1) ? s0 : c0, ss = (quarter & 1) ? c0 : s0;
-    *c = ((quarter + 1) & 2) ? -cc : cc;
-    *s = (quarter & 2) ? -ss : ss;
+// cos and sin of p F, F = hi 2^-32 + lo 2^-64 turns.  Of the product modulo one turn
+// the upper 32 bits are kept: the nearest quarter turn, and the rest, at most an eighth
+// of a turn (pi / 4), whose sine and cosine are their Taylor series.  The first terms
+// left out, x^11 / 11! and x^12 / 12!, are below 2^-29 there.
+__device__ __forceinline__ void turn(int p, uint2 f, float* c, float* s) {
+    // the product of p + 2^32 [p < 0] and F, less F 2^32 [p < 0]
+    unsigned frac = __umulhi((unsigned)p, f.x) + (unsigned)p * f.y - (p < 0 ? f.x : 0u);
+    frac += 1u << 29;
+    const unsigned quarter = frac >> 30;
+    const float x = (float)((int)(frac & 0x3fffffffu) - (1 << 29)) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+    const float z = x * x;
+    float sx = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
+    sx = fmaf(z, sx, 8.3333333e-3f);
+    sx = fmaf(z, sx, -1.6666667e-1f);
+    sx = fmaf(z * x, sx, x);
+    float cx = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+    cx = fmaf(z, cx, -1.3888889e-3f);
+    cx = fmaf(z, cx, 4.1666667e-2f);
+    cx = fmaf(z, cx, -0.5f);
+    cx = fmaf(z, cx, 1.f);
+    const float cc = (quarter & 1) ? sx : cx, ss = (quarter & 1) ? cx : sx;
+    // quarters 1 and 2 turn the cosine's sign, 2 and 3 the sine's
+    *c = __uint_as_float(__float_as_uint(cc) ^ ((quarter + 1) << 30 & 0x80000000u));
+    *s = __uint_as_float(__float_as_uint(ss) ^ (quarter << 30 & 0x80000000u));
 }
 
 // A lane's entries and angles: entries e1..e1+3 and e2..e2+3; in the rotated part
 // its four pairs are number 4 lane + j, (j, j + 4) of its eight with split halves
-// and (2j, 2j + 1) with adjacent ones.
+// and (2j, 2j + 1) with adjacent ones (held with the even entries first).
 template <bool HALVES>
 struct Lane {
     int e1, e2;
@@ -82,225 +121,248 @@ struct Lane {
         e2 = HALVES && turned ? rot / 2 + lane * 4 : lane * 8 + 4;
     }
 
-    __device__ __forceinline__ void angles(const unsigned long long* freq, int lane, int pos,
-                                           float (&c)[4], float (&s)[4]) const {
+    __device__ __forceinline__ void angles(const uint2* freq, int lane, int pos,
+                                           float2 (&c)[2], float2 (&s)[2]) const {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            c[j] = 1.f;
-            s[j] = 0.f;
-            if (turned) turn((unsigned long long)(long long)pos * freq[lane * 4 + j], &c[j], &s[j]);
+        for (int j = 0; j < 2; ++j) {
+            c[j] = make_float2(1.f, 1.f);
+            s[j] = make_float2(0.f, 0.f);
+            if (turned) {
+                turn(pos, freq[lane * 4 + 2 * j], &c[j].x, &s[j].x);
+                turn(pos, freq[lane * 4 + 2 * j + 1], &c[j].y, &s[j].y);
+            }
         }
     }
 
-    // x <- R x (dir = 1) or R^T x (dir = -1)
-    __device__ __forceinline__ static void rotate(float (&x)[8], const float (&c)[4],
-                                                  const float (&s)[4], float dir) {
+    // x <- R x with (c, s), R^T x with (c, -s): its first four entries are the first ones
+    // of the four pairs
+    __device__ __forceinline__ static void rotate(float2 (&x)[4], const float2 (&c)[2], const float2 (&s)[2]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i1 = HALVES ? j : 2 * j, i2 = HALVES ? j + 4 : 2 * j + 1;
-            const float a = x[i1], b = x[i2], sj = dir * s[j];
-            x[i1] = a * c[j] - b * sj;
-            x[i2] = a * sj + b * c[j];
+        for (int j = 0; j < 2; ++j) {
+            const float2 a = x[j], b = x[j + 2], minus = make_float2(-s[j].x, -s[j].y);
+            x[j] = __ffma2_rn(a, c[j], __fmul2_rn(b, minus));
+            x[j + 2] = __ffma2_rn(a, s[j], __fmul2_rn(b, c[j]));
         }
     }
 };
 
-template <bool HALVES>
-__device__ __forceinline__ void load_weights(const float* w, const Lane<HALVES>& l, float (&x)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = 1.f;
-    if (w && l.on) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[j] = __ldg(w + l.e1 + j);
-            x[j + 4] = __ldg(w + l.e2 + j);
-        }
-    }
-}
-
+// Forward: a group takes one item, its rows' loads kFwdRows at a time in registers.
 template <typename T, int G, bool HALVES>
 __global__ void __launch_bounds__(kThreads) qk_rotate_fwd_kernel(const __grid_constant__ QkParams p) {
-    __shared__ unsigned long long freq[128];
+    constexpr bool RUN = !HALVES, PAIRS = !HALVES;
+    __shared__ uint2 freq[128];
     for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) freq[i] = p.freq[i];
     __syncthreads();
+    // a CTA's groups take items of one side, or (both) a token's q and k in turn
+    const int first = blockIdx.x >= p.side[0].ctas, last = p.both ? 1 : first;
+    const unsigned cta = first ? blockIdx.x - p.side[0].ctas : blockIdx.x;
     const int lane = threadIdx.x % G;
-    const unsigned item = blockIdx.x * (kThreads / G) + threadIdx.x / G;
-    const bool live = item < p.items;  // whole groups; dead ones keep the shuffles company
-    int t, hblk, b;
-    p.place(live ? item : 0, &t, &hblk, &b);
     const Lane<HALVES> l(lane, p.d, p.rot);
-    const int pos = p.positions ? __ldg(p.positions + (long long)b * p.T + t) : p.pos0 + t;
-    float c[4], s[4];
-    l.angles(freq, lane, pos, c, s);
-    float wq[8], wk[8];
-    load_weights<HALVES>(p.wq, l, wq);
-    load_weights<HALVES>(p.wk, l, wk);
-    const T* q = (const T*)p.q + b * p.q_sb + t * p.q_st;
-    const T* k = (const T*)p.k + b * p.k_sb + t * p.k_st;
     const float inv_d = 1.f / (float)p.d;
-    const int heads = p.Hq + p.Hk;
-    for (int i = 0; i < p.hb; i += kRows) {
-        const int h0 = hblk * p.hb + i;
-        Raw8<T> raw[kRows];
+    float2 c[2], s[2];
+    for (int side = first; side <= last; ++side) {
+        const Side& a = p.side[side];
+        const Place at(p, a, cta * (kThreads / G) + threadIdx.x / G);
+        const int heads = l.on ? at.heads : 0;
+        const T* x_row = (const T*)a.x + at.b * a.x_b + at.t * a.x_t + at.h0 * a.x_h;
+        T* y_row = (T*)a.y + (((long long)at.b * a.H + at.h0) * p.tokens.T + at.t) * p.d;
+        const long long y_h = (long long)p.tokens.T * p.d;
+        Raw8<T> raw[kFwdRows];
+        auto fetch = [&](int i) {
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int h = h0 + u;
-            const T* row = h < p.Hq ? q + h * p.q_sh : k + (h - p.Hq) * p.k_sh;
-            raw[u] = live && l.on && i + u < p.hb && h < heads ? load_raw8<!HALVES>(row, l.e1, l.e2)
-                                                               : zero_raw8<T>();
-        }
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            if (i + u >= p.hb) break;  // the same for every group
-            const int h = h0 + u;
-            const bool key = h >= p.Hq;
-            float x[8];
-            floats8(raw[u], x);
-            float f = key ? p.k_scale : p.q_scale;
-            if (p.norm) {
-                float ss = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
-                f *= rsqrtf(group_sum<G>(ss) * inv_d + p.eps);
+            for (int u = 0; u < kFwdRows; ++u) {
+                raw[u].a = {};
+                raw[u].b = {};
+                if (i + u < heads) raw[u] = raw8<RUN>(x_row + (i + u) * a.x_h, l.e1, l.e2);
             }
+        };
+        fetch(0);  // before the angles: their arithmetic covers the first loads
+        float2 w[4];
+        row_weights<PAIRS>(a.w, l.on, l.e1, l.e2, w);
+        if (side == first)
+            l.angles(freq, lane,
+                     p.positions ? __ldg(p.positions + (long long)at.b * p.tokens.T + at.t) : p.pos0 + at.t, c, s);
+        for (int i = 0; i < a.hb; i += kFwdRows) {  // the same for every group, dead ones too
+            if (i > 0) fetch(i);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= f * (key ? wk[j] : wq[j]);
-            Lane<HALVES>::rotate(x, c, s, 1.f);
-            if (live && l.on && h < heads) {
-                T* y = key ? (T*)p.yk + (((long long)b * p.Hk + (h - p.Hq)) * p.T + t) * p.d
-                           : (T*)p.yq + (((long long)b * p.Hq + h) * p.T + t) * p.d;
-                store8<!HALVES>(y, l.e1, l.e2, x);
+            for (int u = 0; u < kFwdRows; ++u) {
+                if (i + u >= a.hb) break;
+                float2 x[4];
+                floats8<PAIRS>(raw[u], x);
+                float f = a.scale;
+                if (p.norm) f *= rsqrtf(group_sum<G>(dot8(x, x)) * inv_d + p.eps);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], __fmul2_rn(w[j], both(f)));
+                Lane<HALVES>::rotate(x, c, s);
+                if (i + u < heads) store8<RUN, PAIRS>(y_row + (i + u) * y_h, l.e1, l.e2, x);
             }
         }
     }
 }
 
+// Backward: a CTA's groups walk items of one side; their rows come through the ring.
 template <typename T, int G, bool HALVES>
-__global__ void __launch_bounds__(kThreads) qk_rotate_bwd_kernel(const __grid_constant__ QkParams p) {
-    __shared__ unsigned long long freq[128];
-    __shared__ float red[(kThreads / G) * G * 8];
+__global__ void __launch_bounds__(kThreads, 4) qk_rotate_bwd_kernel(const __grid_constant__ QkParams p) {
+    constexpr int kGroups = kThreads / G, kRing = kRingBytes / (int)sizeof(T), kSlot = 8 * G;
+    constexpr bool RUN = !HALVES, PAIRS = !HALVES;
+    __shared__ __align__(16) T ring[kRing][2][kGroups * kSlot];
+    __shared__ uint2 freq[128];
+    tc::griddep_launch_dependents();  // the sums' kernel may be scheduled (it waits itself)
     for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) freq[i] = p.freq[i];
     __syncthreads();
+    const int key = blockIdx.x >= p.side[0].ctas;
+    const Side& a = p.side[key];
+    const unsigned cta = key ? blockIdx.x - p.side[0].ctas : blockIdx.x, leap = a.ctas * kGroups;
     const int lane = threadIdx.x % G, grp = threadIdx.x / G;
-    constexpr int kGroups = kThreads / G;
     const Lane<HALVES> l(lane, p.d, p.rot);
-    float wq[8], wk[8], dwq[8], dwk[8];
-    load_weights<HALVES>(p.wq, l, wq);
-    load_weights<HALVES>(p.wk, l, wk);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dwq[j] = dwk[j] = 0.f;
     const float inv_d = 1.f / (float)p.d;
-    // the bound is the CTA's first item: every group of a warp takes the same turns
-    for (unsigned base = blockIdx.x * kGroups; base < p.items; base += gridDim.x * kGroups) {
-        const unsigned item = base + grp;
-        const bool live = item < p.items;
-        int t, hblk, b;
-        p.place(live ? item : 0, &t, &hblk, &b);
-        const int pos = p.positions ? __ldg(p.positions + (long long)b * p.T + t) : p.pos0 + t;
-        float c[4], s[4];
-        l.angles(freq, lane, pos, c, s);
-        for (int i = 0; i < p.hb; ++i) {  // the same for every group, dead ones too
-            const int h = hblk * p.hb + i;
-            const bool key = h >= p.Hq, row_on = live && l.on && h < p.Hq + p.Hk;
-            const int hh = key ? h - p.Hq : h;
-            Raw8<T> rx = zero_raw8<T>(), rg = zero_raw8<T>();
-            if (row_on) {
-                const T* xr = key ? (const T*)p.k + b * p.k_sb + t * p.k_st + hh * p.k_sh
-                                  : (const T*)p.q + b * p.q_sb + t * p.q_st + hh * p.q_sh;
-                const T* gr = key ? (const T*)p.gk + (((long long)b * p.Hk + hh) * p.T + t) * p.d
-                                  : (const T*)p.gq + (((long long)b * p.Hq + hh) * p.T + t) * p.d;
-                rx = load_raw8<!HALVES>(xr, l.e1, l.e2);
-                rg = load_raw8<!HALVES>(gr, l.e1, l.e2);
+    const long long g_h = (long long)p.tokens.T * p.d;
+
+    // the fetching end: f_base is the CTA's first item (all groups take the same turns)
+    unsigned f_base = cta * kGroups;
+    int f_i = 0, f_heads = 0, f_slot = 0;
+    const T *f_x = nullptr, *f_g = nullptr;
+    auto fetch = [&]() {
+        if (f_base < a.items) {
+            if (f_i == 0) {
+                const Place at(p, a, f_base + grp);
+                f_heads = at.heads;
+                f_x = (const T*)a.x + at.b * a.x_b + at.t * a.x_t + at.h0 * a.x_h;
+                f_g = (const T*)a.g + (((long long)at.b * a.H + at.h0) * p.tokens.T + at.t) * p.d;
             }
-            float x[8], g[8];
-            floats8(rx, x);
-            floats8(rg, g);
-            const float scale = key ? p.k_scale : p.q_scale;
-            Lane<HALVES>::rotate(g, c, s, -1.f);
+            copy_row<T, G>(&ring[f_slot][0][grp * kSlot], f_x, lane, p.d, f_i < f_heads);
+            copy_row<T, G>(&ring[f_slot][1][grp * kSlot], f_g, lane, p.d, f_i < f_heads);
+            if (++f_i < f_heads) {
+                f_x += a.x_h;
+                f_g += g_h;
+            }
+            if (f_i == a.hb) {
+                f_i = 0;
+                f_base += leap;
+            }
+        }
+        copies_commit();
+        f_slot = f_slot + 1 == kRing ? 0 : f_slot + 1;
+    };
 #pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] *= scale;
+    for (int i = 0; i < kRing; ++i) fetch();
+
+    float2 w[4], dw[4], c[2], s[2];
+    row_weights<PAIRS>(a.w, l.on, l.e1, l.e2, w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[j] = make_float2(0.f, 0.f);
+    int slot = 0;
+    for (unsigned base = cta * kGroups; base < a.items; base += leap) {
+        const Place at(p, a, base + grp);
+        const int heads = l.on ? at.heads : 0;
+        l.angles(freq, lane, p.positions ? __ldg(p.positions + (long long)at.b * p.tokens.T + at.t) : p.pos0 + at.t,
+                 c, s);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // back, and the scale with it
+            c[j] = __fmul2_rn(c[j], both(a.scale));
+            s[j] = __fmul2_rn(s[j], both(-a.scale));
+        }
+        T* y = (T*)a.y + at.b * a.y_b + at.t * a.y_t + at.h0 * a.y_h;
+        for (int i = 0; i < a.hb; ++i) {
+            copies_wait<kRing - 1>();
+            __syncwarp();
+            float2 x[4], g[4];
+            floats8<PAIRS>(raw8<RUN>(&ring[slot][0][grp * kSlot], l.e1, l.e2), x);
+            floats8<PAIRS>(raw8<RUN>(&ring[slot][1][grp * kSlot], l.e1, l.e2), g);
+            __syncwarp();
+            fetch();
+            slot = slot + 1 == kRing ? 0 : slot + 1;
+            Lane<HALVES>::rotate(g, c, s);
             if (p.norm) {
-                float ss = 0.f;
+                float2 gw[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
-                const float r = rsqrtf(group_sum<G>(ss) * inv_d + p.eps);
-                float dot = 0.f;
+                for (int j = 0; j < 4; ++j) gw[j] = __fmul2_rn(g[j], w[j]);
+                const float ss = group_sum<G>(dot8(x, x)), along = group_sum<G>(dot8(gw, x));
+                const float n = rsqrtf(ss * inv_d + p.eps), back = -n * (n * along * inv_d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[j] *= r;
-                    if (row_on) {
-                        if (key) dwk[j] += g[j] * x[j];
-                        else dwq[j] += g[j] * x[j];
-                    }
-                    g[j] *= key ? wk[j] : wq[j];
-                    dot += g[j] * x[j];
+                for (int j = 0; j < 4; ++j) {  // rows that are not there hold zeros and add none
+                    x[j] = __fmul2_rn(x[j], both(n));
+                    dw[j] = __ffma2_rn(g[j], x[j], dw[j]);
+                    g[j] = __ffma2_rn(x[j], both(back), __fmul2_rn(gw[j], both(n)));
                 }
-                dot = group_sum<G>(dot) * inv_d;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = r * (g[j] - x[j] * dot);
             }
-            if (row_on) {
-                T* y = key ? (T*)p.yk + b * p.yk_sb + t * p.yk_st + hh * p.yk_sh
-                           : (T*)p.yq + b * p.yq_sb + t * p.yq_st + hh * p.yq_sh;
-                store8<!HALVES>(y, l.e1, l.e2, g);
-            }
+            if (i < heads) store8<RUN, PAIRS>(y, l.e1, l.e2, g);
+            y += a.y_h;
         }
     }
-    if (!p.part) return;
-#pragma unroll 1
-    for (int m = 0; m < 2; ++m) {
-        __syncthreads();
+    if (!a.part) return;
+    float* red = reinterpret_cast<float*>(&ring[0][0][0]);
+    static_assert(sizeof(ring) >= kThreads * 8 * sizeof(float), "a thread's eight sums fit the ring");
+    copies_wait<0>();
+    __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (l.on) red[grp * G * 8 + (j < 4 ? l.e1 + j : l.e2 + j - 4)] = m ? dwk[j] : dwq[j];
-        __syncthreads();
-        for (int e = threadIdx.x; e < p.d; e += kThreads) {
-            float sum = 0.f;
-            for (int i = 0; i < kGroups; ++i) sum += red[i * G * 8 + e];
-            p.part[((size_t)blockIdx.x * 2 + m) * p.d + e] = sum;
-        }
+    for (int j = 0; j < 8; ++j) {
+        const int e = entry8<PAIRS>(j >> 1, j & 1);
+        if (l.on) red[grp * kSlot + (e < 4 ? l.e1 + e : l.e2 + e - 4)] = j & 1 ? dw[j >> 1].y : dw[j >> 1].x;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.d; e += kThreads) {
+        float sum = 0.f;
+        for (int i = 0; i < kGroups; ++i) sum += red[i * kSlot + e];
+        a.part[(size_t)cta * p.d + e] = sum;
     }
 }
 
-// Heads a group walks: all of them (its angles are then computed once a token)
+constexpr int kBwdPerSm = 4;
+
+// Heads a group walks: all of a side's (its angles are then computed once a token)
 // while that leaves the card full of groups, fewer for short calls.
-int head_block(const QkRotateArgs& a) {
-    const long long threads = (long long)a.B * a.T * group_lanes(a.d), full = sm_count() * 1024LL;
-    const int heads = a.Hq + a.Hk;
+int head_block(const QkRotateArgs& a, int heads) {
+    const long long threads = (long long)a.B * a.T * group_lanes(a.d), full = sm_count() * 256LL;
     int hb = heads;
     while (hb > 1 && threads * ((heads + hb - 1) / hb) < full) hb = (hb + 1) / 2;
     return hb;
 }
 
-// CTAs of the backward kernel: a few per SM, each leaving one row of partial sums.
-int bwd_ctas(const QkRotateArgs& a) {
-    const int groups = kThreads / group_lanes(a.d), hb = head_block(a);
-    const long long items = (long long)a.B * a.T * ((a.Hq + a.Hk + hb - 1) / hb);
-    return (int)std::min<long long>((items + groups - 1) / groups, sm_count() * 4LL);
+// One side's share of the groups and CTAs.  Backward, a few CTAs per SM stay and walk
+// the items, each leaving one row of partial sums.
+void plan_side(Side* s, const QkRotateArgs& a, bool key, bool bwd) {
+    const int groups = kThreads / group_lanes(a.d);
+    s->H = key ? a.Hk : a.Hq;
+    s->hb = head_block(a, s->H);
+    s->nhb = (s->H + s->hb - 1) / s->hb;
+    s->items = (unsigned)((long long)a.B * a.T * s->nhb);
+    s->ctas = (s->items + groups - 1) / groups;
+    if (bwd) {
+        const long long most = (long long)sm_count() * kBwdPerSm * s->H / (a.Hq + a.Hk);
+        s->ctas = std::min(s->ctas, (unsigned)std::max(1ll, most));
+    }
 }
 
-QkParams params(const QkRotateArgs& a) {
+QkParams params(const QkRotateArgs& a, bool bwd) {
     QkParams p;
-    p.q = a.q; p.k = a.k; p.gq = a.dq_out; p.gk = a.dk_out;
-    p.yq = a.yq; p.yk = a.yk;
-    p.wq = a.q_weight; p.wk = a.k_weight;
-    p.part = nullptr;
-    p.q_sb = a.q_strides[0]; p.q_st = a.q_strides[1]; p.q_sh = a.q_strides[2];
-    p.k_sb = a.k_strides[0]; p.k_st = a.k_strides[1]; p.k_sh = a.k_strides[2];
-    p.yq_sb = a.yq_strides[0]; p.yq_st = a.yq_strides[1]; p.yq_sh = a.yq_strides[2];
-    p.yk_sb = a.yk_strides[0]; p.yk_st = a.yk_strides[1]; p.yk_sh = a.yk_strides[2];
+    for (int key = 0; key < 2; ++key) {
+        Side& s = p.side[key];
+        const long long *xs = key ? a.k_strides : a.q_strides, *ys = key ? a.yk_strides : a.yq_strides;
+        s.x = key ? a.k : a.q;
+        s.g = key ? a.dk_out : a.dq_out;
+        s.y = key ? a.yk : a.yq;
+        s.w = key ? a.k_weight : a.q_weight;
+        s.part = nullptr;
+        s.x_b = xs[0]; s.x_t = xs[1]; s.x_h = xs[2];
+        s.y_b = ys[0]; s.y_t = ys[1]; s.y_h = ys[2];
+        s.scale = key ? a.k_scale : a.q_scale;
+        plan_side(&s, a, key, bwd);
+    }
+    // with few heads the angles are the larger part: one group then takes both sides
+    p.both = !bwd && p.side[0].nhb == 1 && p.side[1].nhb == 1;
+    if (p.both) p.side[1].ctas = 0;
     p.positions = a.positions; p.pos0 = a.pos0;
-    p.B = a.B; p.T = a.T; p.Hq = a.Hq; p.Hk = a.Hk; p.d = a.d; p.rot = a.rot; p.norm = a.norm;
-    p.eps = a.eps; p.q_scale = a.q_scale; p.k_scale = a.k_scale;
-    p.hb = head_block(a);
-    p.nhb = (a.Hq + a.Hk + p.hb - 1) / p.hb;
-    p.items = (unsigned)((long long)a.B * a.T * p.nhb);
-    for (int i = 0; i < 128; ++i) p.freq[i] = 0;
+    p.tokens = Divide::by(a.T);
+    p.d = a.d; p.rot = a.rot; p.norm = a.norm;
+    p.eps = a.eps;
+    for (int i = 0; i < 128; ++i) p.freq[i] = make_uint2(0, 0);
     for (int i = 0; i < a.rot / 2; ++i) {
         // the fraction of a turn per position, in [0, 1): whole turns change nothing
         double turns = a.inv_freq[i] * 0.15915494309189533577;
         turns -= std::floor(turns);
-        p.freq[i] = turns >= 1.0 ? 0ull : (unsigned long long)std::ldexp(turns, 64);
+        const unsigned long long F = turns >= 1.0 ? 0ull : (unsigned long long)std::ldexp(turns, 64);
+        p.freq[i] = make_uint2((unsigned)F, (unsigned)(F >> 32));
     }
     return p;
 }
@@ -330,12 +392,15 @@ void launch(const QkParams& p, bool halves, bool bwd, unsigned grid, cudaStream_
 }  // namespace
 
 size_t qk_rotate_bwd_workspace_bytes(const QkRotateArgs& a) {
-    return (size_t)bwd_ctas(a) * 2 * a.d * sizeof(float);
+    Side q, k;
+    plan_side(&q, a, false, true);
+    plan_side(&k, a, true, true);
+    return ((size_t)q.ctas + k.ctas) * a.d * sizeof(float);
 }
 
 cudaError_t launch_qk_rotate_fwd(const QkRotateArgs& a, cudaStream_t s) {
-    const QkParams p = params(a);
-    const unsigned groups = kThreads / group_lanes(a.d), grid = (p.items + groups - 1) / groups;
+    const QkParams p = params(a, false);
+    const unsigned grid = p.side[0].ctas + p.side[1].ctas;
     TraceScope trace("qk_rotate_fwd_kernel", s);
     if (a.bf16) launch<__nv_bfloat16>(p, a.halves, false, grid, s);
     else launch<float>(p, a.halves, false, grid, s);
@@ -343,18 +408,20 @@ cudaError_t launch_qk_rotate_fwd(const QkRotateArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_qk_rotate_bwd(const QkRotateArgs& a, cudaStream_t s) {
-    QkParams p = params(a);
-    const int grid = bwd_ctas(a);
-    const bool sums = a.dq_weight || a.dk_weight;
-    p.part = sums ? (float*)a.workspace : nullptr;
+    QkParams p = params(a, true);
+    const unsigned grid = p.side[0].ctas + p.side[1].ctas;
+    float* part = (float*)a.workspace;
+    if (a.dq_weight) p.side[0].part = part;
+    if (a.dk_weight) p.side[1].part = part + (size_t)p.side[0].ctas * a.d;
     {
         TraceScope trace("qk_rotate_bwd_kernel", s);
-        if (a.bf16) launch<__nv_bfloat16>(p, a.halves, true, (unsigned)grid, s);
-        else launch<float>(p, a.halves, true, (unsigned)grid, s);
+        if (a.bf16) launch<__nv_bfloat16>(p, a.halves, true, grid, s);
+        else launch<float>(p, a.halves, true, grid, s);
     }
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !sums) return e;
-    return launch_partial_sum(p.part, grid, a.dq_weight, a.d, a.dk_weight, a.d, s);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !(a.dq_weight || a.dk_weight)) return e;
+    return launch_partial_sum(p.side[0].part, (int)p.side[0].ctas, a.dq_weight, p.side[1].part,
+                              (int)p.side[1].ctas, a.dk_weight, a.d, s);
 }
 
 }  // namespace la

@@ -3,26 +3,35 @@
 // order of the additions is fixed by the launch shape, so results repeat bit for
 // bit (no atomics).
 #include "rows.cuh"
+#include "tc_ptx.cuh"
 #include "trace.h"
 
 namespace la {
 
 namespace {
 
-constexpr int kSumWarps = 16;
+constexpr int kSumWarps = 32;
 
-// One CTA per 32 columns; warp w adds rows w, w + 16, ... of its lane's column.
-__global__ void __launch_bounds__(kSumWarps * 32) partial_sum_kernel(const float* __restrict__ part,
-                                                                     int rows, float* out0,
-                                                                     int cols0, float* out1,
+struct Sums {
+    const float* part[2];
+    float* out[2];
+    int rows[2];
+};
+
+// One CTA per 32 columns; warp w adds rows w, w + 32, ... of its lane's column.
+__global__ void __launch_bounds__(kSumWarps * 32) partial_sum_kernel(const __grid_constant__ Sums s,
                                                                      int cols) {
     __shared__ float red[kSumWarps][32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, which = blockIdx.y;
     const int c = blockIdx.x * 32 + lane;
+    const float* part = s.part[which];
+    float* out = s.out[which];
+    tc::griddep_wait();  // the rows come from the previous kernel in the stream
+    if (!out) return;
     float acc = 0.f;
     if (c < cols) {
-#pragma unroll 8
-        for (int r = w; r < rows; r += kSumWarps) acc += part[(size_t)r * cols + c];
+#pragma unroll 16
+        for (int r = w; r < s.rows[which]; r += kSumWarps) acc += part[(size_t)r * cols + c];
     }
     red[w][lane] = acc;
     __syncthreads();
@@ -30,23 +39,26 @@ __global__ void __launch_bounds__(kSumWarps * 32) partial_sum_kernel(const float
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < kSumWarps; ++i) sum += red[i][lane];
-        if (c < cols0) {
-            if (out0) out0[c] = sum;
-        } else if (out1) {
-            out1[c - cols0] = sum;
-        }
+        out[c] = sum;
     }
 }
 
 }  // namespace
 
-cudaError_t launch_partial_sum(const float* part, int rows, float* out0, int cols0, float* out1,
-                               int cols1, cudaStream_t s) {
-    const int cols = cols0 + cols1;
+cudaError_t launch_partial_sum(const float* part0, int rows0, float* out0, const float* part1, int rows1,
+                               float* out1, int cols, cudaStream_t s) {
+    const Sums sums = {{part0, part1}, {out0, out1}, {rows0, rows1}};
     TraceScope trace("partial_sum_kernel", s);
-    partial_sum_kernel<<<(cols + 31) / 32, kSumWarps * 32, 0, s>>>(part, rows, out0, cols0, out1,
-                                                                   cols);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];  // scheduled while the kernel before it finishes
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((cols + 31) / 32, out1 ? 2 : 1);
+    cfg.blockDim = dim3(kSumWarps * 32);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, partial_sum_kernel, sums, cols);
 }
 
 int sm_count() {

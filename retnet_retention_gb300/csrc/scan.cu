@@ -116,19 +116,6 @@ __device__ __forceinline__ float after(float A, float b, float s) {
     return A == 0.f ? b : fmaf(A, s, b);
 }
 
-// 16 bytes from global to shared memory, or 16 zero bytes.
-__device__ __forceinline__ void copy16(void* to, const void* from, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                     smem_addr(to)),
-                 "l"(from), "r"(valid ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // V neighbouring entries of a row in shared memory, as fp32.
 template <int V>
 __device__ __forceinline__ void row_floats(const float* p, float (&v)[V]) {
