@@ -149,11 +149,11 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&v)[V])
 }
 
 // One kernel's shape: V channels a lane (a tile has C = 32 V), R rows a thread and
-// round, W warps, S rounds of rows in the ring.
-template <typename T, int V_, int R_, int W_, int S_, bool BWD_>
+// round, W warps, S rounds of rows in the ring, CTAS on an SM.
+template <typename T, int V_, int R_, int W_, int S_, int CTAS_, bool BWD_>
 struct Shape {
     using Elem = T;
-    static constexpr int V = V_, R = R_, W = W_, S = S_, C = 32 * V_;
+    static constexpr int V = V_, R = R_, W = W_, S = S_, kCtas = CTAS_, C = 32 * V_;
     static constexpr bool BWD = BWD_;
     static constexpr int kRun = W * R;  // rows a CTA takes a round
     static constexpr size_t kLog = (size_t)kRun * C * sizeof(float);
@@ -167,7 +167,7 @@ struct Shape {
 // last token to the first.  A warp copies the rows it works on itself, a ring of S
 // rounds ahead, so that the ring needs no barrier beyond the warp's own.
 template <typename K>
-__global__ void __launch_bounds__(K::W * 32, K::W > 8 ? 1 : 2) scan_kernel(const __grid_constant__ ScanParams p) {
+__global__ void __launch_bounds__(K::W * 32, K::kCtas) scan_kernel(const __grid_constant__ ScanParams p) {
     using T = typename K::Elem;
     constexpr int V = K::V, R = K::R, W = K::W, S = K::S, C = K::C;
     constexpr bool BWD = K::BWD;
@@ -438,7 +438,9 @@ cudaError_t launch(const ScanParams& p, int B, int cluster, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, scan_kernel<K>, p);
 }
 
-// CTAs of a cluster until the card is full or a CTA has a single round.
+// CTAs of a cluster until the card is full or a CTA has a single round.  With a wave
+// and a bit of CTAs a long walk is cut in four all the same: the last ones then leave
+// less of the card idle (8 x 8192 x 4096: 328 us, uncut 346).
 template <typename K>
 cudaError_t plan(ScanParams p, int B, cudaStream_t s) {
     p.tiles = (p.D + K::C - 1) / K::C;
@@ -448,12 +450,31 @@ cudaError_t plan(ScanParams p, int B, cudaStream_t s) {
     int cluster = 1;
     while (cluster < kMaxCluster && units * cluster * 2 <= want && (long long)cluster * K::kRun < p.T)
         cluster *= 2;
+    const long long wave = (long long)sm_count() * K::kCtas;
+    if (units > wave && units < 4 * wave && p.T >= 16 * K::kRun) cluster = 4;
     return launch<K>(p, B, cluster, s);
 }
 
+// The shape, by the channel tiles there are (us, one GB300, bf16):
+//   fewer tiles of 32 channels than SMs, so that the walk waits for its rounds: eight
+//     warps of long rows (1 x 65536 x 1024: 115; four warps 117, rows of 16 126);
+//   more: four warps and four CTAs an SM, out of step with each other
+//     (4 x 4096 x 2048: 50; eight warps 55);
+//   backward rows of 16 (three tensors' rows in registers), and where tiles of 64
+//     channels nearly cover the SMs, two channels a lane in bf16 (4 x 4096 x 2048: 80;
+//     one channel 85).
 template <typename T, bool BWD>
 cudaError_t launch(const ScanParams& p, int B, cudaStream_t s) {
-    return plan<Shape<T, 1, 16, 8, 2, BWD>>(p, B, s);
+    const long long sms = sm_count(), tiles = (p.D + 31ll) / 32 * B, wide_tiles = (p.D + 63ll) / 64 * B;
+    if constexpr (BWD) {
+        if constexpr (sizeof(T) == 2)
+            if (wide_tiles * 5 >= sms * 4) return plan<Shape<T, 2, 16, 4, 2, 2, true>>(p, B, s);
+        return plan<Shape<T, 1, 16, 8, 2, 2, true>>(p, B, s);
+    } else {
+        constexpr int R = 64 / (int)sizeof(T);
+        if (tiles < sms) return plan<Shape<T, 1, R, 8, 2, 2, false>>(p, B, s);
+        return plan<Shape<T, 1, R, 4, 2, 4, false>>(p, B, s);
+    }
 }
 
 }  // namespace

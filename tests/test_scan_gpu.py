@@ -37,6 +37,9 @@ CASES = [
     (37, 300, 1024, "bf16", False, True),
     (2, 2049, 192, "f32", True, False),
     (130, 5, 4096, "f32", True, False),
+    (160, 130, 48, "bf16", True, True),
+    (170, 65, 80, "f32", True, True),
+    (3, 700, 3088, "bf16", True, True),
 ]
 
 
