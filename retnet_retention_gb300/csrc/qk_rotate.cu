@@ -153,48 +153,59 @@ __global__ void __launch_bounds__(kThreads) qk_rotate_fwd_kernel(const __grid_co
     __shared__ uint2 freq[128];
     for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) freq[i] = p.freq[i];
     __syncthreads();
-    // a CTA's groups take items of one side, or (both) a token's q and k in turn
-    const int first = blockIdx.x >= p.side[0].ctas, last = p.both ? 1 : first;
-    const unsigned cta = first ? blockIdx.x - p.side[0].ctas : blockIdx.x;
+    // a CTA's groups take items of one side, or (both) a token's heads of q, then of k
+    const int side = blockIdx.x >= p.side[0].ctas;
+    const unsigned cta = side ? blockIdx.x - p.side[0].ctas : blockIdx.x;
     const int lane = threadIdx.x % G;
     const Lane<HALVES> l(lane, p.d, p.rot);
     const float inv_d = 1.f / (float)p.d;
-    float2 c[2], s[2];
-    for (int side = first; side <= last; ++side) {
-        const Side& a = p.side[side];
-        const Place at(p, a, cta * (kThreads / G) + threadIdx.x / G);
-        const int heads = l.on ? at.heads : 0;
-        const T* x_row = (const T*)a.x + at.b * a.x_b + at.t * a.x_t + at.h0 * a.x_h;
-        T* y_row = (T*)a.y + (((long long)at.b * a.H + at.h0) * p.tokens.T + at.t) * p.d;
-        const long long y_h = (long long)p.tokens.T * p.d;
+    const Side& a = p.side[side];
+    const Side& k = p.side[1];
+    const int split = p.both ? a.H : a.hb, rows = split + (p.both ? k.H : 0);  // the same for every group
+    const long long y_h = (long long)p.tokens.T * p.d;
+    for (unsigned base = cta * (kThreads / G); base < a.items; base += a.ctas * (kThreads / G)) {
+        const Place at(p, a, base + threadIdx.x / G);
+        const int there = !l.on || at.heads == 0 ? 0 : p.both ? rows : at.heads;
+        const T* a_row = (const T*)a.x + at.b * a.x_b + at.t * a.x_t + at.h0 * a.x_h;
+        const T* k_row = (const T*)k.x + at.b * k.x_b + at.t * k.x_t;
+        T* y_row = (T*)a.y + ((long long)at.b * a.H + at.h0) * y_h + (long long)at.t * p.d;
         Raw8<T> raw[kFwdRows];
         auto fetch = [&](int i) {
 #pragma unroll
             for (int u = 0; u < kFwdRows; ++u) {
                 raw[u].a = {};
                 raw[u].b = {};
-                if (i + u < heads) raw[u] = raw8<RUN>(x_row + (i + u) * a.x_h, l.e1, l.e2);
+                const int h = i + u;
+                if (h < there)
+                    raw[u] = raw8<RUN>(h < split ? a_row + h * a.x_h : k_row + (h - split) * k.x_h, l.e1, l.e2);
             }
         };
         fetch(0);  // before the angles: their arithmetic covers the first loads
-        float2 w[4];
+        float2 w[4], c[2], s[2];
         row_weights<PAIRS>(a.w, l.on, l.e1, l.e2, w);
-        if (side == first)
-            l.angles(freq, lane,
-                     p.positions ? __ldg(p.positions + (long long)at.b * p.tokens.T + at.t) : p.pos0 + at.t, c, s);
-        for (int i = 0; i < a.hb; i += kFwdRows) {  // the same for every group, dead ones too
+        float scale = a.scale;
+        l.angles(freq, lane,
+                 p.positions ? __ldg(p.positions + (long long)at.b * p.tokens.T + at.t) : p.pos0 + at.t, c, s);
+        for (int i = 0; i < rows; i += kFwdRows) {
             if (i > 0) fetch(i);
 #pragma unroll
             for (int u = 0; u < kFwdRows; ++u) {
-                if (i + u >= a.hb) break;
+                const int h = i + u;
+                if (h >= rows) break;
+                if (h == split) {  // on to the keys
+                    row_weights<PAIRS>(k.w, l.on, l.e1, l.e2, w);
+                    scale = k.scale;
+                    y_row = (T*)k.y + (long long)at.b * k.H * y_h + (long long)at.t * p.d;
+                }
                 float2 x[4];
                 floats8<PAIRS>(raw[u], x);
-                float f = a.scale;
+                float f = scale;
                 if (p.norm) f *= rsqrtf(group_sum<G>(dot8(x, x)) * inv_d + p.eps);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], __fmul2_rn(w[j], both(f)));
                 Lane<HALVES>::rotate(x, c, s);
-                if (i + u < heads) store8<RUN, PAIRS>(y_row + (i + u) * y_h, l.e1, l.e2, x);
+                if (h < there) store8<RUN, PAIRS>(y_row, l.e1, l.e2, x);
+                y_row += y_h;
             }
         }
     }
@@ -308,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_rotate_bwd_kernel(const __grid
     }
 }
 
-constexpr int kBwdPerSm = 4;
+constexpr int kFwdPerSm = 32, kBwdPerSm = 4;
 
 // Heads a group walks: all of a side's (its angles are then computed once a token)
 // while that leaves the card full of groups, fewer for short calls.
@@ -328,10 +339,8 @@ void plan_side(Side* s, const QkRotateArgs& a, bool key, bool bwd) {
     s->nhb = (s->H + s->hb - 1) / s->hb;
     s->items = (unsigned)((long long)a.B * a.T * s->nhb);
     s->ctas = (s->items + groups - 1) / groups;
-    if (bwd) {
-        const long long most = (long long)sm_count() * kBwdPerSm * s->H / (a.Hq + a.Hk);
-        s->ctas = std::min(s->ctas, (unsigned)std::max(1ll, most));
-    }
+    const long long most = (long long)sm_count() * (bwd ? kBwdPerSm : kFwdPerSm) * s->H / (a.Hq + a.Hk);
+    s->ctas = std::min(s->ctas, (unsigned)std::max(1ll, most));
 }
 
 QkParams params(const QkRotateArgs& a, bool bwd) {
@@ -351,7 +360,10 @@ QkParams params(const QkRotateArgs& a, bool bwd) {
     }
     // with few heads the angles are the larger part: one group then takes both sides
     p.both = !bwd && p.side[0].nhb == 1 && p.side[1].nhb == 1;
-    if (p.both) p.side[1].ctas = 0;
+    if (p.both) {
+        p.side[0].ctas += p.side[1].ctas;
+        p.side[1].ctas = 0;
+    }
     p.positions = a.positions; p.pos0 = a.pos0;
     p.tokens = Divide::by(a.T);
     p.d = a.d; p.rot = a.rot; p.norm = a.norm;
