@@ -26,21 +26,49 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kRingBytes = 8;  // rows of the ring: kRingBytes / sizeof(T)
 
+// One tensor's addresses, in elements: head h's rows start at h_stride h, a walk's
+// next token lies `step` further, and `wrap` more where that is past the sequence's end.
+struct Rows {
+    const void* p;
+    long long b, t, h;  // strides
+    long long step, wrap;
+};
+
 struct GateParams {
-    const void *o, *gate, *dy;
-    void *y, *d_o, *d_gate;
+    Rows o, gate, dy, y, d_o, d_gate;  // gate.p may be null
     const float* w;
-    float* part;  // [tokens' blocks][H][d] or null
-    long long o_b, o_h, o_t, g_b, g_t, g_h, dy_b, dy_t, dy_h;
-    long long y_b, y_t, y_h, do_b, do_h, do_t, dg_b, dg_t, dg_h;
+    float* part;         // [tokens' blocks][H][d] or null
     Divide by_T;
-    unsigned tokens;  // B T
+    unsigned tokens;     // B T
+    unsigned leap_t;     // tokens from one to the walk's next, modulo T
     int H, d, center;
     float eps;
 };
 
-// sigma(g) to a few ulp: e^-g may overflow to infinity, whose reciprocal is 0.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + expf(-g)); }
+// A place in one tensor that walks with the tokens.
+template <typename T>
+struct Cursor {
+    T* at;
+
+    __device__ __forceinline__ Cursor(const Rows& r, int h, unsigned b, unsigned t)
+        : at((T*)r.p + h * r.h + b * r.b + t * r.t) {}
+    __device__ __forceinline__ void next(const Rows& r, bool wrapped) {
+        at += r.step;
+        if (wrapped) at += r.wrap;
+    }
+};
+
+// sigma(g) = 1 / (1 + e^-g); e^-g may overflow to infinity, whose reciprocal is 0.  For
+// bf16 results e^-g is one 2^x of the scaled argument, off by (2 + 1.2 |g|) ulp of
+// fp32: below 2^-16 wherever sigma is not 0, against their 2^-9.  For fp32 it is expf.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, s;
+    if (sizeof(T) == 2) e = __expf(-g);
+    else e = expf(-g);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));  // 1 ulp
+    return s;
+}
 
 // x <- its normed row, returns r.  Lanes past the row hold zeros and keep them.
 template <int G>
@@ -60,32 +88,38 @@ __device__ __forceinline__ float norm_row(float2 (&x)[4], bool on, int center, f
 
 // Grid: (heads, blocks of tokens).
 template <typename T, int G, bool BWD>
-__global__ void __launch_bounds__(kThreads, 6) head_gate_kernel(const __grid_constant__ GateParams p) {
+__global__ void __launch_bounds__(kThreads, BWD ? 5 : 6) head_gate_kernel(const __grid_constant__ GateParams p) {
     constexpr int kGroups = kThreads / G, kRing = kRingBytes / (int)sizeof(T), kSlot = 8 * G;
     __shared__ __align__(16) T ring[kRing][BWD ? 3 : 2][kGroups * kSlot];  // o, gate, dy
     if (BWD) tc::griddep_launch_dependents();  // the sums' kernel may be scheduled (it waits itself)
     const int lane = threadIdx.x % G, grp = threadIdx.x / G, e = lane * 8, h = blockIdx.x;
     const bool on = e < p.d;
     const float inv_d = 1.f / (float)p.d;
-    const T* o = (const T*)p.o + h * p.o_h;
-    const T* gate = p.gate ? (const T*)p.gate + h * p.g_h : nullptr;
-    const T* dy = BWD ? (const T*)p.dy + h * p.dy_h : nullptr;
-    const unsigned leap = gridDim.y * kGroups;
+    const bool gated = p.gate.p != nullptr;
+    const unsigned leap = gridDim.y * kGroups, first = blockIdx.y * kGroups + grp;
+    unsigned b0, t0;
+    p.by_T(first, &b0, &t0);
 
-    unsigned f_base = blockIdx.y * kGroups;
+    Cursor<const T> o(p.o, h, b0, t0), gate(p.gate, h, b0, t0), dy(p.dy, h, b0, t0);
+    unsigned f_m = first, f_t = t0;
     int f_slot = 0;
     auto fetch = [&]() {
-        if (f_base < p.tokens) {
-            const bool there = f_base + grp < p.tokens;
-            unsigned b, t;
-            p.by_T(there ? f_base + grp : 0, &b, &t);
-            copy_row<T, G>(&ring[f_slot][0][grp * kSlot], o + b * p.o_b + t * p.o_t, lane, p.d, there);
-            if (gate)
-                copy_row<T, G>(&ring[f_slot][1][grp * kSlot], gate + b * p.g_b + t * p.g_t, lane, p.d, there);
-            if (BWD)
-                copy_row<T, G>(&ring[f_slot][BWD ? 2 : 0][grp * kSlot], dy + b * p.dy_b + t * p.dy_t, lane, p.d,
+        if (f_m - grp < p.tokens) {  // the same for every group
+            const bool there = f_m < p.tokens;
+            copy_row<T, G>(&ring[f_slot][0][grp * kSlot], there ? o.at : (const T*)p.o.p, lane, p.d, there);
+            if (gated)
+                copy_row<T, G>(&ring[f_slot][1][grp * kSlot], there ? gate.at : (const T*)p.gate.p, lane, p.d,
                                there);
-            f_base += leap;
+            if (BWD)
+                copy_row<T, G>(&ring[f_slot][BWD ? 2 : 0][grp * kSlot], there ? dy.at : (const T*)p.dy.p, lane,
+                               p.d, there);
+            f_m += leap;
+            f_t += p.leap_t;
+            const bool wrapped = f_t >= p.by_T.T;
+            if (wrapped) f_t -= p.by_T.T;
+            o.next(p.o, wrapped);
+            gate.next(p.gate, wrapped);
+            if (BWD) dy.next(p.dy, wrapped);
         }
         copies_commit();
         f_slot = f_slot + 1 == kRing ? 0 : f_slot + 1;
@@ -97,36 +131,35 @@ __global__ void __launch_bounds__(kThreads, 6) head_gate_kernel(const __grid_con
     row_weights<false>(p.w ? p.w + (size_t)h * p.d : nullptr, on, e, e + 4, w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[j] = make_float2(0.f, 0.f);
+    Cursor<T> y(BWD ? p.d_o : p.y, h, b0, t0), d_gate(p.d_gate, h, b0, t0);
+    unsigned t = t0;
     int slot = 0;
-    for (unsigned base = blockIdx.y * kGroups; base < p.tokens; base += leap) {
-        const bool row_on = on && base + grp < p.tokens;
+    for (unsigned m = first; m - grp < p.tokens; m += leap) {
+        const bool row_on = on && m < p.tokens;
         copies_wait<kRing - 1>();
         __syncwarp();
         float2 n[4], g[4], du[4];
         floats8<false>(raw8<true>(&ring[slot][0][grp * kSlot], e, e + 4), n);
-        if (gate) floats8<false>(raw8<true>(&ring[slot][1][grp * kSlot], e, e + 4), g);
+        if (gated) floats8<false>(raw8<true>(&ring[slot][1][grp * kSlot], e, e + 4), g);
         if (BWD) floats8<false>(raw8<true>(&ring[slot][BWD ? 2 : 0][grp * kSlot], e, e + 4), du);
         __syncwarp();
         fetch();
         slot = slot + 1 == kRing ? 0 : slot + 1;
-        unsigned b, t;
-        p.by_T(base + grp, &b, &t);
         const float r = norm_row<G>(n, on, p.center, inv_d, p.eps);
         if (!BWD) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) n[j] = __fmul2_rn(n[j], w[j]);
-            if (gate) {
+            if (gated) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    n[j] = __fmul2_rn(n[j], __fmul2_rn(g[j], make_float2(sigmoid(g[j].x), sigmoid(g[j].y))));
+                    n[j] = __fmul2_rn(n[j], __fmul2_rn(g[j], make_float2(sigmoid<T>(g[j].x), sigmoid<T>(g[j].y))));
             }
-            if (row_on)
-                store8<true, false>((T*)p.y + h * p.y_h + b * p.y_b + t * p.y_t, e, e + 4, n);
+            if (row_on) store8<true, false>(y.at, e, e + 4, n);
         } else {
-            if (gate) {
+            if (gated) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 sg = make_float2(sigmoid(g[j].x), sigmoid(g[j].y));
+                    const float2 sg = make_float2(sigmoid<T>(g[j].x), sigmoid<T>(g[j].y));
                     // slope: sigma (1 + g (1 - sigma))
                     const float2 slope = __fmul2_rn(
                         sg, __ffma2_rn(g[j], __fadd2_rn(both(1.f), make_float2(-sg.x, -sg.y)), both(1.f)));
@@ -134,8 +167,7 @@ __global__ void __launch_bounds__(kThreads, 6) head_gate_kernel(const __grid_con
                     g[j] = __fmul2_rn(__fmul2_rn(du[j], __fmul2_rn(n[j], w[j])), slope);
                     du[j] = __fmul2_rn(du[j], act);
                 }
-                if (row_on)
-                    store8<true, false>((T*)p.d_gate + h * p.dg_h + b * p.dg_b + t * p.dg_t, e, e + 4, g);
+                if (row_on) store8<true, false>(d_gate.at, e, e + 4, g);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // rows that are not there hold zeros and add none
@@ -151,8 +183,13 @@ __global__ void __launch_bounds__(kThreads, 6) head_gate_kernel(const __grid_con
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 du[j] = __fmul2_rn(both(r), __ffma2_rn(n[j], both(along), __fadd2_rn(du[j], both(mean))));
-            if (row_on) store8<true, false>((T*)p.d_o + h * p.do_h + b * p.do_b + t * p.do_t, e, e + 4, du);
+            if (row_on) store8<true, false>(y.at, e, e + 4, du);
         }
+        t += p.leap_t;
+        const bool wrapped = t >= p.by_T.T;
+        if (wrapped) t -= p.by_T.T;
+        y.next(BWD ? p.d_o : p.y, wrapped);
+        if (BWD) d_gate.next(p.d_gate, wrapped);
     }
     if (!BWD || !p.part) return;
     float* red = reinterpret_cast<float*>(&ring[0][0][0]);
@@ -173,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 6) head_gate_kernel(const __grid_con
 
 // CTAs a head's tokens are shared out to: a few CTAs per SM in all; backward each
 // leaves one row of partial sums.
-constexpr int kFwdPerSm = 32, kBwdPerSm = 12;
+constexpr int kFwdPerSm = 48, kBwdPerSm = 10;
 
 unsigned token_blocks(const HeadGateArgs& a, bool bwd) {
     const long long groups = kThreads / group_lanes(a.d);
@@ -182,20 +219,26 @@ unsigned token_blocks(const HeadGateArgs& a, bool bwd) {
     return (unsigned)std::min(turns, std::min(most, 65535ll));
 }
 
-GateParams params(const HeadGateArgs& a) {
+GateParams params(const HeadGateArgs& a, unsigned blocks) {
+    const unsigned leap = blocks * (unsigned)(kThreads / group_lanes(a.d));
+    const long long leap_b = leap / (unsigned)a.T, leap_t = leap % (unsigned)a.T;
+    auto rows = [&](const void* p, long long b, long long t, long long h) {
+        return Rows{p, b, t, h, leap_b * b + leap_t * t, b - a.T * t};
+    };
+    auto heads_first = [&](const void* p, const long long* s) { return rows(p, s[0], s[2], s[1]); };
+    auto tokens_first = [&](const void* p, const long long* s) { return rows(p, s[0], s[1], s[2]); };
     GateParams p;
-    p.o = a.o; p.gate = a.gate; p.dy = a.dy;
-    p.y = a.y; p.d_o = a.d_o; p.d_gate = a.d_gate;
+    p.o = heads_first(a.o, a.o_strides);
+    p.gate = tokens_first(a.gate, a.gate_strides);
+    p.dy = tokens_first(a.dy, a.dy_strides);
+    p.y = tokens_first(a.y, a.y_strides);
+    p.d_o = heads_first(a.d_o, a.do_strides);
+    p.d_gate = tokens_first(a.d_gate, a.dgate_strides);
     p.w = a.weight;
     p.part = a.d_weight ? (float*)a.workspace : nullptr;
-    p.o_b = a.o_strides[0]; p.o_h = a.o_strides[1]; p.o_t = a.o_strides[2];
-    p.g_b = a.gate_strides[0]; p.g_t = a.gate_strides[1]; p.g_h = a.gate_strides[2];
-    p.dy_b = a.dy_strides[0]; p.dy_t = a.dy_strides[1]; p.dy_h = a.dy_strides[2];
-    p.y_b = a.y_strides[0]; p.y_t = a.y_strides[1]; p.y_h = a.y_strides[2];
-    p.do_b = a.do_strides[0]; p.do_h = a.do_strides[1]; p.do_t = a.do_strides[2];
-    p.dg_b = a.dgate_strides[0]; p.dg_t = a.dgate_strides[1]; p.dg_h = a.dgate_strides[2];
-    p.tokens = (unsigned)((long long)a.B * a.T);
     p.by_T = Divide::by(a.T);
+    p.tokens = (unsigned)((long long)a.B * a.T);
+    p.leap_t = (unsigned)leap_t;
     p.H = a.H; p.d = a.d; p.center = a.center;
     p.eps = a.eps;
     return p;
@@ -225,8 +268,8 @@ size_t head_gate_bwd_workspace_bytes(const HeadGateArgs& a) {
 }
 
 cudaError_t launch_head_gate_fwd(const HeadGateArgs& a, cudaStream_t s) {
-    const GateParams p = params(a);
     const dim3 grid(a.H, token_blocks(a, false));
+    const GateParams p = params(a, grid.y);
     TraceScope trace("head_gate_fwd_kernel", s);
     if (a.bf16) launch<__nv_bfloat16>(p, false, grid, s);
     else launch<float>(p, false, grid, s);
@@ -234,8 +277,8 @@ cudaError_t launch_head_gate_fwd(const HeadGateArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_head_gate_bwd(const HeadGateArgs& a, cudaStream_t s) {
-    const GateParams p = params(a);
     const dim3 grid(a.H, token_blocks(a, true));
+    const GateParams p = params(a, grid.y);
     {
         TraceScope trace("head_gate_bwd_kernel", s);
         if (a.bf16) launch<__nv_bfloat16>(p, true, grid, s);

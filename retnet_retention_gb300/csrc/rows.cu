@@ -26,12 +26,22 @@ __global__ void __launch_bounds__(kSumWarps * 32) partial_sum_kernel(const __gri
     const int c = blockIdx.x * 32 + lane;
     const float* part = s.part[which];
     float* out = s.out[which];
+    const int rows = s.rows[which];
     tc::griddep_wait();  // the rows come from the previous kernel in the stream
     if (!out) return;
     float acc = 0.f;
     if (c < cols) {
-#pragma unroll 16
-        for (int r = w; r < s.rows[which]; r += kSumWarps) acc += part[(size_t)r * cols + c];
+        constexpr int kBatch = 24;  // loads in flight together
+        for (int r0 = w; r0 < rows; r0 += kBatch * kSumWarps) {
+            float v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = r0 + i * kSumWarps;
+                v[i] = r < rows ? part[(size_t)r * cols + c] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) acc += v[i];
+        }
     }
     red[w][lane] = acc;
     __syncthreads();
