@@ -438,42 +438,49 @@ cudaError_t launch(const ScanParams& p, int B, int cluster, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, scan_kernel<K>, p);
 }
 
-// CTAs of a cluster until the card is full or a CTA has a single round.  With a wave
-// and a bit of CTAs a long walk is cut in four all the same: the last ones then leave
-// less of the card idle (8 x 8192 x 4096: 328 us, uncut 346).
+// CTAs of a cluster until the card is full (kCtas an SM, two at most: more only wait
+// for each other) or a CTA has a single round.  With a wave and a bit of CTAs a long
+// walk is cut in four all the same: the last ones then leave less of the card idle
+// (8 x 8192 x 4096: 328 us, uncut 346).
 template <typename K>
 cudaError_t plan(ScanParams p, int B, cudaStream_t s) {
     p.tiles = (p.D + K::C - 1) / K::C;
     p.mute = opt_force_timeout();
     p.limit_ns = p.mute ? 1000000ull : 2000000000ull;
-    const long long want = sm_count() * 2LL, units = (long long)B * p.tiles;
+    const long long sms = sm_count(), units = (long long)B * p.tiles, wave = sms * K::kCtas;
     int cluster = 1;
-    while (cluster < kMaxCluster && units * cluster * 2 <= want && (long long)cluster * K::kRun < p.T)
-        cluster *= 2;
-    const long long wave = (long long)sm_count() * K::kCtas;
-    if (units > wave && units < 4 * wave && p.T >= 16 * K::kRun) cluster = 4;
+    if (K::kCtas > 1) {
+        while (cluster < kMaxCluster && units * cluster * 2 <= sms * 2 && (long long)cluster * K::kRun < p.T)
+            cluster *= 2;
+        if (units > wave && units < 4 * wave && p.T >= 16 * K::kRun) cluster = 4;
+    }
     return launch<K>(p, B, cluster, s);
 }
 
-// The shape, by the channel tiles there are (us, one GB300, bf16):
-//   fewer tiles of 32 channels than SMs, so that the walk waits for its rounds: eight
-//     warps of long rows (1 x 65536 x 1024: 115; four warps 117, rows of 16 126);
-//   more: four warps and four CTAs an SM, out of step with each other
-//     (4 x 4096 x 2048: 50; eight warps 55);
-//   backward rows of 16 (three tensors' rows in registers), and where tiles of 64
-//     channels nearly cover the SMs, two channels a lane in bf16 (4 x 4096 x 2048: 80;
-//     one channel 85).
+// The shape, by the channel tiles there are (us, one GB300, bf16).
+//   Forward, fewer tiles of 32 channels than SMs, so that the walk waits for its rounds:
+//     long rows, six warps and two CTAs an SM where clusters can fill the card (1 x
+//     65536 x 1024: 105; eight warps 115, four warps 116, rows of 16 126), eight warps
+//     where they cannot (1 x 65536 x 64: 70; six 76, four 93).
+//   Forward, more tiles: four warps and four CTAs an SM, out of step with each other
+//     (4 x 4096 x 2048: 50; eight warps 55).
+//   Backward: rows of 16 (three tensors' rows in registers).  In bf16, where tiles of 64
+//     channels make a wave of one CTA an SM, or many, two channels a lane (4 x 4096 x
+//     2048: 76, 2 x 8192 x 4096: 141; one channel 85 and 160).
 template <typename T, bool BWD>
 cudaError_t launch(const ScanParams& p, int B, cudaStream_t s) {
     const long long sms = sm_count(), tiles = (p.D + 31ll) / 32 * B, wide_tiles = (p.D + 63ll) / 64 * B;
     if constexpr (BWD) {
         if constexpr (sizeof(T) == 2)
-            if (wide_tiles * 5 >= sms * 4) return plan<Shape<T, 2, 16, 4, 2, 2, true>>(p, B, s);
+            if ((wide_tiles * 5 >= sms * 4 && wide_tiles <= sms) || wide_tiles >= 4 * sms)
+                return plan<Shape<T, 2, 16, 8, 2, 1, true>>(p, B, s);
         return plan<Shape<T, 1, 16, 8, 2, 2, true>>(p, B, s);
     } else {
         constexpr int R = 64 / (int)sizeof(T);
-        if (tiles < sms) return plan<Shape<T, 1, R, 8, 2, 2, false>>(p, B, s);
-        return plan<Shape<T, 1, R, 4, 2, 4, false>>(p, B, s);
+        if (tiles >= sms) return plan<Shape<T, 1, R, 4, 2, 4, false>>(p, B, s);
+        if constexpr (sizeof(T) == 2)
+            if (tiles * kMaxCluster >= sms) return plan<Shape<T, 1, R, 6, 2, 2, false>>(p, B, s);
+        return plan<Shape<T, 1, R, 8, 2, 2, false>>(p, B, s);
     }
 }
 

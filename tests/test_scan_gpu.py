@@ -40,6 +40,9 @@ CASES = [
     (160, 130, 48, "bf16", True, True),
     (170, 65, 80, "f32", True, True),
     (3, 700, 3088, "bf16", True, True),
+    (2, 5000, 4080, "bf16", True, True),
+    (1, 4001, 720, "bf16", True, True),
+    (5, 2500, 8208, "bf16", False, False),
 ]
 
 
