@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kFwdRows = 4;    // rows (heads) whose loads are in flight together
-constexpr int kRingBytes = 16; // backward: the ring's rows are kRingBytes / sizeof(T)
+constexpr int kRingBytes = 8;  // backward: the ring's rows are kRingBytes / sizeof(T)
 
 // q or k.
 struct Side {
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) qk_rotate_fwd_kernel(const __grid_co
 
 // Backward: a CTA's groups walk items of one side; their rows come through the ring.
 template <typename T, int G, bool HALVES>
-__global__ void __launch_bounds__(kThreads, 4) qk_rotate_bwd_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kThreads, 5) qk_rotate_bwd_kernel(const __grid_constant__ QkParams p) {
     constexpr int kGroups = kThreads / G, kRing = kRingBytes / (int)sizeof(T), kSlot = 8 * G;
     constexpr bool RUN = !HALVES, PAIRS = !HALVES;
     __shared__ __align__(16) T ring[kRing][2][kGroups * kSlot];
@@ -263,11 +263,16 @@ __global__ void __launch_bounds__(kThreads, 4) qk_rotate_bwd_kernel(const __grid
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[j] = make_float2(0.f, 0.f);
     int slot = 0;
+    auto position = [&](unsigned base) {
+        const Place at(p, a, base + grp);
+        return p.positions ? __ldg(p.positions + (long long)at.b * p.tokens.T + at.t) : p.pos0 + at.t;
+    };
+    int pos = position(cta * kGroups);
     for (unsigned base = cta * kGroups; base < a.items; base += leap) {
         const Place at(p, a, base + grp);
         const int heads = l.on ? at.heads : 0;
-        l.angles(freq, lane, p.positions ? __ldg(p.positions + (long long)at.b * p.tokens.T + at.t) : p.pos0 + at.t,
-                 c, s);
+        l.angles(freq, lane, pos, c, s);
+        if (base + leap < a.items) pos = position(base + leap);  // an item ahead
 #pragma unroll
         for (int j = 0; j < 2; ++j) {  // back, and the scale with it
             c[j] = __fmul2_rn(c[j], both(a.scale));
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_rotate_bwd_kernel(const __grid
     }
 }
 
-constexpr int kFwdPerSm = 32, kBwdPerSm = 4;
+constexpr int kFwdPerSm = 32, kBwdPerSm = 5;
 
 // Heads a group walks: all of a side's (its angles are then computed once a token)
 // while that leaves the card full of groups, fewer for short calls.
@@ -339,8 +344,12 @@ void plan_side(Side* s, const QkRotateArgs& a, bool key, bool bwd) {
     s->nhb = (s->H + s->hb - 1) / s->hb;
     s->items = (unsigned)((long long)a.B * a.T * s->nhb);
     s->ctas = (s->items + groups - 1) / groups;
-    const long long most = (long long)sm_count() * (bwd ? kBwdPerSm : kFwdPerSm) * s->H / (a.Hq + a.Hk);
-    s->ctas = std::min(s->ctas, (unsigned)std::max(1ll, most));
+    // an item costs its heads' rows and, for its set-up and angles, about 1.5 rows more
+    const double rows = s->hb + 1.5, share = s->nhb * rows;
+    const int other = key ? a.Hq : a.Hk, other_hb = head_block(a, other);
+    const double rest = (double)((other + other_hb - 1) / other_hb) * (other_hb + 1.5);
+    const double most = sm_count() * (bwd ? kBwdPerSm : kFwdPerSm) * share / (share + rest);
+    s->ctas = std::min(s->ctas, (unsigned)std::max(1.0, most));
 }
 
 QkParams params(const QkRotateArgs& a, bool bwd) {

@@ -21,6 +21,7 @@
 // Bound by HBM: log_a 4, x 2, h 2 bytes an entry (bf16).  State, products and sums
 // are fp32; h is rounded where it is stored, never the state that is carried on.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "rows.cuh"
@@ -396,6 +397,70 @@ __global__ void __launch_bounds__(K::W * 32, K::kCtas) scan_kernel(const __grid_
     }
 }
 
+// Short walks over many channels: a thread takes two channels of a sequence from end to
+// end, eight rows' loads ahead, with no exchange between threads.
+template <typename T, bool BWD>
+__global__ void __launch_bounds__(128) scan_short_kernel(const __grid_constant__ ScanParams p, unsigned pairs) {
+    constexpr int R = 8;
+    const unsigned i = blockIdx.x * 128 + threadIdx.x;
+    if (i >= pairs) return;
+    const unsigned half = (unsigned)p.D / 2, b = i / half;
+    const long long c = (long long)b * p.D + 2 * (i - b * half);  // in [B][D]
+    const long long step = BWD ? -(long long)p.D : (long long)p.D;
+    const long long origin = c + (long long)b * (p.T - 1) * p.D + (BWD ? (p.T - 1ll) * p.D : 0);
+    const float* log_a = p.log_a + origin;
+    const T* x = (const T*)p.x + origin;
+    const T* h_in = (const T*)p.h_in + origin + step;  // a token earlier
+    T* y = (T*)p.y + origin;
+    float* dlog_a = p.dlog_a + origin;
+    float s[2] = {0.f, 0.f};
+    if (p.s0) row_floats<2>(p.s0 + c, s);
+    float h0[2] = {0.f, 0.f};
+    if (BWD && p.h0) row_floats<2>(p.h0 + c, h0);
+    struct Rows {
+        float a[R][2], v[R][2], h[BWD ? R : 1][2];
+    } now, next;
+    const int last = p.T - 1;
+    auto fetch = [&](Rows& r, int u0) {  // past the end the last row again: no branch holds a load back
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const long long at = min(u0 + k, last) * step;
+            row_floats<2>(log_a + at, r.a[k]);
+            row_floats<2>(x + at, r.v[k]);
+            if (BWD) row_floats<2>(h_in + min(u0 + k, last - 1) * step, r.h[BWD ? k : 0]);  // T = 1: token 0, unused
+        }
+    };
+    auto work = [&](const Rows& r, int u0) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (u0 + k > last) break;
+            float out[2], dla[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float a = expf(r.a[k][j]);
+                if (BWD) {
+                    const float h = u0 + k == last ? h0[j] : r.h[BWD ? k : 0][j];
+                    out[j] = r.v[k][j] + s[j];
+                    s[j] = a == 0.f ? 0.f : a * out[j];
+                    dla[j] = a == 0.f ? 0.f : s[j] * h;
+                } else {
+                    s[j] = out[j] = after(a, r.v[k][j], s[j]);
+                }
+            }
+            store_row<2>(y + (u0 + k) * step, out);
+            if (BWD) store_row<2>(dlog_a + (u0 + k) * step, dla);
+        }
+    };
+    fetch(now, 0);
+    for (int u0 = 0; u0 < p.T; u0 += 2 * R) {
+        fetch(next, u0 + R);
+        work(now, u0);
+        fetch(now, u0 + 2 * R);
+        work(next, u0 + R);
+    }
+    if (p.s_out) store_row<2>(p.s_out + c, s);
+}
+
 // h_out = a h_in + x, h = its rounding; four entries a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) scan_step_kernel(const T* __restrict__ x,
@@ -420,7 +485,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const T* __restrict__ x,
 }
 
 template <typename K>
-cudaError_t launch(const ScanParams& p, int B, int cluster, cudaStream_t s) {
+cudaError_t launch_kernel(const ScanParams& p, int B, int cluster, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(scan_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)K::kShared);
     if (e != cudaSuccess) return e;
@@ -435,53 +500,70 @@ cudaError_t launch(const ScanParams& p, int B, int cluster, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    TraceScope trace(K::BWD ? "scan_bwd_kernel" : "scan_kernel", s);
     return cudaLaunchKernelEx(&cfg, scan_kernel<K>, p);
 }
 
-// CTAs of a cluster until the card is full (kCtas an SM, two at most: more only wait
-// for each other) or a CTA has a single round.  With a wave and a bit of CTAs a long
-// walk is cut in four all the same: the last ones then leave less of the card idle
-// (8 x 8192 x 4096: 328 us, uncut 346).
 template <typename K>
-cudaError_t plan(ScanParams p, int B, cudaStream_t s) {
+cudaError_t launch(ScanParams p, int B, int cluster, cudaStream_t s) {
     p.tiles = (p.D + K::C - 1) / K::C;
     p.mute = opt_force_timeout();
     p.limit_ns = p.mute ? 1000000ull : 2000000000ull;
-    const long long sms = sm_count(), units = (long long)B * p.tiles, wave = sms * K::kCtas;
-    int cluster = 1;
-    if (K::kCtas > 1) {
-        while (cluster < kMaxCluster && units * cluster * 2 <= sms * 2 && (long long)cluster * K::kRun < p.T)
-            cluster *= 2;
-        if (units > wave && units < 4 * wave && p.T >= 16 * K::kRun) cluster = 4;
-    }
-    return launch<K>(p, B, cluster, s);
+    return launch_kernel<K>(p, B, cluster, s);
 }
 
-// The shape, by the channel tiles there are (us, one GB300, bf16).
-//   Forward, fewer tiles of 32 channels than SMs, so that the walk waits for its rounds:
-//     long rows, six warps and two CTAs an SM where clusters can fill the card (1 x
-//     65536 x 1024: 105; eight warps 115, four warps 116, rows of 16 126), eight warps
-//     where they cannot (1 x 65536 x 64: 70; six 76, four 93).
-//   Forward, more tiles: four warps and four CTAs an SM, out of step with each other
-//     (4 x 4096 x 2048: 50; eight warps 55).
-//   Backward: rows of 16 (three tensors' rows in registers).  In bf16, where tiles of 64
-//     channels make a wave of one CTA an SM, or many, two channels a lane (4 x 4096 x
-//     2048: 76, 2 x 8192 x 4096: 141; one channel 85 and 160).
+// How well `ctas` CTAs, four of which fit an SM, use the card: their spread over the
+// SMs, at least 1.6 an SM needed to keep the memory busy, less for the exchange in
+// clusters.  More waves spread themselves out, by and by.  Within 0.1 of the fractions of
+// the copy rate measured at 97 to 400 tiles of 8192 tokens.
+double card_use(long long ctas, int cluster, long long sms) {
+    const double exchange = cluster == 8 ? 0.75 : cluster > 1 ? 0.93 : 1.0;
+    const double per_sm = (double)ctas / (double)sms, waves = per_sm / 4;
+    if (waves > 1) return (0.35 + 0.65 * waves / std::ceil(waves)) * exchange;
+    return per_sm / std::ceil(per_sm) * std::min(1.0, per_sm / 1.6) * exchange;
+}
+
+// The shape and the cluster, by the channel tiles there are (fractions of the copy rate,
+// one GB300, 8192 tokens unless said).  CTAs of four warps, four on an SM, out of step
+// with each other, in the clusters that use the card best (97 tiles of 32 channels in
+// fours 0.69, 195 in twos 0.78, 256 uncut 0.86, 1024 in fours 0.97); a long walk of more
+// than a wave is cut in four.  Where no cluster fills the card the walk waits for its
+// rounds: larger CTAs then make fewer (1 x 65536 x 1024: 0.75 with six warps, 0.69 with
+// eight or four; 1 x 55483 x 256: 0.26 with eight, 0.20 with four).  Backward in bf16,
+// where tiles of 64 channels are nearly a wave of one CTA an SM: two channels a lane
+// (115 tiles 0.88, 128 0.98; one channel 0.81 and 0.86).
 template <typename T, bool BWD>
 cudaError_t launch(const ScanParams& p, int B, cudaStream_t s) {
-    const long long sms = sm_count(), tiles = (p.D + 31ll) / 32 * B, wide_tiles = (p.D + 63ll) / 64 * B;
-    if constexpr (BWD) {
-        if constexpr (sizeof(T) == 2)
-            if ((wide_tiles * 5 >= sms * 4 && wide_tiles <= sms) || wide_tiles >= 4 * sms)
-                return plan<Shape<T, 2, 16, 8, 2, 1, true>>(p, B, s);
-        return plan<Shape<T, 1, 16, 8, 2, 2, true>>(p, B, s);
-    } else {
-        constexpr int R = 64 / (int)sizeof(T);
-        if (tiles >= sms) return plan<Shape<T, 1, R, 4, 2, 4, false>>(p, B, s);
-        if constexpr (sizeof(T) == 2)
-            if (tiles * kMaxCluster >= sms) return plan<Shape<T, 1, R, 6, 2, 2, false>>(p, B, s);
-        return plan<Shape<T, 1, R, 8, 2, 2, false>>(p, B, s);
+    constexpr int R = BWD ? 16 : 64 / (int)sizeof(T);  // backward three tensors' rows are in registers
+    using Small = Shape<T, 1, R, 4, 2, 4, BWD>;
+    using Large = Shape<T, 1, R, 8, 2, 2, BWD>;
+    const long long sms = sm_count(), tiles = (p.D + 31ll) / 32 * B, channels = (long long)B * p.D;
+    // us at 262,144 channels: 16 tokens 12 (a round of the ring 49), 64 tokens 30 (53), 128
+    // tokens 53 (57); at 1024 channels 16 tokens 8 either way, 64 tokens 12 (8)
+    if ((p.T <= 16 || (p.T <= 64 && p.T * 2048ll <= channels)) && channels < 1ll << 31) {
+        const unsigned pairs = (unsigned)(channels / 2);
+        TraceScope trace(BWD ? "scan_short_bwd_kernel" : "scan_short_kernel", s);
+        scan_short_kernel<T, BWD><<<(pairs + 127) / 128, 128, 0, s>>>(p, pairs);
+        return cudaGetLastError();
     }
+    if constexpr (BWD && sizeof(T) == 2) {
+        const long long wide = (p.D + 63ll) / 64 * B;
+        if (wide * 100 >= sms * 72 && wide * 100 <= sms * 90)
+            return launch<Shape<T, 2, 16, 8, 2, 1, true>>(p, B, 1, s);
+    }
+    if (tiles > 4 * sms)
+        return launch<Small>(p, B, tiles < 16 * sms && p.T >= 16 * Small::kRun ? 4 : 1, s);
+    int cluster = 1;
+    double use = card_use(tiles, 1, sms);
+    for (int c = 2; c <= kMaxCluster && (long long)(c / 2) * Small::kRun < p.T; c *= 2)
+        if (card_use(tiles * c, c, sms) > use) cluster = c, use = card_use(tiles * c, c, sms);
+    if (use >= 0.65 || p.T <= Small::kRun) return launch<Small>(p, B, cluster, s);
+    cluster = 1;
+    while (cluster < kMaxCluster && tiles * cluster <= sms && (long long)cluster * Large::kRun < p.T)
+        cluster *= 2;
+    if constexpr (!BWD && sizeof(T) == 2)
+        if (tiles * kMaxCluster >= sms) return launch<Shape<T, 1, R, 6, 2, 2, BWD>>(p, B, cluster, s);
+    return launch<Large>(p, B, cluster, s);
 }
 
 }  // namespace
@@ -490,7 +572,6 @@ cudaError_t launch_scan_fwd(const RecurrenceArgs& a, cudaStream_t s) {
     ScanParams p = {};
     p.x = a.x; p.log_a = a.log_a; p.s0 = a.h0; p.y = a.h; p.s_out = a.h_out;
     p.T = a.T; p.D = a.D; p.dev_status = a.dev_status;
-    TraceScope trace("scan_kernel", s);
     const cudaError_t e = a.bf16 ? launch<__nv_bfloat16, false>(p, a.B, s)
                                  : launch<float, false>(p, a.B, s);
     return e == cudaSuccess ? cudaGetLastError() : e;
@@ -501,7 +582,6 @@ cudaError_t launch_scan_bwd(const RecurrenceArgs& a, cudaStream_t s) {
     p.x = a.dh; p.log_a = a.log_a; p.s0 = a.dh_T; p.h_in = a.h; p.h0 = a.h0;
     p.y = a.dx; p.dlog_a = a.dlog_a; p.s_out = a.dh0;
     p.T = a.T; p.D = a.D; p.dev_status = a.dev_status;
-    TraceScope trace("scan_bwd_kernel", s);
     const cudaError_t e = a.bf16 ? launch<__nv_bfloat16, true>(p, a.B, s)
                                  : launch<float, true>(p, a.B, s);
     return e == cudaSuccess ? cudaGetLastError() : e;

@@ -43,6 +43,10 @@ CASES = [
     (2, 5000, 4080, "bf16", True, True),
     (1, 4001, 720, "bf16", True, True),
     (5, 2500, 8208, "bf16", False, False),
+    (2, 17, 48, "bf16", True, True),
+    (40, 39, 4080, "f32", True, True),
+    (33, 64, 4080, "bf16", True, True),
+    (7, 16, 80, "bf16", True, True),
 ]
 
 
