@@ -338,8 +338,8 @@ LA_API size_t la_bwd_workspace_size(int B, int H, int T, int d_k, int d_v, la_dt
  *   eps       > 0, finite (with LA_QK_NORM)
  *   q_scale, k_scale    finite
  *   flags     LA_QK_NORM | LA_QK_ADJACENT
- *   q_out, k_out  [B][Hq][T][d], [B][Hk][T][d] dtype, dense; they may overlap no
- *             input and not each other
+ *   q_out, k_out  [B][Hq][T][d], [B][Hk][T][d] dtype, dense; their memory may overlap
+ *             no input's (first to last row) and not each other's
  *
  * Sums, norms and angles are fp32, rounded once to dtype at the end; the sum of a
  * row's squares must stay below the fp32 range (|x| below about 1e18).
@@ -361,9 +361,9 @@ LA_API la_status la_qk_rotate_fwd(const void* q, const long long* q_strides, con
  *   q, k .. flags   as the forward call
  *   dq_out, dk_out  [B][Hq][T][d], [B][Hk][T][d] dtype, dense: the loss's gradient
  *             with respect to q_out, k_out (la_chunk_bwd's dQ, dK)
- *   dq, dk    [B][T][Hq][d], [B][T][Hk][d] dtype with strides as q's (they may be
- *             slices of one packed row); their rows may overlap neither each other
- *             nor any input
+ *   dq, dk    [B][T][Hq][d], [B][T][Hk][d] dtype with strides as q's; they may be
+ *             slices of one packed row, their rows apart, and their memory (first to
+ *             last row) may overlap no input's
  *   dq_weight, dk_weight  fp32 [d] or NULL: the weights' gradients, summed over
  *             batch, tokens and heads in a fixed order; overwritten
  *   workspace at least la_qk_rotate_bwd_workspace_size(...) bytes when a weight
@@ -401,7 +401,9 @@ LA_API size_t la_qk_rotate_bwd_workspace_size(int B, int T, int Hq, int Hk, int 
  *   weight    DEVICE fp32 [H][d] or NULL (ones)
  *   flags     LA_GATE_CENTER;  eps > 0, finite
  *   y         [B][T][H][d] dtype, y_strides (batch, token, head) or NULL; its rows
- *             may overlap neither each other nor any input
+ *             may not overlap each other, nor its memory (first to last row) an input's
+ *   A gate of -infinity makes its entry NaN (0 times infinity), the type's lowest
+ *   value makes it 0.
  * Strides as la_qk_rotate_fwd: rows dense, strides >= 0 and multiples of 16 bytes.
  * d a multiple of 16 in [16, 256], H in [1, 65536], B * T < 2^31; sums in fp32 (as
  * la_qk_rotate_fwd).  B or T == 0 is a no-op.  Errors: LA_ERR_INVALID_ARG,
@@ -425,8 +427,9 @@ LA_API la_status la_head_gate_fwd(const void* o, const long long* o_strides, con
  *             overwritten
  *   workspace at least la_head_gate_bwd_workspace_size(...) bytes when dweight is
  *             asked for, else may be NULL; one for each call that may run at once
- * The outputs' rows overlap nothing.  B or T == 0: dweight is zeroed, nothing else
- * is done.  Errors as la_head_gate_fwd.
+ * Each output's rows lie apart, in memory (first to last row) that overlaps no
+ * input's and no other output's.  B or T == 0: dweight is zeroed, nothing else is
+ * done.  Errors as la_head_gate_fwd.
  */
 LA_API la_status la_head_gate_bwd(const void* o, const long long* o_strides, const void* gate,
                                   const long long* gate_strides, const void* dy,
@@ -455,7 +458,9 @@ LA_API size_t la_head_gate_bwd_workspace_size(int B, int H, int T, int d, la_dty
  *   h_out   [B][D] fp32 final state h_T, or NULL
  *   dev_status  device int or NULL (see the conventions above)
  *
- * The state is fp32 throughout; h is rounded where it is stored.  T == 0: h_out is
+ * The state is fp32 throughout; h is rounded where it is stored.  An infinity or NaN
+ * lasts in the state until a restart, or until the decays' product over some run of
+ * tokens is zero in fp32.  T == 0: h_out is
  * the initial state.  B == 0 is a no-op.  B * D at most 2^33.  No workspace.
  * Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
  */

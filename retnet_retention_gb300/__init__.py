@@ -594,8 +594,9 @@ class _launch_on:
         with contextlib.ExitStack() as switched:
             switched.enter_context(torch.cuda.device(dev))
             if stream is not None:
-                if not isinstance(stream, torch.cuda.Stream):
-                    stream = torch.cuda.ExternalStream(int(stream), device=dev)
+                if not isinstance(stream, torch.cuda.Stream):  # a handle; 0 is the default stream
+                    stream = (torch.cuda.ExternalStream(int(stream), device=dev) if int(stream)
+                              else torch.cuda.default_stream(dev))
                 if stream.device != dev:
                     raise ValueError(f"the stream is on {stream.device}; the inputs are on {dev}")
                 switched.enter_context(torch.cuda.stream(stream))
@@ -628,12 +629,25 @@ def _rows(t, name: str, shape: tuple, dtype, dev):
         return None, None
     if t.shape != shape or t.dtype != dtype or t.device != dev:
         _refuse(t, name, shape, dtype, dev)
+    return _strided(t, name)
+
+
+def _strided(t, name: str):
+    """_rows of a tensor whose shape, dtype and device are the call's own."""
     if t.is_contiguous():
         return t.data_ptr(), None
     s0, s1, s2, s3 = t.stride()
     if s3 != 1:
         raise ValueError(f"{name}: the entries of a row must lie one after another")
     return t.data_ptr(), _Strides(s0, s1, s2)
+
+
+def _output(t, name: str, shape: tuple, dtype, dev):
+    """(tensor, address) of a dense output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _dense(t, name, shape, dtype, dev)
 
 
 def _dense(t, name: str, shape: tuple, dtype, dev) -> int | None:
@@ -690,7 +704,9 @@ def _qk_args(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight, 
     if not 0 <= pos0 < 2 ** 31:
         raise ValueError(f"pos0 must be from 0 to 2^31 - 1, not {pos0}")
     f32 = torch.float32
-    inputs = _rows(q, "q", (B, T, Hq, d), dt, dev) + _rows(k, "k", (B, T, Hk, d), dt, dev)
+    if k.device != dev:
+        raise ValueError(f"k is on {k.device}; the inputs are on {dev}")
+    inputs = _strided(q, "q") + _strided(k, "k")
     rest = (_dtype_code(q), B, T, Hq, Hk, d, rot, freq.buffer_info()[0] if rot else None,
             _dense(positions, "positions", (B, T), torch.int32, dev), pos0,
             _dense(q_weight, "q_weight", (d,), f32, dev), _dense(k_weight, "k_weight", (d,), f32, dev),
@@ -716,12 +732,9 @@ def qk_rotate_fwd(q, k, *, positions=None, pos0=0, rot=None, inv_freq=None, inte
                                   k_weight, eps, q_scale, k_scale)
     (B, T, Hq, d), Hk, dt, dev = q.shape, k.shape[2], q.dtype, q.device
     with _launch_on(dev, stream) as s:
-        if q_out is None:
-            q_out = torch.empty((B, Hq, T, d), dtype=dt, device=dev)
-        if k_out is None:
-            k_out = torch.empty((B, Hk, T, d), dtype=dt, device=dev)
-        st = _load().la_qk_rotate_fwd(*inputs, *rest, _dense(q_out, "q_out", (B, Hq, T, d), dt, dev),
-                                      _dense(k_out, "k_out", (B, Hk, T, d), dt, dev), s)
+        q_out, yq = _output(q_out, "q_out", (B, Hq, T, d), dt, dev)
+        k_out, yk = _output(k_out, "k_out", (B, Hk, T, d), dt, dev)
+        st = _load().la_qk_rotate_fwd(*inputs, *rest, yq, yk, s)
     _check(st, "la_qk_rotate_fwd")
     return q_out, k_out
 
@@ -773,11 +786,13 @@ def head_gate_fwd(o, gate=None, *, weight=None, eps=1e-6, center=False, out=None
     with _launch_on(dev, stream) as s:
         if out is None:
             out = torch.empty((B, T, H, d), dtype=dt, device=dev)
-        st = _load().la_head_gate_fwd(*_rows(o, "o", (B, H, T, d), dt, dev),
-                                      *_rows(gate, "gate", (B, T, H, d), dt, dev), code,
+            y = (out.data_ptr(), None)
+        else:
+            y = _rows(out, "out", (B, T, H, d), dt, dev)
+        st = _load().la_head_gate_fwd(*_strided(o, "o"), *_rows(gate, "gate", (B, T, H, d), dt, dev), code,
                                       _dense(weight, "weight", (H, d), torch.float32, dev), B, H, T,
                                       d, LA_GATE_CENTER if center else 0, float(eps),
-                                      *_rows(out, "out", (B, T, H, d), dt, dev), s)
+                                      *y, s)
     _check(st, "la_head_gate_fwd")
     return out
 
@@ -833,15 +848,13 @@ def scan_fwd(x, log_a, *, h0=None, out=None, h_out=None, return_state=True, dev_
     f32 = torch.float32
     _buffer(dev_status, "dev_status", 1, torch.int32, dev)
     with _launch_on(dev, stream) as s:
-        if out is None:
-            out = torch.empty((B, T, D), dtype=dt, device=dev)
-        if return_state and h_out is None:
-            h_out = torch.empty((B, D), dtype=f32, device=dev)
+        out, y = _output(out, "out", (B, T, D), dt, dev)
+        last = None
+        if return_state or h_out is not None:
+            h_out, last = _output(h_out, "h_out", (B, D), f32, dev)
         st = _load().la_scan_fwd(_dense(x, "x", (B, T, D), dt, dev), code,
                                  _dense(log_a, "log_a", (B, T, D), f32, dev), B, T, D,
-                                 _dense(h0, "h0", (B, D), f32, dev),
-                                 _dense(out, "out", (B, T, D), dt, dev),
-                                 _dense(h_out, "h_out", (B, D), f32, dev), _ptr(dev_status), s)
+                                 _dense(h0, "h0", (B, D), f32, dev), y, last, _ptr(dev_status), s)
     _check(st, "la_scan_fwd")
     return out, h_out
 
@@ -858,18 +871,14 @@ def scan_bwd(log_a, h, dh, *, h0=None, dh_T=None, dx=None, dlog_a=None, state_gr
     f32 = torch.float32
     _buffer(dev_status, "dev_status", 1, torch.int32, dev)
     with _launch_on(dev, stream) as s:
-        if dx is None:
-            dx = torch.empty((B, T, D), dtype=dt, device=dev)
-        if dlog_a is None:
-            dlog_a = torch.empty((B, T, D), dtype=f32, device=dev)
+        dx, gx = _output(dx, "dx", (B, T, D), dt, dev)
+        dlog_a, ga = _output(dlog_a, "dlog_a", (B, T, D), f32, dev)
         dh0 = torch.empty((B, D), dtype=f32, device=dev) if state_grads else None
         st = _load().la_scan_bwd(_dense(log_a, "log_a", (B, T, D), f32, dev),
                                  _dense(h, "h", (B, T, D), dt, dev),
                                  _dense(dh, "dh", (B, T, D), dt, dev), code, B, T, D,
                                  _dense(h0, "h0", (B, D), f32, dev),
-                                 _dense(dh_T, "dh_T", (B, D), f32, dev),
-                                 _dense(dx, "dx", (B, T, D), dt, dev),
-                                 _dense(dlog_a, "dlog_a", (B, T, D), f32, dev), _ptr(dh0),
+                                 _dense(dh_T, "dh_T", (B, D), f32, dev), gx, ga, _ptr(dh0),
                                  _ptr(dev_status), s)
     _check(st, "la_scan_bwd")
     return dx, dlog_a, dh0
@@ -884,13 +893,11 @@ def scan_step(x, log_a, h, *, out=None, h_out=None, stream=None):
     dev, dt, code = x.device, x.dtype, _dtype_code(x)
     f32 = torch.float32
     with _launch_on(dev, stream) as s:
-        if out is None:
-            out = torch.empty((B, D), dtype=dt, device=dev)
+        out, y = _output(out, "out", (B, D), dt, dev)
+        state = _dense(h, "h", (B, D), f32, dev)
         st = _load().la_scan_step(_dense(x, "x", (B, D), dt, dev), code,
-                                  _dense(log_a, "log_a", (B, D), f32, dev), B, D,
-                                  _dense(h, "h", (B, D), f32, dev),
-                                  _dense(h if h_out is None else h_out, "h_out", (B, D), f32, dev),
-                                  _dense(out, "out", (B, D), dt, dev), s)
+                                  _dense(log_a, "log_a", (B, D), f32, dev), B, D, state,
+                                  state if h_out is None else _dense(h_out, "h_out", (B, D), f32, dev), y, s)
     _check(st, "la_scan_step")
     return out
 

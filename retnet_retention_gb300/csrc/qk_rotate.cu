@@ -382,7 +382,7 @@ QkParams params(const QkRotateArgs& a, bool bwd) {
         // the fraction of a turn per position, in [0, 1): whole turns change nothing
         double turns = a.inv_freq[i] * 0.15915494309189533577;
         turns -= std::floor(turns);
-        const unsigned long long F = turns >= 1.0 ? 0ull : (unsigned long long)std::ldexp(turns, 64);
+        const unsigned long long F = turns >= 1.0 ? 0ull : (unsigned long long)(turns * 18446744073709551616.0);  // 2^64: exact
         p.freq[i] = make_uint2((unsigned)F, (unsigned)(F >> 32));
     }
     return p;
