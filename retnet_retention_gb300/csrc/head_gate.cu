@@ -64,7 +64,7 @@ struct Cursor {
 template <typename T>
 __device__ __forceinline__ float sigmoid(float g) {
     float e, s;
-    if (sizeof(T) == 2) e = __expf(-g);
+    if (sizeof(T) == 2) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
     else e = expf(-g);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));  // 1 ulp
     return s;
@@ -160,10 +160,9 @@ __global__ void __launch_bounds__(kThreads, BWD ? 5 : 6) head_gate_kernel(const 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 sg = make_float2(sigmoid<T>(g[j].x), sigmoid<T>(g[j].y));
-                    // slope: sigma (1 + g (1 - sigma))
-                    const float2 slope = __fmul2_rn(
-                        sg, __ffma2_rn(g[j], __fadd2_rn(both(1.f), make_float2(-sg.x, -sg.y)), both(1.f)));
+                    // the gate's slope: sigma + g sigma (1 - sigma)
                     const float2 act = __fmul2_rn(g[j], sg);
+                    const float2 slope = __ffma2_rn(act, __ffma2_rn(sg, both(-1.f), both(1.f)), sg);
                     g[j] = __fmul2_rn(__fmul2_rn(du[j], __fmul2_rn(n[j], w[j])), slope);
                     du[j] = __fmul2_rn(du[j], act);
                 }
