@@ -335,8 +335,8 @@ constexpr int kFwdPerSm = 32, kBwdPerSm = 5;
 
 // Heads a group walks: all of a side's (its angles are then computed once a token)
 // while that leaves the card full of groups, fewer for short calls.
-int head_block(const QkRotateArgs& a, int heads) {
-    const long long threads = (long long)a.B * a.T * group_lanes(a.d), full = sm_count() * 256LL;
+int head_block(const QkRotateArgs& a, int heads, int sms) {
+    const long long threads = (long long)a.B * a.T * group_lanes(a.d), full = sms * 256LL;
     int hb = heads;
     while (hb > 1 && threads * ((heads + hb - 1) / hb) < full) hb = (hb + 1) / 2;
     return hb;
@@ -344,23 +344,24 @@ int head_block(const QkRotateArgs& a, int heads) {
 
 // One side's share of the groups and CTAs.  Backward, a few CTAs per SM stay and walk
 // the items, each leaving one row of partial sums.
-void plan_side(Side* s, const QkRotateArgs& a, bool key, bool bwd) {
+void plan_side(Side* s, const QkRotateArgs& a, bool key, bool bwd, int sms) {
     const int groups = kThreads / group_lanes(a.d);
     s->H = key ? a.Hk : a.Hq;
-    s->hb = head_block(a, s->H);
+    s->hb = head_block(a, s->H, sms);
     s->nhb = (s->H + s->hb - 1) / s->hb;
     s->items = (unsigned)((long long)a.B * a.T * s->nhb);
     s->ctas = (s->items + groups - 1) / groups;
     // an item costs its heads' rows and, for its set-up and angles, about 1.5 rows more
     const double rows = s->hb + 1.5, share = s->nhb * rows;
-    const int other = key ? a.Hq : a.Hk, other_hb = head_block(a, other);
+    const int other = key ? a.Hq : a.Hk, other_hb = head_block(a, other, sms);
     const double rest = (double)((other + other_hb - 1) / other_hb) * (other_hb + 1.5);
-    const double most = sm_count() * (bwd ? kBwdPerSm : kFwdPerSm) * share / (share + rest);
+    const double most = sms * (bwd ? kBwdPerSm : kFwdPerSm) * share / (share + rest);
     s->ctas = std::min(s->ctas, (unsigned)std::max(1.0, most));
 }
 
 QkParams params(const QkRotateArgs& a, bool bwd) {
     QkParams p;
+    const int sms = sm_count();
     for (int key = 0; key < 2; ++key) {
         Side& s = p.side[key];
         const long long *xs = key ? a.k_strides : a.q_strides, *ys = key ? a.yk_strides : a.yq_strides;
@@ -372,7 +373,7 @@ QkParams params(const QkRotateArgs& a, bool bwd) {
         s.x_b = xs[0]; s.x_t = xs[1]; s.x_h = xs[2];
         s.y_b = ys[0]; s.y_t = ys[1]; s.y_h = ys[2];
         s.scale = key ? a.k_scale : a.q_scale;
-        plan_side(&s, a, key, bwd);
+        plan_side(&s, a, key, bwd, sms);
     }
     // with few heads the angles are the larger part: one group then takes both sides
     p.both = !bwd && p.side[0].nhb == 1 && p.side[1].nhb == 1;
@@ -384,12 +385,12 @@ QkParams params(const QkRotateArgs& a, bool bwd) {
     p.tokens = Divide::by(a.T);
     p.d = a.d; p.rot = a.rot; p.norm = a.norm;
     p.eps = a.eps;
-    for (int i = 0; i < 128; ++i) p.freq[i] = make_uint2(0, 0);
     for (int i = 0; i < a.rot / 2; ++i) {
         // the fraction of a turn per position, in [0, 1): whole turns change nothing
         double turns = a.inv_freq[i] * 0.15915494309189533577;
         turns -= std::floor(turns);
-        const unsigned long long F = turns >= 1.0 ? 0ull : (unsigned long long)(turns * 18446744073709551616.0);  // 2^64: exact
+        // times 2^64: exact
+        const unsigned long long F = turns >= 1.0 ? 0ull : (unsigned long long)(turns * 18446744073709551616.0);
         p.freq[i] = make_uint2((unsigned)F, (unsigned)(F >> 32));
     }
     return p;
@@ -421,8 +422,9 @@ void launch(const QkParams& p, bool halves, bool bwd, unsigned grid, cudaStream_
 
 size_t qk_rotate_bwd_workspace_bytes(const QkRotateArgs& a) {
     Side q, k;
-    plan_side(&q, a, false, true);
-    plan_side(&k, a, true, true);
+    const int sms = sm_count();
+    plan_side(&q, a, false, true, sms);
+    plan_side(&k, a, true, true, sms);
     return ((size_t)q.ctas + k.ctas) * a.d * sizeof(float);
 }
 
