@@ -16,7 +16,9 @@
 //
 // A decay of exactly zero (log_a = -inf) restarts its channel: the old state is
 // dropped by a selection, not multiplied by zero, so that an infinity or a NaN in
-// it does not pass.  (A run whose product underflows drops it the same way.)
+// it does not pass.  Nothing else drops one: a run's product that underflows without a
+// zero among its decays is held at the least fp32 number (an error of 2^-149 of the
+// state), so that what an infinity or a NaN reaches does not depend on the runs' lengths.
 //
 // Bound by HBM: log_a 4, x 2, h 2 bytes an entry (bf16).  State, products and sums
 // are fp32; h is rounded where it is stored, never the state that is carried on.
@@ -31,7 +33,7 @@
 // a round waits for.
 //
 // One GB300, bf16: 8 x 8192 x 4096 332 us (6.5 TB/s, 0.95 of a copy's rate), 1 x 65536 x
-// 1024 107 us (5.0 TB/s: 32 tiles of channels in clusters of 8 fill 256 of 304 places,
+// 1024 109 us (4.9 TB/s: 32 tiles of channels in clusters of 8 fill 256 of 304 places,
 // issue slots half used), gradients of 4 x 4096 x 2048 73 us (6.4 TB/s).
 #include <algorithm>
 #include <cmath>
@@ -129,6 +131,8 @@ __device__ __forceinline__ void wait_runs(const uint64_t* bar, uint32_t parity, 
 __device__ __forceinline__ float after(float A, float b, float s) {
     return A == 0.f ? b : fmaf(A, s, b);
 }
+
+constexpr float kLeast = 1.401298464e-45f;  // 2^-149, the least fp32 number
 
 // V neighbouring entries of a row in shared memory, as fp32.
 template <int V>
@@ -311,31 +315,42 @@ __global__ void __launch_bounds__(K::W * 32, K::kCtas) scan_kernel(const __grid_
         const bool cut = __any_sync(0xffffffffu, zero);
         if (cut) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) bb[j] = 0.f;
+            for (int j = 0; j < V; ++j) {
+                float least = kLeast;
+                bb[j] = 0.f;
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-#pragma unroll
-                for (int j = 0; j < V; ++j)
+                for (int i = 0; i < R; ++i) {
+                    least = fminf(least, a[i][j]);
                     bb[j] = BWD ? (a[i][j] == 0.f ? 0.f : a[i][j] * (v[i][j] + bb[j]))
                                 : after(a[i][j], v[i][j], bb[j]);
+                }
+                A[j] = fmaxf(A[j], least);
+            }
         }
 #pragma unroll
         for (int j = 0; j < V; ++j)
             warp_run[(par * W + w) * C + lane * V + j] = make_float2(A[j], bb[j]);
         __syncthreads();
         // the run before this warp's in the CTA, and the whole CTA's
-        float pA[V], pb[V], tA[V], tb[V];
+        float pA[V], pb[V], tA[V], tb[V], p_least[V], least[V];  // least: 0 once a run holds a restart
 #pragma unroll
-        for (int j = 0; j < V; ++j) tA[j] = 1.f, tb[j] = 0.f, pA[j] = 1.f, pb[j] = 0.f;
+        for (int j = 0; j < V; ++j)
+            tA[j] = pA[j] = 1.f, tb[j] = pb[j] = 0.f, least[j] = p_least[j] = kLeast;
 #pragma unroll
         for (int i = 0; i < W; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float2 r = warp_run[(par * W + i) * C + lane * V + j];
-                if (i == w) pA[j] = tA[j], pb[j] = tb[j];
+                if (i == w) pA[j] = tA[j], pb[j] = tb[j], p_least[j] = least[j];
                 tb[j] = after(r.x, r.y, tb[j]);
                 tA[j] *= r.x;
+                least[j] = fminf(least[j], r.x);
             }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            tA[j] = fmaxf(tA[j], least[j]);
+            pA[j] = fmaxf(pA[j], p_least[j]);
+        }
         float s[V];
         if (n > 1) {
             // A slot and its barrier are used again two rounds later.  A CTA pushes its

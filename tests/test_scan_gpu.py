@@ -164,6 +164,41 @@ def test_nothing_passes_a_restart(T):
     assert torch.equal(got[1][:, cut:], want[1][:, cut:]) and torch.equal(got[0], want[0])
 
 
+@pytest.mark.parametrize("B,T,D,dt", [(1, 12, 32, "f32"), (2, 100, 64, "f32"), (2, 100, 48, "bf16"),
+                                      (1, 5003, 48, "f32"), (1, 900, 7680, "bf16"),
+                                      (3, 700, 3088, "bf16"), (5, 600, 8208, "f32")])
+def test_infinities_and_nan_last_until_a_restart(B, T, D, dt):
+    """Decays whose product underflows over any run of more than three tokens are no
+    restart: what an infinity or a NaN reaches is what the formula says."""
+    at, cut = T // 6, T - T // 6
+    x = torch.ones(B, T, D, dtype=TYPES[dt], device=DEV)
+    log_a = torch.full((B, T, D), -30.0, device=DEV)
+    log_a[:, cut] = float("-inf")
+    clean, _ = la.scan_fwd(x, log_a)
+    bad = x.clone()
+    bad[:, at, 0::3], bad[:, at, 1::3] = float("inf"), float("nan")
+    h, hT = la.scan_fwd(bad, log_a)
+    torch.cuda.synchronize()
+    assert bool(torch.isposinf(h[:, at:cut, 0::3]).all()) and bool(torch.isnan(h[:, at:cut, 1::3]).all())
+    assert torch.equal(h[:, :at], clean[:, :at]) and torch.equal(h[:, cut:], clean[:, cut:])
+    assert torch.equal(h[..., 2::3], clean[..., 2::3]) and bool(torch.isfinite(hT).all())
+    # backward: from cut towards the first token, as far as the restart's own dx
+    restart = T // 8
+    log_a[:, cut], log_a[:, restart] = -30.0, float("-inf")
+    want = la.scan_bwd(log_a, clean, x)
+    bad = x.clone()
+    bad[:, cut, 0::3], bad[:, cut, 1::3] = float("inf"), float("nan")
+    dx, dla, dh0 = la.scan_bwd(log_a, clean, bad)
+    torch.cuda.synchronize()
+    assert bool(torch.isposinf(dx[:, restart:cut + 1, 0::3]).all())
+    assert bool(torch.isnan(dx[:, restart:cut + 1, 1::3]).all())
+    assert bool(torch.isposinf(dla[:, restart + 1:cut + 1, 0::3]).all())
+    for a, b in zip((dx, dla), want):
+        assert torch.equal(a[:, :restart], b[:, :restart]) and torch.equal(a[:, cut + 1:], b[:, cut + 1:])
+        assert torch.equal(a[..., 2::3], b[..., 2::3])
+    assert torch.equal(dh0, want[2])
+
+
 @pytest.mark.parametrize("B,D,dt", [(1, 16, "f32"), (3, 48, "bf16"), (256, 4096, "bf16"), (5, 1040, "f32")])
 def test_step(B, D, dt):
     """One step is a scan of one token, bit for bit; in place or not."""
