@@ -417,7 +417,11 @@ __global__ void __launch_bounds__(K::W * 32, K::kCtas) scan_kernel(const __grid_
     }
     if (n > 1) {
         cluster_barrier();  // no CTA ends while another may still write to it
-        if (gave_up && threadIdx.x == 0 && p.dev_status) *p.dev_status = LA_ERR_TIMEOUT;
+        if (gave_up && threadIdx.x == 0) {
+            if (p.dev_status) *p.dev_status = LA_ERR_TIMEOUT;
+            // runs it did not wait for may still be on their way here: microseconds
+            for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 50000;) {}
+        }
     }
     if (p.s_out && on && rank == 0 && w == 0) {
 #pragma unroll
