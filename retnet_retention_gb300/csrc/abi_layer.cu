@@ -57,7 +57,7 @@ bool make_view(View* v, const void* p, const long long* strides, long long n0, l
     for (int i = 0; i < 3; ++i) {
         long long s = strides ? strides[i] : dense[i];
         if (v->size[i] == 1) s = 0;
-        if (s < 0 || (s * (long long)v->es) % 16 != 0 || s > kMaxSpan) return false;
+        if (s < 0 || s > kMaxSpan || s * (long long)v->es % 16 != 0) return false;
         if (s > 0 && v->size[i] - 1 > (kMaxSpan - span) / s) return false;
         span += (v->size[i] - 1) * s;
         v->stride[i] = s;
