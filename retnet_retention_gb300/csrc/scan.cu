@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(K::W * 32, K::kCtas) scan_kernel(const __grid_
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 a[i][j] = expf(a[i][j]);
-                bb[j] = BWD ? a[i][j] * (v[i][j] + bb[j]) : fmaf(a[i][j], bb[j], v[i][j]);
+                bb[j] = BWD && i == 0 ? v[i][j] : fmaf(a[BWD && i > 0 ? i - 1 : i][j], bb[j], v[i][j]);
                 A[j] *= a[i][j];
             }
         // a zero among the decays makes the product zero: only then (or after an
@@ -321,11 +321,14 @@ __global__ void __launch_bounds__(K::W * 32, K::kCtas) scan_kernel(const __grid_
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     least = fminf(least, a[i][j]);
-                    bb[j] = BWD ? (a[i][j] == 0.f ? 0.f : a[i][j] * (v[i][j] + bb[j]))
-                                : after(a[i][j], v[i][j], bb[j]);
+                    bb[j] = BWD && i == 0 ? v[i][j] : after(a[BWD && i > 0 ? i - 1 : i][j], v[i][j], bb[j]);
                 }
                 A[j] = fmaxf(A[j], least);
             }
+        }
+        if (BWD) {  // so far the run's last dx: what it passes on
+#pragma unroll
+            for (int j = 0; j < V; ++j) bb[j] = a[R - 1][j] == 0.f ? 0.f : a[R - 1][j] * bb[j];
         }
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -395,9 +398,13 @@ __global__ void __launch_bounds__(K::W * 32, K::kCtas) scan_kernel(const __grid_
                 for (int j = 0; j < V; ++j) {
                     const bool drop = decltype(select)::value && a[i][j] == 0.f;
                     if (BWD) {
-                        out[j] = v[i][j] + s[j];
-                        s[j] = drop ? 0.f : a[i][j] * out[j];
-                        dla[j] = drop ? 0.f : s[j] * hp[BWD ? i : 0][j];
+                        // s: what the run before passed on, then the rows' dx.  The sum is one
+                        // operation in both forms, so that a channel's bits do not hang on
+                        // whether another one of its warp restarts.
+                        const float before = i > 0 ? a[i > 0 ? i - 1 : 0][j] : 1.f;
+                        s[j] = decltype(select)::value && before == 0.f ? v[i][j] : fmaf(before, s[j], v[i][j]);
+                        out[j] = s[j];
+                        dla[j] = drop ? 0.f : a[i][j] * s[j] * hp[BWD ? i : 0][j];
                     } else {
                         s[j] = drop ? v[i][j] : fmaf(a[i][j], s[j], v[i][j]);
                         out[j] = s[j];
