@@ -16,9 +16,10 @@
 //
 // A decay of exactly zero (log_a = -inf) restarts its channel: the old state is
 // dropped by a selection, not multiplied by zero, so that an infinity or a NaN in
-// it does not pass.  Nothing else drops one: a run's product that underflows without a
-// zero among its decays is held at the least fp32 number (an error of 2^-149 of the
-// state), so that what an infinity or a NaN reaches does not depend on the runs' lengths.
+// it, or in a decay before, does not pass.  Nothing else drops one: a run's product
+// that underflows without a zero among its decays is held at the least fp32 number (an
+// error of 2^-149 of the state), so that what an infinity or a NaN reaches does not
+// depend on the runs' lengths.
 //
 // Bound by HBM: log_a 4, x 2, h 2 bytes an entry (bf16).  State, products and sums
 // are fp32; h is rounded where it is stored, never the state that is carried on.
@@ -307,11 +308,12 @@ __global__ void __launch_bounds__(K::W * 32, K::kCtas) scan_kernel(const __grid_
                 bb[j] = BWD && i == 0 ? v[i][j] : fmaf(a[BWD && i > 0 ? i - 1 : i][j], bb[j], v[i][j]);
                 A[j] *= a[i][j];
             }
-        // a zero among the decays makes the product zero: only then (or after an
-        // underflow) do the restarts' selections run, for the whole warp
+        // a zero among the decays makes the product zero, or a NaN where another one is
+        // NaN or infinite: only then (or after an underflow) do the restarts' selections
+        // run, for the whole warp
         bool zero = false;
 #pragma unroll
-        for (int j = 0; j < V; ++j) zero |= A[j] == 0.f;
+        for (int j = 0; j < V; ++j) zero |= !(A[j] > 0.f);
         const bool cut = __any_sync(0xffffffffu, zero);
         if (cut) {
 #pragma unroll
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(K::W * 32, K::kCtas) scan_kernel(const __grid_
                     least = fminf(least, a[i][j]);
                     bb[j] = BWD && i == 0 ? v[i][j] : after(a[BWD && i > 0 ? i - 1 : i][j], v[i][j], bb[j]);
                 }
-                A[j] = fmaxf(A[j], least);
+                A[j] = fmaxf(A[j], least);  // a number: after a NaN decay and no restart bb is the NaN
             }
         }
         if (BWD) {  // so far the run's last dx: what it passes on

@@ -1,5 +1,5 @@
 """Calls of the layer operators at the edges of what their documentation allows:
-restarts beside channels that have none (GPU)."""
+restarts beside channels that have none, and behind decays that are no numbers (GPU)."""
 import pytest
 import torch
 
@@ -43,3 +43,56 @@ def test_a_restart_leaves_the_other_channels_bits(c):
     others = torch.arange(D, device=DEV) % 3 != 0
     for a, b in zip((h, hT, *got_b), (want, last, *want_b)):
         assert torch.equal(a[..., others], b[..., others])
+
+
+# ---- scan: a decay that is no number, then a restart ---------------------------------
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+@pytest.mark.parametrize("gap", [1, 2, 40])
+@pytest.mark.parametrize("c", SCANS, ids=lambda c: "x".join(map(str, c)))
+def test_a_decay_that_is_no_number_stays_before_the_restart(c, gap, bad):
+    """One token's decay is NaN (or infinite), the restart follows in the same run of
+    rows or in a later one, and no other channel restarts: from the restart on, nothing
+    is left of it; backward nothing before it."""
+    B, T, D, dt = c
+    at = T // 3
+    cut = at + min(gap, T - 2 - at)
+    g = torch.Generator().manual_seed(T + D)
+    x, dh = (torch.randn(B, T, D, generator=g).to(TYPES[dt]).to(DEV) for _ in range(2))
+    h0, dT = (torch.randn(B, D, generator=g).to(DEV) for _ in range(2))
+    log_a = -torch.rand(B, T, D, generator=g).to(DEV)
+    log_a[:, cut, ::3] = float("-inf")
+    clean, last = la.scan_fwd(x, log_a, h0=h0)
+    hit = log_a.clone()
+    hit[:, at, ::3] = bad
+    h, hT = la.scan_fwd(x, hit, h0=h0)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(hT).all()) and torch.equal(hT, last)
+    assert torch.equal(h[:, cut:], clean[:, cut:]) and torch.equal(h[:, :at], clean[:, :at])
+    others = torch.arange(D, device=DEV) % 3 != 0
+    assert torch.equal(h[..., others], clean[..., others])
+    assert not bool(torch.isfinite(h[:, at:cut, ::3]).any())
+    # backward the walk meets the bad decay first, the restart then at a token before it
+    log_a[:, cut, ::3], back = -0.5, at - min(gap, at - 1)
+    log_a[:, back, ::3] = float("-inf")
+    want = la.scan_bwd(log_a, clean, dh, h0=h0, dh_T=dT)
+    hit = log_a.clone()
+    hit[:, at, ::3] = bad
+    dx, dla, dh0 = la.scan_bwd(hit, clean, dh, h0=h0, dh_T=dT)
+    torch.cuda.synchronize()
+    assert torch.equal(dh0, want[2])
+    assert torch.equal(dx[:, :back], want[0][:, :back]) and torch.equal(dx[:, at:], want[0][:, at:])
+    assert torch.equal(dla[:, :back + 1], want[1][:, :back + 1]) and torch.equal(dla[:, at + 1:], want[1][:, at + 1:])
+    assert torch.equal(dx[..., others], want[0][..., others]) and torch.equal(dla[..., others], want[1][..., others])
+    assert not bool(torch.isfinite(dx[:, back:at, ::3]).any())
+    assert not bool(torch.isfinite(dla[:, back + 1:at + 1, ::3]).any())
+
+
+def test_a_step_drops_what_its_restart_cuts_off():
+    x = torch.randn(2, 48, device=DEV)
+    h = torch.full((2, 48), float("nan"), device=DEV)
+    h[1] = float("inf")
+    log_a = torch.full((2, 48), float("-inf"), device=DEV)
+    out = la.scan_step(x, log_a, h)
+    torch.cuda.synchronize()
+    assert torch.equal(out, x) and torch.equal(h, x)
