@@ -142,13 +142,18 @@ struct Lane {
     }
 
     // x <- R x with (c, s), R^T x with (c, -s): its first four entries are the first ones
-    // of the four pairs
-    __device__ __forceinline__ static void rotate(float2 (&x)[4], const float2 (&c)[2], const float2 (&s)[2]) {
+    // of the four pairs.  Entries that do not turn take c alone: a product with s = 0 would
+    // hand on another entry's infinity as a NaN.
+    __device__ __forceinline__ void rotate(float2 (&x)[4], const float2 (&c)[2], const float2 (&s)[2]) const {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float2 a = x[j], b = x[j + 2], minus = make_float2(-s[j].x, -s[j].y);
-            x[j] = __ffma2_rn(a, c[j], __fmul2_rn(b, minus));
-            x[j + 2] = __ffma2_rn(a, s[j], __fmul2_rn(b, c[j]));
+            x[j] = __fmul2_rn(a, c[j]);
+            x[j + 2] = __fmul2_rn(b, c[j]);
+            if (turned) {
+                x[j] = __ffma2_rn(b, minus, x[j]);
+                x[j + 2] = __ffma2_rn(a, s[j], x[j + 2]);
+            }
         }
     }
 };
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) qk_rotate_fwd_kernel(const __grid_co
                 if (p.norm) f *= rsqrtf(group_sum<G>(dot8(x, x)) * inv_d + p.eps);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], __fmul2_rn(w[j], both(f)));
-                Lane<HALVES>::rotate(x, c, s);
+                l.rotate(x, c, s);
                 if (h < there) store8<RUN, PAIRS>(y_row, l.e1, l.e2, x);
                 y_row += y_h;
             }
@@ -295,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 5) qk_rotate_bwd_kernel(const __grid
             __syncwarp();
             fetch();
             slot = slot + 1 == kRing ? 0 : slot + 1;
-            Lane<HALVES>::rotate(g, c, s);
+            l.rotate(g, c, s);
             if (p.norm) {
                 float2 gw[4];
 #pragma unroll

@@ -1,5 +1,6 @@
 """Calls of the layer operators at the edges of what their documentation allows:
-restarts beside channels that have none, and behind decays that are no numbers (GPU)."""
+restarts beside channels that have none, and behind decays that are no numbers;
+infinities beside entries that do not turn (GPU)."""
 import pytest
 import torch
 
@@ -16,6 +17,11 @@ def _built():
     from retnet_retention_gb300 import _build
     _build.build()
     la.library()
+
+
+def same(a, b):
+    """Equal, NaN to NaN."""
+    return bool(((a == b) | (torch.isnan(a) & torch.isnan(b))).all())
 
 
 # ---- scan: a channel beside one that restarts ----------------------------------------
@@ -96,3 +102,30 @@ def test_a_step_drops_what_its_restart_cuts_off():
     out = la.scan_step(x, log_a, h)
     torch.cuda.synchronize()
     assert torch.equal(out, x) and torch.equal(h, x)
+
+
+# ---- qk_rotate: entries that do not turn ---------------------------------------------
+
+@pytest.mark.parametrize("interleaved", [True, False], ids=["adjacent", "halves"])
+@pytest.mark.parametrize("d,rot", [(64, 32), (80, 16), (48, 0), (256, 240)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_an_entry_that_does_not_turn_stands_alone(d, rot, interleaved, dt):
+    """Without the norm an infinity or a NaN among the entries past rot reaches no other
+    entry, forward or backward: y = s x there."""
+    B, T, H = 2, 5, 3
+    g = torch.Generator().manual_seed(d + rot)
+    q = torch.randn(B, T, H, d, generator=g).to(TYPES[dt]).to(DEV)
+    hurt = q.clone()
+    for i, e in enumerate(range(rot, d, 5)):
+        hurt[..., e] = (float("inf"), float("nan"), float("-inf"))[i % 3]
+    bad = ~torch.isfinite(hurt[0, 0, 0])
+    opts = dict(rot=rot, interleaved=interleaved, norm=False, q_scale=-0.5)
+    got, want = la.qk_rotate_fwd(hurt, q, **opts)[0], la.qk_rotate_fwd(q, q, **opts)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(got[..., ~bad], want[..., ~bad])
+    assert same(got[..., bad], -0.5 * hurt.transpose(1, 2)[..., bad])
+    dy, dk = hurt.transpose(1, 2).contiguous(), q.transpose(1, 2).contiguous()
+    got, want = la.qk_rotate_bwd(q, q, dy, dk, **opts)[0], la.qk_rotate_bwd(q, q, dk, dk, **opts)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(got[..., ~bad], want[..., ~bad])
+    assert same(got[..., bad], -0.5 * hurt[..., bad])
