@@ -362,8 +362,9 @@ LA_API la_status la_qk_rotate_fwd(const void* q, const long long* q_strides, con
  *   dq_out, dk_out  [B][Hq][T][d], [B][Hk][T][d] dtype, dense: the loss's gradient
  *             with respect to q_out, k_out (la_chunk_bwd's dQ, dK)
  *   dq, dk    [B][T][Hq][d], [B][T][Hk][d] dtype with strides as q's; they may be
- *             slices of one packed row, their rows apart, and their memory (first to
- *             last row) may overlap no input's
+ *             slices of one packed row (side by side, or interleaved head by head,
+ *             the outer strides then multiples of the heads'), their rows apart, and
+ *             their memory (first to last row) may overlap no input's
  *   dq_weight, dk_weight  fp32 [d] or NULL: the weights' gradients, summed over
  *             batch, tokens and heads in a fixed order; overwritten
  *   workspace at least la_qk_rotate_bwd_workspace_size(...) bytes when a weight

@@ -93,23 +93,36 @@ bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 bool overlap(const View& v, const void* b, size_t nb) { return ranges_overlap(v.p, v.bytes(), b, nb); }
 
-// Two views of one buffer (slices of a packed row) may interleave without sharing an
-// element: when the two outer strides agree and the footprints inside one token are
-// apart.
-bool overlap(const View& a, const View& b) {
-    if (!ranges_overlap(a.p, a.bytes(), b.p, b.bytes())) return false;
-    if (a.size[0] != b.size[0] || a.size[1] != b.size[1] || a.stride[0] != b.stride[0] ||
-        a.stride[1] != b.stride[1] || a.es != b.es)
-        return true;
-    const long long outer = a.stride[0], token = a.stride[1];
-    const long long period = token > 0 ? token : outer;  // 0: a single token, apart or not by range
-    if (period <= 0 || (token > 0 && outer % token != 0)) return true;
-    const long long fa = a.d + (a.size[2] - 1) * a.stride[2], fb = b.d + (b.size[2] - 1) * b.stride[2];
+// Are two views of one buffer apart modulo `period`?  Where it divides every stride that
+// is not smaller, each view lies in the footprint of its smaller strides, repeated; the
+// views share no element where the two footprints are apart within one period.
+bool apart_modulo(const View& a, const View& b, long long period) {
+    long long foot[2];
+    for (int k = 0; k < 2; ++k) {
+        const View& v = k ? b : a;
+        foot[k] = v.d;
+        for (int i = 0; i < 3; ++i) {
+            if (v.stride[i] < period) foot[k] += (v.size[i] - 1) * v.stride[i];
+            else if (v.stride[i] % period != 0) return false;
+        }
+    }
     const intptr_t bytes = (intptr_t)((uintptr_t)b.p - (uintptr_t)a.p);
-    if (bytes % (intptr_t)a.es != 0) return true;
+    if (bytes % (intptr_t)a.es != 0) return false;
     long long delta = (long long)(bytes / (intptr_t)a.es) % period;
     if (delta < 0) delta += period;
-    return !(delta >= fa && delta + fb <= period);
+    return delta >= foot[0] && delta + foot[1] <= period;
+}
+
+// Slices of a packed row may interleave without sharing an element, token by token (q's
+// heads beside k's) or head by head (each head's q beside its k): apart modulo one of
+// their strides.
+bool overlap(const View& a, const View& b) {
+    if (!ranges_overlap(a.p, a.bytes(), b.p, b.bytes())) return false;
+    if (a.es != b.es) return true;
+    for (const View* v : {&a, &b})
+        for (long long s : v->stride)
+            if (s > 0 && apart_modulo(a, b, s)) return false;
+    return true;
 }
 
 void keep(long long (&to)[3], const View& v) { std::memcpy(to, v.stride, sizeof(to)); }

@@ -1,0 +1,33 @@
+"""Refusals of the layer operators at the edges of what their documentation allows.
+
+Pointers are fake integers that are never touched: each call fails its host checks.
+"""
+import pytest
+
+import retnet_retention_gb300 as la
+from test_layer_cpu import BAD, FAKE, MB, qk_bwd, s3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from retnet_retention_gb300 import _build
+    _build.build()
+    return la.library()
+
+
+# a packed gradient row of 4 heads with q, k and v of 64 beside each other: dq first, dk
+# behind it
+STEP = 3 * 64
+ROW = 4 * STEP
+INTERLEAVED = dict(Hk=4, dq=FAKE + 6 * MB, dqs=s3(3 * ROW, ROW, STEP), dk=FAKE + 6 * MB + 64 * 2,
+                   dks=s3(3 * ROW, ROW, STEP))
+
+
+@pytest.mark.parametrize("over", [
+    dict(dk=FAKE + 6 * MB), dict(dk=FAKE + 6 * MB + 32 * 2), dict(dk=FAKE + 6 * MB + (2 * 64 + 32) * 2),
+    dict(dk=FAKE + 6 * MB - 32 * 2), dict(dk=FAKE + 6 * MB + (ROW + 16) * 2),
+    dict(dks=s3(3 * ROW, ROW, STEP + 64)), dict(dks=s3(3 * (ROW + 64), ROW + 64, STEP)),
+    dict(dks=s3(3 * ROW, ROW, 64)), dict(Hk=2, dks=s3(3 * ROW, ROW, STEP + 8)),
+], ids=lambda d: ",".join(d))
+def test_interleaved_gradients_that_touch_are_refused(lib, over):
+    assert qk_bwd(lib, **dict(INTERLEAVED, **over)) == BAD

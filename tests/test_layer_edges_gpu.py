@@ -1,6 +1,6 @@
 """Calls of the layer operators at the edges of what their documentation allows:
 restarts beside channels that have none, and behind decays that are no numbers;
-infinities beside entries that do not turn (GPU)."""
+infinities beside entries that do not turn; gradients in slices that interleave (GPU)."""
 import pytest
 import torch
 
@@ -129,3 +129,36 @@ def test_an_entry_that_does_not_turn_stands_alone(d, rot, interleaved, dt):
     torch.cuda.synchronize()
     assert torch.equal(got[..., ~bad], want[..., ~bad])
     assert same(got[..., bad], -0.5 * hurt[..., bad])
+
+
+# ---- qk_rotate_bwd: gradients in slices that interleave ------------------------------
+
+def interleaved_slices(kind, B, T, H, d):
+    """(the whole gradient, its slices for q and k): each head's q, k and v side by side
+    in a token's row, the heads first, or the parts of a head kept in separate rows."""
+    if kind == "rows":
+        row = torch.full((B, T, H, 3, d), 7.0, dtype=torch.bfloat16, device=DEV)
+        return row, row[..., 0, :], row[..., 1, :], row[..., 2, :]
+    if kind == "heads":
+        row = torch.full((B, H, T, 3, d), 7.0, dtype=torch.bfloat16, device=DEV)
+        return row, row[..., 2, :].permute(0, 2, 1, 3), row[..., 0, :].permute(0, 2, 1, 3), row[..., 1, :]
+    row = torch.full((B, T, 3, H, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    return row, row[:, :, 1], row[:, :, 2], row[:, :, 0]
+
+
+@pytest.mark.parametrize("kind", ["rows", "heads", "blocks"])
+@pytest.mark.parametrize("B,T,H,d", [(2, 7, 4, 64), (1, 5, 3, 16), (3, 1, 5, 48), (2, 6, 1, 32), (1, 1, 2, 128)])
+def test_gradients_into_interleaved_slices(kind, B, T, H, d):
+    """What the forward call reads as slices the gradients fill as such: equal to dense
+    ones, and the third part of the row keeps what it held."""
+    g = torch.Generator().manual_seed(B + T + H + d)
+    q, k = (torch.randn(B, T, H, d, generator=g).bfloat16().to(DEV) for _ in range(2))
+    gq, gk = (torch.randn(B, H, T, d, generator=g).bfloat16().to(DEV) for _ in range(2))
+    w = torch.rand(d, generator=g).to(DEV)
+    want = la.qk_rotate_bwd(q, k, gq, gk, q_weight=w, k_weight=w)
+    _, dq, dk, rest = interleaved_slices(kind, B, T, H, d)
+    got = la.qk_rotate_bwd(q, k, gq, gk, q_weight=w, k_weight=w, dq=dq, dk=dk)
+    torch.cuda.synchronize()
+    assert got[0] is dq and got[1] is dk
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert bool((rest == 7).all())
