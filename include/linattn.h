@@ -330,7 +330,7 @@ LA_API size_t la_bwd_workspace_size(int B, int H, int T, int d_k, int d_v, la_dt
  *             bytes, or NULL for the dense layout.  The stride of a dimension of
  *             size 1 is not read.
  *   d         a multiple of 16 in [16, 256];  rot a multiple of 16 in [0, d]
- *   inv_freq  HOST double[rot/2], radians per position (rot > 0); finite
+ *   inv_freq  HOST double[rot/2], radians per position (rot > 0); below 2^64 in size
  *   positions DEVICE int32 [B][T], any values, or NULL: token t stands at pos0 + t,
  *             0 <= pos0 and pos0 + T - 1 < 2^31.  The angle keeps fp32 accuracy at
  *             every position (its fraction of a turn is taken in 64-bit integers).

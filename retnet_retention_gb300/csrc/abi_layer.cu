@@ -156,7 +156,7 @@ la_status qk_args(QkRotateArgs* a, View* vq, View* vk, const void* q, const long
     if (rot > 0) {
         if (!inv_freq) return LA_ERR_INVALID_ARG;
         for (int i = 0; i < rot / 2; ++i)
-            if (!std::isfinite(inv_freq[i])) return LA_ERR_INVALID_ARG;
+            if (!(std::fabs(inv_freq[i]) < 18446744073709551616.0)) return LA_ERR_INVALID_ARG;  // or NaN
     }
     std::memset(a, 0, sizeof(*a));
     a->B = B; a->T = T; a->Hq = Hq; a->Hk = Hk; a->d = d; a->rot = rot;

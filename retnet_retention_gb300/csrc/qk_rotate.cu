@@ -10,8 +10,8 @@
 // gx = g w and dx = r (gx - x r^2 mean(gx x)).
 //
 // The angle of pair i at position p is p f_i.  Its fraction of a turn is taken in
-// integers: F_i = f_i / 2 pi in units of 2^-64 turns, p F_i mod 2^64 is exact, so a
-// position of any size keeps the angle to fp32 accuracy, without 64-bit floats.
+// integers: F_i = f_i / 2 pi modulo one turn, in units of 2^-64 turns, p F_i mod 2^64 is
+// exact, so a position of any size keeps the angle to fp32 accuracy, without 64-bit floats.
 //
 // Bound by HBM: 2 bytes in and 2 out an entry (bf16), about 10 operations.  A
 // group of d / 8 lanes holds one row.  With split halves a lane holds four entries
@@ -364,6 +364,23 @@ void plan_side(Side* s, const QkRotateArgs& a, bool key, bool bwd, int sms) {
     s->ctas = std::min(s->ctas, (unsigned)std::max(1.0, most));
 }
 
+// f / 2 pi modulo one turn in units of 2^-64 turns, |f| < 2^64: the product of f's 53 bits
+// and 128 bits of 1 / 2 pi.  Below 2 units off (below 1 up to 2^63, where the product's
+// own truncation is all).  In doubles it would be 2^-53 of f / 2 pi off: at a position of
+// 2^31 that is 2^-22 radians for f = 1 and 2^-12 for f = 1000.
+unsigned long long turn_fraction(double f) {
+    using Wide = unsigned __int128;
+    constexpr unsigned long long kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;  // 2^128 / 2 pi
+    int e;
+    const auto m = (unsigned long long)std::ldexp(std::frexp(std::fabs(f), &e), 53);  // |f| = m 2^(e - 53)
+    const Wide low = (Wide)m * kLo, high = (Wide)m * kHi + (low >> 64);  // m 2^128 / 2 pi = high 2^64 + low % 2^64
+    const int s = 117 - e;  // its bits from 2^s on are the units, s >= 53
+    unsigned long long F = 0;
+    if (s < 64) F = (unsigned long long)(high << (64 - s)) | (unsigned long long)low >> s;
+    else if (s < 192) F = (unsigned long long)(high >> (s - 64));
+    return f < 0 ? 0ull - F : F;
+}
+
 QkParams params(const QkRotateArgs& a, bool bwd) {
     QkParams p;
     const int sms = sm_count();
@@ -391,11 +408,7 @@ QkParams params(const QkRotateArgs& a, bool bwd) {
     p.d = a.d; p.rot = a.rot; p.norm = a.norm;
     p.eps = a.eps;
     for (int i = 0; i < a.rot / 2; ++i) {
-        // the fraction of a turn per position, in [0, 1): whole turns change nothing
-        double turns = a.inv_freq[i] * 0.15915494309189533577;
-        turns -= std::floor(turns);
-        // times 2^64: exact
-        const unsigned long long F = turns >= 1.0 ? 0ull : (unsigned long long)(turns * 18446744073709551616.0);
+        const unsigned long long F = turn_fraction(a.inv_freq[i]);
         p.freq[i] = make_uint2((unsigned)F, (unsigned)(F >> 32));
     }
     return p;

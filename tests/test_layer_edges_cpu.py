@@ -2,10 +2,12 @@
 
 Pointers are fake integers that are never touched: each call fails its host checks.
 """
+import ctypes
+
 import pytest
 
 import retnet_retention_gb300 as la
-from test_layer_cpu import BAD, FAKE, MB, qk_bwd, s3
+from test_layer_cpu import BAD, FAKE, MB, qk_bwd, qk_fwd, s3
 
 
 @pytest.fixture(scope="module")
@@ -31,3 +33,10 @@ INTERLEAVED = dict(Hk=4, dq=FAKE + 6 * MB, dqs=s3(3 * ROW, ROW, STEP), dk=FAKE +
 ], ids=lambda d: ",".join(d))
 def test_interleaved_gradients_that_touch_are_refused(lib, over):
     assert qk_bwd(lib, **dict(INTERLEAVED, **over)) == BAD
+
+
+@pytest.mark.parametrize("f", [2.0 ** 64, -(2.0 ** 64), 1e300, float("inf"), float("-inf"), float("nan")])
+def test_frequencies_without_an_angle_are_refused(lib, f):
+    """From 2^64 radians a position on, a double's step is more than the table resolves."""
+    freq = (ctypes.c_double * 32)(*([0.5] * 31 + [f]))
+    assert qk_fwd(lib, freq=freq) == BAD and qk_bwd(lib, freq=freq) == BAD

@@ -1,8 +1,14 @@
 """Calls of the layer operators at the edges of what their documentation allows:
 restarts beside channels that have none, and behind decays that are no numbers;
-infinities beside entries that do not turn; gradients in slices that interleave (GPU)."""
+infinities beside entries that do not turn; gradients in slices that interleave;
+far positions with large frequencies (GPU)."""
+from fractions import Fraction
+
+import numpy as np
 import pytest
 import torch
+
+import layer_ref as ref
 
 la = pytest.importorskip("retnet_retention_gb300")
 
@@ -162,3 +168,44 @@ def test_gradients_into_interleaved_slices(kind, B, T, H, d):
     assert got[0] is dq and got[1] is dk
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert bool((rest == 7).all())
+
+
+# ---- qk_rotate: the angle at far positions with large frequencies --------------------
+
+# pi to 100 digits
+PI = Fraction(31415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679,
+              10 ** 100)
+
+
+def exact_turn(p, f):
+    """cos and sin of p f: the rest of p f over 2 pi in rationals, then in doubles."""
+    turns = Fraction(int(p)) * Fraction(float(f)) / (2 * PI)
+    rest = float(turns - round(turns)) * 2.0 * np.pi
+    return np.cos(rest), np.sin(rest)
+
+
+@pytest.mark.parametrize("interleaved", [True, False], ids=["adjacent", "halves"])
+def test_the_angle_of_far_positions(interleaved):
+    """fp32 accuracy at every position and frequency.  The angle loses 2^-32 turns to the
+    word that is kept and |p| 2^-63 <= 2^-32 to the table, 2^-28.3 radians; the rest of an
+    eighth of a turn is rounded three times (its word, 2 pi and the product: 3 U of at most
+    pi / 4), its series add 2 U and leave out 2^-29; so cosine and sine are off by less
+    than 5 U, and y by 3 U more for the scale, a product and a sum."""
+    freq = [1.0, 7.3, -3.0, 1000.0, 0.5 ** 20, -12345.678, 3.1e6, 10000.0 ** -0.25,
+            2.0 ** 40 + 0.123, -1e15 / 7, 2.0 ** 52 + 1, 1e18, 0.0, 5e-324, 1e-12, 2.0 ** 64 * (1 - 2.0 ** -53)]
+    pos = [0, 1, -1, 77, 65537, 2 ** 24 + 1, -(2 ** 27) - 5, 2 ** 31 - 1, -(2 ** 31), 2 ** 31 - 12345]
+    rot = d = 2 * len(freq)
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(1, len(pos), 2, d, generator=g)
+    y = la.qk_rotate_fwd(q.to(DEV), q.to(DEV), positions=torch.tensor([pos], dtype=torch.int32, device=DEV),
+                         inv_freq=freq, interleaved=interleaved, norm=False, q_scale=0.75)[0]
+    torch.cuda.synchronize()
+    c, s = np.array([[exact_turn(p, f) for f in freq] for p in pos]).transpose(2, 0, 1)[:, None, :, None]
+    m = np.arange(rot // 2)
+    i, j = (2 * m, 2 * m + 1) if interleaved else (m, m + rot // 2)
+    x = ref.f64(q)
+    want, size = np.empty_like(x), np.empty_like(x)
+    want[..., i], want[..., j] = x[..., i] * c - x[..., j] * s, x[..., i] * s + x[..., j] * c
+    size[..., i] = size[..., j] = np.abs(x[..., i]) + np.abs(x[..., j])
+    as_out = lambda v: 0.75 * v.transpose(0, 2, 1, 3)
+    ref.check("y", y, as_out(want), 8.0 * ref.U * as_out(size), torch.float32)
