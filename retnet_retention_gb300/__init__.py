@@ -676,7 +676,7 @@ def rotary_frequencies(rot: int, base: float = 10000.0) -> list[float]:
 def _qk_args(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight, k_weight, eps, q_scale,
              k_scale):
     """The arguments qk_rotate_fwd and qk_rotate_bwd share, checked: (q and k with their
-    strides, the rest, what has to outlive the call)."""
+    strides, those up to the positions, those behind them, what has to outlive the call)."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"shape mismatch: q{tuple(q.shape)} k{tuple(k.shape)} are [B,T,heads,d]")
     dt, dev = q.dtype, q.device
@@ -707,12 +707,18 @@ def _qk_args(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight, 
     if k.device != dev:
         raise ValueError(f"k is on {k.device}; the inputs are on {dev}")
     inputs = _strided(q, "q") + _strided(k, "k")
-    rest = (_dtype_code(q), B, T, Hq, Hk, d, rot, freq.buffer_info()[0] if rot else None,
-            _dense(positions, "positions", (B, T), torch.int32, dev), pos0,
-            _dense(q_weight, "q_weight", (d,), f32, dev), _dense(k_weight, "k_weight", (d,), f32, dev),
+    _dense(positions, "positions", (B, T), torch.int32, dev)
+    head = (_dtype_code(q), B, T, Hq, Hk, d, rot, freq.buffer_info()[0] if rot else None)
+    tail = (pos0, _dense(q_weight, "q_weight", (d,), f32, dev), _dense(k_weight, "k_weight", (d,), f32, dev),
             float(eps), float(q_scale), float(k_scale),
             (LA_QK_NORM if norm else 0) | (LA_QK_ADJACENT if interleaved else 0))
-    return inputs, rest, freq
+    return inputs, head, tail, freq
+
+
+def _aligned(positions):
+    """positions (None passes), copied on the current stream where their address, a place
+    in a longer buffer, is not the multiple of 16 bytes the library asks of every tensor."""
+    return positions if positions is None or positions.data_ptr() % 16 == 0 else positions.clone()
 
 
 def qk_rotate_fwd(q, k, *, positions=None, pos0=0, rot=None, inv_freq=None, interleaved=False,
@@ -723,18 +729,19 @@ def qk_rotate_fwd(q, k, *, positions=None, pos0=0, rot=None, inv_freq=None, inte
     q [B,T,Hq,d] and k [B,T,Hk,d] as the projections leave them (slices of a packed
     row will do: rows of d entries dense, other strides multiples of 16 bytes).
     Returns (q [B,Hq,T,d], k [B,Hk,T,d]), dense: what chunk_fwd reads, and for T = 1
-    (squeezed) recurrent_step.  positions: int32 [B,T] device tensor, or token t
-    stands at pos0 + t.  rot: the first entries that turn (None: all d), inv_freq:
+    (squeezed) recurrent_step.  positions: int32 [B,T] device tensor, contiguous (it may
+    start anywhere in a longer buffer), or token t stands at pos0 + t.  rot: the first entries that turn (None: all d), inv_freq:
     rot/2 host values, radians per position (None: rotary_frequencies(rot));
     interleaved: pairs (2m, 2m+1), else (m, m + rot/2).  norm: each row divided by
     the root of its mean square (plus eps), times q_weight / k_weight (fp32 [d])."""
-    inputs, rest, freq = _qk_args(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight,
-                                  k_weight, eps, q_scale, k_scale)
+    inputs, head, tail, freq = _qk_args(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight,
+                                        k_weight, eps, q_scale, k_scale)
     (B, T, Hq, d), Hk, dt, dev = q.shape, k.shape[2], q.dtype, q.device
     with _launch_on(dev, stream) as s:
         q_out, yq = _output(q_out, "q_out", (B, Hq, T, d), dt, dev)
         k_out, yk = _output(k_out, "k_out", (B, Hk, T, d), dt, dev)
-        st = _load().la_qk_rotate_fwd(*inputs, *rest, yq, yk, s)
+        positions = _aligned(positions)
+        st = _load().la_qk_rotate_fwd(*inputs, *head, _ptr(positions), *tail, yq, yk, s)
     _check(st, "la_qk_rotate_fwd")
     return q_out, k_out
 
@@ -747,8 +754,8 @@ def qk_rotate_bwd(q, k, dq_out, dk_out, *, positions=None, pos0=0, rot=None, inv
     dq_weight [d], dk_weight [d]); a weight's gradient is None where there is no
     weight or weight_grads is False.  dq and dk may be given, with strides (slices of
     one packed gradient)."""
-    inputs, rest, freq = _qk_args(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight,
-                                  k_weight, eps, q_scale, k_scale)
+    inputs, head, tail, freq = _qk_args(q, k, positions, pos0, rot, inv_freq, interleaved, norm, q_weight,
+                                        k_weight, eps, q_scale, k_scale)
     (B, T, Hq, d), Hk, dt, dev = q.shape, k.shape[2], q.dtype, q.device
     lib = _load()
     with _launch_on(dev, stream) as s:
@@ -760,12 +767,13 @@ def qk_rotate_bwd(q, k, dq_out, dk_out, *, positions=None, pos0=0, rot=None, inv
                     if weight_grads and w is not None else None for w in (q_weight, k_weight))
         need = 0
         if dwq is not None or dwk is not None:
-            need = int(lib.la_qk_rotate_bwd_workspace_size(B, T, Hq, Hk, d, rest[0]))
+            need = int(lib.la_qk_rotate_bwd_workspace_size(B, T, Hq, Hk, d, head[0]))
             if need and workspace is None:
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         ws_bytes = _workspace(workspace, need, dev)
+        positions = _aligned(positions)
         st = lib.la_qk_rotate_bwd(*inputs, _dense(dq_out, "dq_out", (B, Hq, T, d), dt, dev),
-                                  _dense(dk_out, "dk_out", (B, Hk, T, d), dt, dev), *rest,
+                                  _dense(dk_out, "dk_out", (B, Hk, T, d), dt, dev), *head, _ptr(positions), *tail,
                                   *_rows(dq, "dq", (B, T, Hq, d), dt, dev),
                                   *_rows(dk, "dk", (B, T, Hk, d), dt, dev),
                                   _ptr(dwq), _ptr(dwk), _ptr(workspace), ws_bytes, s)

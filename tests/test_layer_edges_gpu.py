@@ -1,7 +1,7 @@
 """Calls of the layer operators at the edges of what their documentation allows:
 restarts beside channels that have none, and behind decays that are no numbers;
 infinities beside entries that do not turn; gradients in slices that interleave;
-far positions with large frequencies (GPU)."""
+far positions with large frequencies; positions anywhere in a buffer (GPU)."""
 from fractions import Fraction
 
 import numpy as np
@@ -209,3 +209,32 @@ def test_the_angle_of_far_positions(interleaved):
     size[..., i] = size[..., j] = np.abs(x[..., i]) + np.abs(x[..., j])
     as_out = lambda v: 0.75 * v.transpose(0, 2, 1, 3)
     ref.check("y", y, as_out(want), 8.0 * ref.U * as_out(size), torch.float32)
+
+
+# ---- qk_rotate: positions anywhere in a buffer ---------------------------------------
+
+@pytest.mark.parametrize("start", [0, 1, 2, 3, 4])
+def test_positions_from_the_middle_of_a_buffer(start):
+    """A decoder's slice of its position buffer: int32 addresses, any of them, on a side
+    stream and in a captured graph that reads what the buffer holds at its replay."""
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(6, 1, 3, 64, generator=g).bfloat16().to(DEV)
+    buf = torch.randint(0, 5000, (12, 1), generator=g, dtype=torch.int32).to(DEV)
+    pos = buf[start:start + 6]
+    want = la.qk_rotate_fwd(q, q, positions=pos.clone())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = la.qk_rotate_fwd(q, q, positions=pos, stream=side)
+    grads = la.qk_rotate_bwd(q, q, *want, positions=pos)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    wantg = la.qk_rotate_bwd(q, q, *want, positions=pos.clone())
+    assert all(torch.equal(a, b) for a, b in zip(grads[:2], wantg[:2]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = la.qk_rotate_fwd(q, q, positions=pos)
+    buf.add_(17)
+    graph.replay()
+    want = la.qk_rotate_fwd(q, q, positions=pos.clone())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
