@@ -77,11 +77,6 @@ __device__ __forceinline__ unsigned cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ unsigned cluster_id() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
@@ -196,7 +191,8 @@ __global__ void __launch_bounds__(K::W * 32, K::kCtas) scan_kernel(const __grid_
     float2* warp_run = reinterpret_cast<float2*>(smem + S * K::kStage);  // [2][W][C]
     float2* cta_run = warp_run + 2 * W * C;                              // [2][kMaxCluster][C]
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const unsigned rank = cluster_rank(), n = cluster_size(), unit = cluster_id();
+    const unsigned rank = cluster_rank(), n = cluster_size();
+    const unsigned unit = blockIdx.x / n;  // not %clusterid: past 2^24 it came back rounded to 24 bits
     const unsigned b = unit / (unsigned)p.tiles, tile = unit - b * (unsigned)p.tiles;
     const int first = (int)tile * C, c0 = first + lane * V;
     const bool on = c0 < p.D;

@@ -1,7 +1,8 @@
 """Calls of the layer operators at the edges of what their documentation allows:
 restarts beside channels that have none, and behind decays that are no numbers;
 infinities beside entries that do not turn; gradients in slices that interleave;
-far positions with large frequencies; positions anywhere in a buffer (GPU)."""
+far positions with large frequencies; positions anywhere in a buffer;
+many short sequences (GPU)."""
 from fractions import Fraction
 
 import numpy as np
@@ -238,3 +239,21 @@ def test_positions_from_the_middle_of_a_buffer(start):
     want = la.qk_rotate_fwd(q, q, positions=pos.clone())
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+# ---- scan: many channels -------------------------------------------------------------
+
+def test_more_than_2_24_tiles():
+    """2^27 + 3 sequences of 16 channels, a CTA each: every one is walked."""
+    B, D = 2 ** 27 + 3, 16
+    x = torch.full((B, 1, D), 1.5, dtype=torch.bfloat16, device=DEV)
+    h0 = torch.full((B, D), 2.0, device=DEV)
+    log_a = torch.full((B, 1, D), -1.0, device=DEV)
+    want = torch.tensor(1.5 + 2.0 * np.exp(-1.0)).bfloat16()
+    h, hT = la.scan_fwd(x, log_a, h0=h0, out=torch.zeros_like(x), h_out=h0)
+    left = int((h != want).sum())
+    assert left == 0
+    dx, _, dh0 = la.scan_bwd(log_a, h, x, h0=h0, dx=torch.zeros_like(x))
+    # dh0 = a x 1.5: expf's 4 U and a rounding
+    left = int((dx != 1.5).sum()), int(((dh0 - 1.5 * np.exp(-1.0)).abs() > 8 * ref.U).sum())
+    assert left == (0, 0)
