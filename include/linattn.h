@@ -461,7 +461,7 @@ LA_API size_t la_head_gate_bwd_workspace_size(int B, int H, int T, int d, la_dty
  *
  * The state is fp32 throughout; h is rounded where it is stored.  An infinity or NaN
  * lasts in the state until a restart.  T == 0: h_out is the initial state.  B == 0
- * is a no-op.  B * D at most 2^33.  No workspace.
+ * is a no-op.  B * D at most 2^33, B * T * D at most 2^44.  No workspace.
  * Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
  */
 LA_API la_status la_scan_fwd(const void* x, la_dtype dtype, const float* log_a, int B, int T, int D,

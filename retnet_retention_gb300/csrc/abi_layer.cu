@@ -207,10 +207,14 @@ la_status gate_args(HeadGateArgs* a, View* vo, View* vg, const void* o, const lo
 
 // ---- scan ----------------------------------------------------------------------------
 
+// Channels of all sequences together.  They are at most 2^29 tiles of 32 (sequences of 16
+// channels fill half a tile each), and so many tiles are one CTA each: a grid's limit is
+// 2^31 - 1.
+constexpr long long kMaxChannels = 1ll << 33;
+
 bool scan_shape_ok(int B, int T, int D, la_dtype dtype) {
     return B >= 0 && T >= 0 && D >= 16 && D % 16 == 0 && valid_dtype(dtype) &&
-           (B == 0 || T == 0 || (long long)B * T <= kMaxSpan / D) &&
-           (long long)B * ((D + 31) / 32) <= INT_MAX / 8;
+           (B == 0 || T == 0 || (long long)B * T <= kMaxSpan / D) && (long long)B * D <= kMaxChannels;
 }
 
 bool any_misaligned(std::initializer_list<const void*> ps) {

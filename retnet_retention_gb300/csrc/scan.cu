@@ -543,7 +543,7 @@ cudaError_t launch_kernel(const ScanParams& p, int B, int cluster, cudaStream_t 
 
 template <typename K>
 cudaError_t launch(ScanParams p, int B, int cluster, cudaStream_t s) {
-    p.tiles = (p.D + K::C - 1) / K::C;
+    p.tiles = (int)((p.D + (K::C - 1ll)) / K::C);  // D may be 2^31 - 16
     p.mute = opt_force_timeout();
     p.limit_ns = p.mute ? 1000000ull : 2000000000ull;
     return launch_kernel<K>(p, B, cluster, s);

@@ -2,7 +2,7 @@
 restarts beside channels that have none, and behind decays that are no numbers;
 infinities beside entries that do not turn; gradients in slices that interleave;
 far positions with large frequencies; positions anywhere in a buffer;
-many short sequences (GPU)."""
+many short sequences, more than 2^32 channels (GPU)."""
 from fractions import Fraction
 
 import numpy as np
@@ -257,3 +257,19 @@ def test_more_than_2_24_tiles():
     # dh0 = a x 1.5: expf's 4 U and a rounding
     left = int((dx != 1.5).sum()), int(((dh0 - 1.5 * np.exp(-1.0)).abs() > 8 * ref.U).sum())
     assert left == (0, 0)
+
+
+@pytest.mark.parametrize("B,D", [(2 ** 28 + 3, 16), (2 ** 27 + 1, 48), (2, 2 ** 31 - 16)])
+def test_as_many_channels_as_the_header_allows(B, D):
+    """More than 2^32 channels in all, in sequences of an odd number of 16s."""
+    x = torch.full((B, 1, D), 1.5, dtype=torch.bfloat16, device=DEV)
+    log_a = torch.full((B, 1, D), -1.0, device=DEV)
+    h0 = torch.full((B, D), 2.0, device=DEV)
+    want = torch.tensor(1.5 + 2.0 * np.exp(-1.0)).bfloat16()
+    h, _ = la.scan_fwd(x, log_a, h0=h0, out=torch.zeros_like(x), h_out=h0)
+    left = int((h != want).sum())
+    assert left == 0
+    want = torch.tensor(1.5 + (1.5 + 2.0 * np.exp(-1.0)) * np.exp(-1.0)).bfloat16()
+    out = la.scan_step(x[:, 0], log_a[:, 0], h0, out=h[:, 0].zero_())
+    left = int((out != want).sum())
+    assert left == 0
