@@ -561,14 +561,22 @@ double card_use(long long ctas, int cluster, long long sms) {
 }
 
 // The shape and the cluster, by the channel tiles there are (fractions of the copy rate,
-// one GB300, 8192 tokens unless said).  CTAs of four warps, four on an SM, out of step
+// one GB300, bf16, 8192 tokens unless said).  CTAs of four warps, four on an SM, out of step
 // with each other, in the clusters that use the card best (97 tiles of 32 channels in
-// fours 0.69, 195 in twos 0.78, 256 uncut 0.86, 1024 in fours 0.97); a long walk of more
-// than a wave is cut in four.  Where no cluster fills the card the walk waits for its
-// rounds: larger CTAs then make fewer (1 x 65536 x 1024: 0.75 with six warps, 0.69 with
-// eight or four; 1 x 55483 x 256: 0.26 with eight, 0.20 with four).  Backward in bf16,
-// where tiles of 64 channels are nearly a wave of one CTA an SM: two channels a lane
-// (115 tiles 0.88, 128 0.98; one channel 0.81 and 0.86).
+// fours 0.69, 195 in twos 0.78, 256 uncut 0.85, 1024 in fours 0.90 to 0.97); a long walk of
+// more than a wave is cut in four.  Where no cluster fills the card the walk waits for its
+// rounds: larger CTAs then make fewer, of six warps forward in bf16 where clusters of
+// eight give every SM one (19 tiles and more; 1 x 65536 x 1024: 0.74 with six warps, 0.66
+// with eight, 0.67 with four; 32 tiles of 16384 tokens 35 us with six, 38 with eight; 16 to
+// 19 tiles of 65536 tokens within 2 %), of eight below (12 tiles of 65536 tokens 72 us with
+// eight, 79 with six; 1 x 55483 x 256: 0.26 with eight, 0.20 with four).
+//
+// Backward in bf16, where tiles of 64 channels are 0.72 to 0.86 of a wave of one CTA an SM,
+// two channels a lane (us, against one channel a lane, at 4096 / 8192 / 32768 tokens):
+//   100 tiles 74 (66) / 140 (138) / 536 (570)    110 tiles 74 (74) / 140 (156) / 537 (622)
+//   121 tiles 74 (83) / 141 (161) / 537 (660)    128 tiles 74 (79) / 140 (150) / 537 (585)
+//   132 tiles 77 (81) / 155 (152) / 656 (597)    136 tiles 86 (82) / 173 (156) / 690 (603)
+//   152 tiles 103 (88) / 201 (170) / 775 (728)
 template <typename T, bool BWD>
 cudaError_t launch(const ScanParams& p, int B, cudaStream_t s) {
     constexpr int R = BWD ? 16 : 64 / (int)sizeof(T);  // backward three tensors' rows are in registers
@@ -585,7 +593,7 @@ cudaError_t launch(const ScanParams& p, int B, cudaStream_t s) {
     }
     if constexpr (BWD && sizeof(T) == 2) {
         const long long wide = (p.D + 63ll) / 64 * B;
-        if (wide * 100 >= sms * 72 && wide * 100 <= sms * 90)
+        if (wide * 100 >= sms * 72 && wide * 100 <= sms * 86)
             return launch<Shape<T, 2, 16, 8, 2, 1, true>>(p, B, 1, s);
     }
     if (tiles > 4 * sms)
