@@ -24,8 +24,8 @@
 // the ring of rows.cuh (register double buffers: 80 us where the ring takes 74).
 //
 // One GB300, bf16: 8 x 8192 tokens of 16 + 16 heads of 128 in 166 us (6.5 TB/s, 0.96 of
-// a copy's rate); the gradients of 4 x 4096 of them in 71 us (5.7 TB/s; the kernel alone
-// 60 to 66, the sums over its CTAs and the launch the rest).  With one or two heads the
+// a copy's rate); the gradients of 4 x 4096 of them in 69 us (5.8 TB/s; the kernel alone
+// 61, the sums over its CTAs and the launch the rest).  With one or two heads the
 // angles are the larger part: 16 x 8192 tokens of 1 + 1 heads of 128 in 44 us (3.0 TB/s).
 #include <algorithm>
 #include <cmath>
@@ -365,9 +365,9 @@ void plan_side(Side* s, const QkRotateArgs& a, bool key, bool bwd, int sms) {
 }
 
 // f / 2 pi modulo one turn in units of 2^-64 turns, |f| < 2^64: the product of f's 53 bits
-// and 128 bits of 1 / 2 pi.  Below 2 units off (below 1 up to 2^63, where the product's
-// own truncation is all).  In doubles it would be 2^-53 of f / 2 pi off: at a position of
-// 2^31 that is 2^-22 radians for f = 1 and 2^-12 for f = 1000.
+// and 128 bits of 1 / 2 pi, each cut off: less than 2 units off.  In doubles it would be
+// 2^-53 of f / 2 pi off: at a position of 2^31 that is 2^-22 radians for f = 1 and 2^-12
+// for f = 1000.
 unsigned long long turn_fraction(double f) {
     using Wide = unsigned __int128;
     constexpr unsigned long long kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;  // 2^128 / 2 pi

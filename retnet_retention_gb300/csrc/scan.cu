@@ -33,9 +33,11 @@
 // it is finished gained nothing (142 against 141 us on one GPU): the exchange is not what
 // a round waits for.
 //
-// One GB300, bf16: 8 x 8192 x 4096 332 us (6.5 TB/s, 0.95 of a copy's rate), 1 x 65536 x
-// 1024 109 us (4.9 TB/s: 32 tiles of channels in clusters of 8 fill 256 of 304 places,
-// issue slots half used), gradients of 4 x 4096 x 2048 73 us (6.4 TB/s).
+// One GB300, bf16: 8 x 8192 x 4096 326 us (6.6 TB/s, 0.97 of a copy's rate; 333 on another
+// card), 1 x 65536 x 1024 109 us (4.9 TB/s: 32 tiles of channels in clusters of 8 fill 256
+// of 304 places, 1.19 of the 1.37 it lies above its floor; the rest is a round's chain of
+// copies, exponentials, barrier, exchange and replay with 12 warps an SM, issue slots half
+// used), gradients of 4 x 4096 x 2048 73 us (6.4 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
