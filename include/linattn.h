@@ -496,6 +496,213 @@ LA_API la_status la_scan_step(const void* x, la_dtype dtype, const float* log_a,
                               const float* h_in, float* h_out, void* h, la_stream_t stream);
 
 /*
+ * The short causal convolution over each channel, as it stands before a state space or
+ * gated mixer:
+ *
+ *   u_t = bias + sum_j w[c][j] x_(t-W+1+j),   y = u,  or  u sigmoid(u) with LA_CONV_SILU
+ *
+ *   x, y      [B][T][D] dtype, rows of D entries dense, x_strides, y_strides: HOST arrays
+ *             of 2 strides (batch, token) in elements or NULL for dense, each >= 0 and a
+ *             multiple of 16 bytes (x may be a slice of a packed projection; y's rows lie
+ *             apart).  The stride of a dimension of size 1 is not read.
+ *   weight    DEVICE fp32 [D][W], W from 2 to 4, the last tap the token's own;
+ *             bias DEVICE fp32 [D] or NULL
+ *   state     [B][W-1][D] dtype: the rows before token 0, oldest first, or NULL (zeros)
+ *   positions DEVICE int32 [B][T], each token's place in its document, or NULL: a tap k
+ *             tokens back counts only where k <= positions[b][t] (documents packed one
+ *             behind another, or padding before a sequence).  What does not count is not
+ *             read into the sum, infinities and NaN included.  The taps of a token below
+ *             W - 1 of no other document reach into the state.
+ *   state_out [B][W-1][D] dtype: the last W - 1 rows of state and x, or NULL; may be
+ *             state itself, else may not overlap it
+ *   flags     LA_CONV_SILU
+ * No output may overlap an input (state_out: but state itself) or another output.  Sums in
+ * fp32, rounded once.  D a multiple of 16, B * T < 2^31, B * D at most 2^33, D * W < 2^31.
+ * T == 0: state_out is the state.  B == 0 is a no-op.
+ * Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
+ */
+#define LA_CONV_SILU 1u
+LA_API la_status la_short_conv_fwd(const void* x, const long long* x_strides, la_dtype dtype,
+                                   const float* weight, const float* bias, int B, int T, int D,
+                                   int W, unsigned flags, const void* state, const int* positions,
+                                   void* y, const long long* y_strides, void* state_out,
+                                   la_stream_t stream);
+
+/*
+ * Gradients of la_short_conv_fwd.
+ *   x .. positions  as the forward call
+ *   dy        [B][T][D] dtype, dy_strides as x's;  dstate_T [B][W-1][D] dtype or NULL: the
+ *             gradient with respect to state_out
+ *   dx        [B][T][D] dtype, dx_strides (rows apart; may be a slice of a packed gradient)
+ *   dweight   fp32 [D][W] or NULL, dbias fp32 [D] or NULL: summed over batch and tokens
+ *             in a fixed order; overwritten
+ *   dstate    [B][W-1][D] dtype or NULL: with respect to state (given or not)
+ *   workspace at least la_short_conv_bwd_workspace_size(...) bytes when dweight or dbias is
+ *             asked for, else may be NULL; one for each call that may run at once
+ * No output may overlap an input or another output.  B or T == 0: dweight and dbias are
+ * zeroed, dstate is dstate_T.  Errors as la_short_conv_fwd.
+ */
+LA_API la_status la_short_conv_bwd(const void* x, const long long* x_strides, const void* dy,
+                                   const long long* dy_strides, la_dtype dtype,
+                                   const float* weight, const float* bias, int B, int T, int D,
+                                   int W, unsigned flags, const void* state, const int* positions,
+                                   const void* dstate_T, void* dx, const long long* dx_strides,
+                                   float* dweight, float* dbias, void* dstate, void* workspace,
+                                   size_t workspace_bytes, la_stream_t stream);
+LA_API size_t la_short_conv_bwd_workspace_size(int B, int T, int D, int W, la_dtype dtype);
+
+/*
+ * One token of la_short_conv_fwd: x [B][D] dtype with x_stride elements from sequence to
+ * sequence, y [B][D] dense.  state [B][W-1][D] and state_out as there (state_out may be
+ * state itself).  Errors as la_short_conv_fwd.
+ */
+LA_API la_status la_short_conv_step(const void* x, long long x_stride, la_dtype dtype,
+                                    const float* weight, const float* bias, int B, int D, int W,
+                                    unsigned flags, const void* state, void* state_out, void* y,
+                                    la_stream_t stream);
+
+/*
+ * The selective scan: "decay the old state, add, read out" with N numbers of state a
+ * channel, their decay chosen by each token:
+ *
+ *   delta = softplus(dt + dt_bias)    with LA_SSM_SOFTPLUS, else dt + dt_bias
+ *   h_t = exp(delta A) h_(t-1) + delta x_t b_t       (entry by entry over [D][N])
+ *   y_t = c_t . h_t + skip x_t    [ times gate sigmoid(gate) ]
+ *
+ *   x, dt, gate, y  [B][T][D] dtype;  gate may be NULL
+ *   b, c      [B][T][G][N] dtype, shared by the D / G channels of a group; G divides D,
+ *             N is 8, 16, 32 or 64
+ *   strides   HOST array of 6 pairs of strides (batch, token) in elements, for x, dt, b,
+ *             c, gate and y in this order, or NULL (all dense): rows (of D or G N entries)
+ *             dense, strides >= 0 and multiples of 16 bytes, y's rows apart.  The stride of a
+ *             dimension of size 1 is not read.
+ *   A         DEVICE fp32 [D][N], finite (as a rule below 0);  skip, dt_bias DEVICE fp32
+ *             [D] or NULL (zero)
+ *   h0        [B][D][N] fp32 initial state or NULL for zero; may be h_out itself, else may
+ *             not overlap it
+ *   positions DEVICE int32 [B][T] or NULL: a token with position 0 starts a document: the old state
+ *             is dropped, infinities and NaN included
+ *   h_out     [B][D][N] fp32 final state or NULL
+ *   flags     LA_SSM_SOFTPLUS
+ *   workspace at least la_ssm_workspace_size(...) bytes (which may be 0); overwritten;
+ *             one for each call that may run at once
+ * States, decays and sums are fp32; y is rounded where it is stored.  No output may overlap an
+ * input or another output.  D a multiple of 16, B < 65536, B * T < 2^31, D * N < 2^31.  T == 0:
+ * h_out is the initial state.  B == 0 is a no-op.
+ * Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
+ */
+#define LA_SSM_SOFTPLUS 1u
+LA_API la_status la_ssm_fwd(const void* x, const void* dt, const float* A, const void* b,
+                            const void* c, const float* skip, const void* gate,
+                            const float* dt_bias, const long long* strides, la_dtype dtype, int B,
+                            int T, int D, int N, int G, unsigned flags, const float* h0,
+                            const int* positions, void* y, float* h_out, void* workspace,
+                            size_t workspace_bytes, la_stream_t stream);
+LA_API size_t la_ssm_workspace_size(int B, int T, int D, int N, int G, la_dtype dtype);
+
+/*
+ * Gradients of la_ssm_fwd for the loss sum dy . y + <dh_T, h_T>; the states are computed
+ * again from the inputs.
+ *   x .. positions  as the forward call
+ *   dy        [B][T][D] dtype;  dh_T [B][D][N] fp32 or NULL (zero)
+ *   strides   HOST array of 11 pairs, for x, dt, b, c, gate, dy, dx, ddt, db, dc and
+ *             dgate, or NULL (all dense); the outputs' rows lie apart
+ *   dx, ddt, dgate  [B][T][D], db, dc [B][T][G][N] dtype; dgate is NULL exactly when gate
+ *             is.  ddt is with respect to dt as given (through the softplus).
+ *   dA        fp32 [D][N], dskip, ddt_bias fp32 [D], or NULL: summed over batch and tokens
+ *             in a fixed order; overwritten
+ *   dh0       [B][D][N] fp32 or NULL
+ *   workspace at least la_ssm_bwd_workspace_size(...) bytes; overwritten; one for each
+ *             call that may run at once
+ * A token that starts a document passes nothing to the tokens before it.  db and dc are summed
+ * in fp32 over a group's channels and rounded once.  No output may overlap an input or another
+ * output.  B or T == 0: dA, dskip and ddt_bias are zeroed, dh0 is dh_T.  Errors as la_ssm_fwd.
+ */
+LA_API la_status la_ssm_bwd(const void* x, const void* dt, const float* A, const void* b,
+                            const void* c, const float* skip, const void* gate,
+                            const float* dt_bias, const void* dy, const long long* strides,
+                            la_dtype dtype, int B, int T, int D, int N, int G, unsigned flags,
+                            const float* h0, const int* positions, const float* dh_T, void* dx,
+                            void* ddt, float* dA, void* db, void* dc, float* dskip, void* dgate,
+                            float* ddt_bias, float* dh0, void* workspace, size_t workspace_bytes,
+                            la_stream_t stream);
+LA_API size_t la_ssm_bwd_workspace_size(int B, int T, int D, int N, int G, la_dtype dtype);
+
+/*
+ * One token of la_ssm_fwd: x, dt, gate [B][D], b, c [B][G][N] dtype; strides: HOST array
+ * of 5 strides from sequence to sequence, for x, dt, b, c and gate, or NULL (dense);
+ * h_in, h_out [B][D][N] fp32, h_out may be h_in itself; y [B][D] dense.
+ * Errors as la_ssm_fwd.
+ */
+LA_API la_status la_ssm_step(const void* x, const void* dt, const float* A, const void* b,
+                             const void* c, const float* skip, const void* gate,
+                             const float* dt_bias, const long long* strides, la_dtype dtype, int B,
+                             int D, int N, int G, unsigned flags, const float* h_in, float* h_out,
+                             void* y, la_stream_t stream);
+
+/*
+ * The seam between two blocks of a residual stream: the norm after a block, its gate, the
+ * residual, and the norm before the next block, in one pass over the rows:
+ *
+ *   p  = norm(o) post_weight  with LA_BLOCK_POST_NORM, else o
+ *   h' = residual_scale h + scale gate p
+ *   y  = norm(h') pre_weight  with LA_BLOCK_PRE_NORM
+ *   norm(v) = v (mean(v^2) + eps)^(-1/2)       (v less its mean with LA_BLOCK_CENTER)
+ *
+ *   o, y      [B][T][D] dtype;  h, h_out [B][T][D] residual_dtype: dtype or fp32.  h may be
+ *             NULL (no residual), h_out may be NULL (not kept), y is NULL exactly without
+ *             LA_BLOCK_PRE_NORM.  Each with 2 strides (batch, token) as la_short_conv_fwd's
+ *             x, or NULL for dense; the outputs' rows lie apart.
+ *   post_weight, pre_weight  DEVICE fp32 [D] or NULL (ones); NULL without their norm
+ *   gate      DEVICE fp32 [D], or [B][D] with LA_BLOCK_GATE_EACH, or NULL (ones)
+ *   scale, residual_scale    finite;  eps > 0, finite
+ * h_out may be h itself with the same strides; else no output may overlap an input or another
+ * output.  y is the norm of h' before its rounding.  Sums in fp32; a row's squares must stay
+ * below its range.  D a multiple of 16 up to 8192, B < 65536, B * T < 2^31.  B or T == 0 is a
+ * no-op.  Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
+ */
+#define LA_BLOCK_POST_NORM 1u
+#define LA_BLOCK_PRE_NORM 2u
+#define LA_BLOCK_CENTER 4u
+#define LA_BLOCK_GATE_EACH 8u
+LA_API la_status la_block_norm_fwd(const void* o, const long long* o_strides, la_dtype dtype,
+                                   const void* h, const long long* h_strides,
+                                   la_dtype residual_dtype, const float* post_weight,
+                                   const float* gate, const float* pre_weight, int B, int T, int D,
+                                   unsigned flags, float scale, float residual_scale, float eps,
+                                   void* h_out, const long long* h_out_strides, void* y,
+                                   const long long* y_strides, la_stream_t stream);
+
+/*
+ * Gradients of la_block_norm_fwd from its output h_out.
+ *   o, post_weight .. eps  as the forward call;  h_out as it left it (read with
+ *             LA_BLOCK_PRE_NORM only)
+ *   dy        [B][T][D] dtype, NULL exactly without LA_BLOCK_PRE_NORM;  dh_out [B][T][D]
+ *             residual_dtype or NULL (zero): the gradient with respect to h_out; one of the
+ *             two is given
+ *   d_o       [B][T][D] dtype;  dh [B][T][D] residual_dtype or NULL: with respect to h; may
+ *             be dh_out itself with the same strides
+ *   dpost_weight, dpre_weight fp32 [D], dgate like gate, or NULL: summed over the rows they
+ *             are shared by in a fixed order; overwritten
+ *   workspace at least la_block_norm_bwd_workspace_size(...) bytes when one of these is asked
+ *             for, else may be NULL; one for each call that may run at once
+ * No other output may overlap an input or another output.  B or T == 0: the sums are zeroed.
+ * Errors as la_block_norm_fwd.
+ */
+LA_API la_status la_block_norm_bwd(const void* o, const long long* o_strides, la_dtype dtype,
+                                   const void* h_out, const long long* h_out_strides,
+                                   la_dtype residual_dtype, const void* dy,
+                                   const long long* dy_strides, const void* dh_out,
+                                   const long long* dh_out_strides, const float* post_weight,
+                                   const float* gate, const float* pre_weight, int B, int T, int D,
+                                   unsigned flags, float scale, float residual_scale, float eps,
+                                   void* d_o, const long long* d_o_strides, void* dh,
+                                   const long long* dh_strides, float* dpost_weight, float* dgate,
+                                   float* dpre_weight, void* workspace, size_t workspace_bytes,
+                                   la_stream_t stream);
+LA_API size_t la_block_norm_bwd_workspace_size(int B, int T, int D, la_dtype dtype, unsigned flags);
+
+/*
  * la_chunk_fwd for callers that cannot allocate device memory.  The source
  * pages have no counterpart to this entry point.
  *

@@ -19,6 +19,10 @@ Around them, for a whole layer:
   head_gate_fwd(o, gate, ...) / head_gate_bwd  per-head norm and gate  (la_head_gate_fwd / _bwd)
   scan_fwd(x, log_a, ...) / scan_bwd           per-channel recurrence  (la_scan_fwd / _bwd)
   scan_step(x, log_a, h, ...)                  one token of it         (la_scan_step)
+And for a state space layer in its residual block:
+  short_conv_fwd(x, weight, ...) / short_conv_bwd / short_conv_step    (la_short_conv_*)
+  ssm_fwd(x, dt, A, b, c, ...) / ssm_bwd / ssm_step    selective scan  (la_ssm_*)
+  block_norm_fwd(o, h, ...) / block_norm_bwd   norms, gate, residual   (la_block_norm_*)
 """
 from __future__ import annotations
 
@@ -39,6 +43,9 @@ LA_PHI_ELU1, LA_NORMALIZE, LA_NONCAUSAL, LA_NORM_FLOOR, LA_GATED, LA_PHI_TAYLOR 
 LA_OPT_PATH, LA_OPT_TC_LOCKSTEP, LA_OPT_FORCE_TIMEOUT = 1, 2, 3
 LA_QK_NORM, LA_QK_ADJACENT = 1, 2
 LA_GATE_CENTER = 1
+LA_CONV_SILU = 1
+LA_SSM_SOFTPLUS = 1
+LA_BLOCK_POST_NORM, LA_BLOCK_PRE_NORM, LA_BLOCK_CENTER, LA_BLOCK_GATE_EACH = 1, 2, 4, 8
 
 LIBRARY_PATH = _build.LIBRARY
 _LIB = None
@@ -132,6 +139,33 @@ def _load() -> ctypes.CDLL:
     lib.la_scan_bwd.restype = i
     lib.la_scan_step.argtypes = [vp, i, vp, i, i, vp, vp, vp, vp]
     lib.la_scan_step.restype = i
+    ll = ctypes.c_longlong
+    lib.la_short_conv_fwd.argtypes = [vp, vp, i, vp, vp, i, i, i, i, u, vp, vp, vp, vp, vp, vp]
+    lib.la_short_conv_fwd.restype = i
+    lib.la_short_conv_bwd.argtypes = [vp, vp, vp, vp, i, vp, vp, i, i, i, i, u, vp, vp, vp, vp, vp, vp, vp,
+                                      vp, vp, sz, vp]
+    lib.la_short_conv_bwd.restype = i
+    lib.la_short_conv_bwd_workspace_size.argtypes = [i, i, i, i, i]
+    lib.la_short_conv_bwd_workspace_size.restype = sz
+    lib.la_short_conv_step.argtypes = [vp, ll, i, vp, vp, i, i, i, u, vp, vp, vp, vp]
+    lib.la_short_conv_step.restype = i
+    lib.la_ssm_fwd.argtypes = [vp] * 9 + [i, i, i, i, i, i, u, vp, vp, vp, vp, vp, sz, vp]
+    lib.la_ssm_fwd.restype = i
+    lib.la_ssm_workspace_size.argtypes = [i, i, i, i, i, i]
+    lib.la_ssm_workspace_size.restype = sz
+    lib.la_ssm_bwd.argtypes = [vp] * 10 + [i, i, i, i, i, i, u] + [vp] * 13 + [sz, vp]
+    lib.la_ssm_bwd.restype = i
+    lib.la_ssm_bwd_workspace_size.argtypes = [i, i, i, i, i, i]
+    lib.la_ssm_bwd_workspace_size.restype = sz
+    lib.la_ssm_step.argtypes = [vp] * 9 + [i, i, i, i, i, u, vp, vp, vp, vp]
+    lib.la_ssm_step.restype = i
+    lib.la_block_norm_fwd.argtypes = [vp, vp, i, vp, vp, i, vp, vp, vp, i, i, i, u, f, f, f, vp, vp, vp, vp, vp]
+    lib.la_block_norm_fwd.restype = i
+    lib.la_block_norm_bwd.argtypes = [vp, vp, i, vp, vp, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, u, f, f, f,
+                                      vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.la_block_norm_bwd.restype = i
+    lib.la_block_norm_bwd_workspace_size.argtypes = [i, i, i, i, u]
+    lib.la_block_norm_bwd_workspace_size.restype = sz
     lib.la_debug_set.argtypes = [i, i]
     lib.la_debug_set.restype = i
     lib.la_trace_enable.argtypes = [i]
@@ -910,7 +944,361 @@ def scan_step(x, log_a, h, *, out=None, h_out=None, stream=None):
     return out
 
 
-__all__ = ["qk_rotate_fwd", "qk_rotate_bwd", "rotary_frequencies", "head_gate_fwd", "head_gate_bwd",
+_Pair = ctypes.c_longlong * 2
+
+
+def _tokens(t, name: str, shape: tuple, dtype, dev):
+    """Address and host array of the two outer strides (None: dense) of a [B, T, D] tensor
+    whose rows of D entries are dense (None passes): shape, dtype and device are checked
+    here, alignment in the library."""
+    if t is None:
+        return None, None
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        _refuse(t, name, shape, dtype, dev)
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        raise ValueError(f"{name}: the entries of a row must lie one after another")
+    return t.data_ptr(), _Pair(s0, s1)
+
+
+def _place(t, shape: tuple, dtype, dev):
+    return torch.empty(shape, dtype=dtype, device=dev) if t is None else t
+
+
+def _scratch(workspace, need: int, dev):
+    """(workspace, its bytes): the caller's, checked, or a new one on the current stream."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        return workspace, need
+    return workspace, _workspace(workspace, need, dev)
+
+
+def _conv_shape(x, weight, bias, dims: int):
+    if x.dim() != dims or weight.dim() != 2:
+        raise ValueError(f"x is {tuple(x.shape)}, weight {tuple(weight.shape)}; "
+                         f"{'[B,T,D]' if dims == 3 else '[B,D]'} and [D,W] are needed")
+    D, W = weight.shape
+    dev, f32 = x.device, torch.float32
+    if x.shape[-1] != D:
+        raise ValueError(f"x is {tuple(x.shape)}; its rows are not weight's {D} channels")
+    if not 2 <= W <= 4:
+        raise ValueError(f"weight has {W} taps; 2 to 4 are supported")
+    return W, dev, _dtype_code(x), _dense(weight, "weight", (D, W), f32, dev), _dense(bias, "bias", (D,), f32, dev)
+
+
+def short_conv_fwd(x, weight, *, bias=None, silu=True, state=None, positions=None, out=None, state_out=None,
+                   return_state=True, stream=None):
+    """Short causal convolution over each channel of x [B,T,D] (rows dense, other strides
+    multiples of 16 bytes) with weight fp32 [D,W] (W 2 to 4, the last tap the token's own),
+    bias fp32 [D], then u * sigmoid(u) with silu.  state [B,W-1,D]: the rows before token 0
+    (None: zeros).  positions int32 [B,T]: a tap k tokens back counts only where
+    k <= positions (packed documents, padding in front).  Returns (y [B,T,D], the state
+    behind the last token); the state is None when return_state is False and no state_out was
+    given.  state_out may be state."""
+    W, dev, code, w, b = _conv_shape(x, weight, bias, 3)
+    B, T, D = x.shape
+    dt, held = x.dtype, (B, W - 1, D)
+    with _launch_on(dev, stream) as s:
+        out = _place(out, (B, T, D), dt, dev)
+        last = None
+        if return_state or state_out is not None:
+            state_out, last = _output(state_out, "state_out", held, dt, dev)
+        positions = _aligned(positions)
+        st = _load().la_short_conv_fwd(*_tokens(x, "x", (B, T, D), dt, dev), code, w, b, B, T, D, W,
+                                       LA_CONV_SILU if silu else 0, _dense(state, "state", held, dt, dev),
+                                       _dense(positions, "positions", (B, T), torch.int32, dev),
+                                       *_tokens(out, "out", (B, T, D), dt, dev), last, s)
+    _check(st, "la_short_conv_fwd")
+    return out, state_out
+
+
+def short_conv_bwd(x, weight, dy, *, bias=None, silu=True, state=None, positions=None, dstate_T=None, dx=None,
+                   weight_grads=True, state_grads=True, workspace=None, stream=None):
+    """Gradients of short_conv_fwd for dy [B,T,D] and dstate_T [B,W-1,D] (that of the state
+    it returned): (dx [B,T,D], dweight [D,W], dbias [D], dstate [B,W-1,D]).  dweight and
+    dbias are None with weight_grads False, dbias without a bias, dstate with state_grads
+    False.  dx may be given, with strides."""
+    W, dev, code, w, b = _conv_shape(x, weight, bias, 3)
+    B, T, D = x.shape
+    dt, held, f32 = x.dtype, (B, W - 1, D), torch.float32
+    lib = _load()
+    with _launch_on(dev, stream) as s:
+        dx = _place(dx, (B, T, D), dt, dev)
+        dw = torch.empty((D, W), dtype=f32, device=dev) if weight_grads else None
+        db = torch.empty(D, dtype=f32, device=dev) if weight_grads and bias is not None else None
+        d0 = torch.empty(held, dtype=dt, device=dev) if state_grads else None
+        need = int(lib.la_short_conv_bwd_workspace_size(B, T, D, W, code)) if weight_grads else 0
+        workspace, ws_bytes = _scratch(workspace, need, dev)
+        positions = _aligned(positions)
+        st = lib.la_short_conv_bwd(*_tokens(x, "x", (B, T, D), dt, dev), *_tokens(dy, "dy", (B, T, D), dt, dev),
+                                   code, w, b, B, T, D, W, LA_CONV_SILU if silu else 0,
+                                   _dense(state, "state", held, dt, dev),
+                                   _dense(positions, "positions", (B, T), torch.int32, dev),
+                                   _dense(dstate_T, "dstate_T", held, dt, dev),
+                                   *_tokens(dx, "dx", (B, T, D), dt, dev), _ptr(dw), _ptr(db), _ptr(d0),
+                                   _ptr(workspace), ws_bytes, s)
+    _check(st, "la_short_conv_bwd")
+    return dx, dw, db, d0
+
+
+def short_conv_step(x, weight, state, *, bias=None, silu=True, out=None, state_out=None, stream=None):
+    """One token of short_conv_fwd: x [B,D] (rows dense); state [B,W-1,D] moves up by one
+    row, in place or into state_out.  Returns y [B,D]."""
+    W, dev, code, w, b = _conv_shape(x, weight, bias, 2)
+    B, D = x.shape
+    dt, held = x.dtype, (B, W - 1, D)
+    if D > 1 and x.stride(1) != 1:
+        raise ValueError("x: the entries of a row must lie one after another")
+    with _launch_on(dev, stream) as s:
+        out, y = _output(out, "out", (B, D), dt, dev)
+        old = _dense(state, "state", held, dt, dev)
+        new = old if state_out is None else _dense(state_out, "state_out", held, dt, dev)
+        st = _load().la_short_conv_step(x.data_ptr(), x.stride(0), code, w, b, B, D, W, LA_CONV_SILU if silu else 0,
+                                        old, new, y, s)
+    _check(st, "la_short_conv_step")
+    return out
+
+
+def _ssm_shape(x, dt, A, b, c, skip, gate, dt_bias, dims: int):
+    """The arguments the ssm calls share, checked: (dims, N, G, type code, device and the
+    addresses of A, skip and dt_bias)."""
+    if x.dim() != dims or A.dim() != 2 or b.dim() not in (dims, dims + 1):
+        raise ValueError(f"x is {tuple(x.shape)}, A {tuple(A.shape)}, b {tuple(b.shape)}; "
+                         f"{'[B,T,D], [D,N] and [B,T,G,N]' if dims == 3 else '[B,D], [D,N] and [B,G,N]'} are needed")
+    D, N = A.shape
+    G = b.shape[-2] if b.dim() == dims + 1 else 1
+    dev, ty, f32 = x.device, x.dtype, torch.float32
+    if x.shape[-1] != D:
+        raise ValueError(f"x is {tuple(x.shape)}; its rows are not A's {D} channels")
+    if N not in (8, 16, 32, 64):
+        raise ValueError(f"A has {N} states a channel; 8, 16, 32 or 64 are supported")
+    if G < 1 or D % G:
+        raise ValueError(f"{G} groups do not divide {D} channels")
+    for name, t, shape in (("dt", dt, x.shape), ("gate", gate, x.shape), ("b", b, x.shape[:-1] + b.shape[dims - 1:]),
+                           ("c", c, b.shape)):
+        if t is not None and (t.shape != shape or t.dtype != ty or t.device != dev):
+            _refuse(t, name, shape, ty, dev)
+    if b.shape[-1] != N:
+        raise ValueError(f"b is {tuple(b.shape)}; its rows are not A's {N} states")
+    return N, G, _dtype_code(x), dev, (_dense(A, "A", (D, N), f32, dev), _dense(skip, "skip", (D,), f32, dev),
+                                       _dense(dt_bias, "dt_bias", (D,), f32, dev))
+
+
+def _row_strides(named, outer: int):
+    """The host array of the outer strides of tensors whose rows are dense (None: all are
+    wholly dense); named: (name, tensor) pairs, absent tensors get zeros."""
+    if all(t is None or t.is_contiguous() for _, t in named):
+        return None
+    strides = []
+    for name, t in named:
+        if t is None:
+            strides += [0] * outer
+            continue
+        width = 1
+        for size, step in zip(reversed(t.shape[outer:]), reversed(t.stride()[outer:])):
+            if size > 1 and step != width:
+                raise ValueError(f"{name}: the entries of a row must lie one after another")
+            width *= size
+        strides += t.stride()[:outer]
+    return (ctypes.c_longlong * len(strides))(*strides)
+
+
+def ssm_fwd(x, dt, A, b, c, *, skip=None, gate=None, dt_bias=None, softplus=True, h0=None, positions=None,
+            out=None, h_out=None, return_state=True, workspace=None, stream=None):
+    """Selective scan: delta = softplus(dt + dt_bias) (softplus False: the sum itself),
+    h_t = exp(delta A) h_(t-1) + delta x_t b_t, y_t = (c_t . h_t + skip x_t) gate sigmoid(gate).
+
+    x, dt, gate [B,T,D]; A fp32 [D,N] (below 0; N 8, 16, 32 or 64); b, c [B,T,N], or
+    [B,T,G,N] shared by groups of D / G channels; skip, dt_bias fp32 [D].  Rows dense, other
+    strides multiples of 16 bytes (slices of packed projections).  positions int32 [B,T]: a
+    0 starts a document, which drops the old state.  Returns (y [B,T,D], h_T fp32 [B,D,N]); h_T
+    is None when return_state is False and no h_out was given.  h_out may be h0."""
+    N, G, code, dev, weights = _ssm_shape(x, dt, A, b, c, skip, gate, dt_bias, 3)
+    B, T, D = x.shape
+    f32, state = torch.float32, (B, D, N)
+    lib = _load()
+    with _launch_on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((B, T, D), dtype=x.dtype, device=dev)
+        elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
+            _refuse(out, "out", x.shape, x.dtype, dev)
+        last = None
+        if return_state or h_out is not None:
+            h_out, last = _output(h_out, "h_out", state, f32, dev)
+        strides = _row_strides((("x", x), ("dt", dt), ("b", b), ("c", c), ("gate", gate), ("out", out)), 2)
+        workspace, ws_bytes = _scratch(workspace, int(lib.la_ssm_workspace_size(B, T, D, N, G, code)), dev)
+        positions = _aligned(positions)
+        a, k, bias = weights
+        st = lib.la_ssm_fwd(x.data_ptr(), dt.data_ptr(), a, b.data_ptr(), c.data_ptr(), k,
+                            None if gate is None else gate.data_ptr(), bias, strides, code, B, T, D, N, G,
+                            LA_SSM_SOFTPLUS if softplus else 0, _dense(h0, "h0", state, f32, dev),
+                            _dense(positions, "positions", (B, T), torch.int32, dev), out.data_ptr(), last,
+                            _ptr(workspace), ws_bytes, s)
+    _check(st, "la_ssm_fwd")
+    return out, h_out
+
+
+def ssm_bwd(x, dt, A, b, c, dy, *, skip=None, gate=None, dt_bias=None, softplus=True, h0=None, positions=None,
+            dh_T=None, dx=None, ddt=None, db=None, dc=None, dgate=None, weight_grads=True, state_grads=True,
+            workspace=None, stream=None):
+    """Gradients of ssm_fwd for dy [B,T,D] and dh_T fp32 [B,D,N], from its inputs: (dx, ddt
+    [B,T,D], dA [D,N], db, dc like b, dskip [D], dgate [B,T,D], ddt_bias [D], dh0 [B,D,N]).
+    A gradient is None where its input is; dA, dskip and ddt_bias with weight_grads False,
+    dh0 with state_grads False.  dx, ddt, db, dc and dgate may be given, with strides."""
+    N, G, code, dev, weights = _ssm_shape(x, dt, A, b, c, skip, gate, dt_bias, 3)
+    B, T, D = x.shape
+    ty, f32, state = x.dtype, torch.float32, (B, D, N)
+    if gate is None and dgate is not None:
+        raise ValueError("dgate is given without a gate")
+    lib = _load()
+    with _launch_on(dev, stream) as s:
+        def place(t, name, shape):
+            if t is None:
+                return torch.empty(shape, dtype=ty, device=dev)
+            if t.shape != shape or t.dtype != ty or t.device != dev:
+                _refuse(t, name, shape, ty, dev)
+            return t
+
+        if dy.shape != x.shape or dy.dtype != ty or dy.device != dev:
+            _refuse(dy, "dy", x.shape, ty, dev)
+        dx, ddt = place(dx, "dx", x.shape), place(ddt, "ddt", x.shape)
+        db, dc = place(db, "db", b.shape), place(dc, "dc", b.shape)
+        dgate = None if gate is None else place(dgate, "dgate", x.shape)
+        small = lambda there, *shape: torch.empty(shape, dtype=f32, device=dev) if there else None
+        dA = small(weight_grads, D, N)
+        dskip = small(weight_grads and skip is not None, D)
+        dbias = small(weight_grads and dt_bias is not None, D)
+        dh0 = small(state_grads, *state)
+        strides = _row_strides((("x", x), ("dt", dt), ("b", b), ("c", c), ("gate", gate), ("dy", dy), ("dx", dx),
+                                ("ddt", ddt), ("db", db), ("dc", dc), ("dgate", dgate)), 2)
+        workspace, ws_bytes = _scratch(workspace, int(lib.la_ssm_bwd_workspace_size(B, T, D, N, G, code)), dev)
+        positions = _aligned(positions)
+        a, k, bias = weights
+        at = lambda t: None if t is None else t.data_ptr()
+        st = lib.la_ssm_bwd(at(x), at(dt), a, at(b), at(c), k, at(gate), bias, at(dy), strides, code, B, T, D, N, G,
+                            LA_SSM_SOFTPLUS if softplus else 0, _dense(h0, "h0", state, f32, dev),
+                            _dense(positions, "positions", (B, T), torch.int32, dev),
+                            _dense(dh_T, "dh_T", state, f32, dev), at(dx), at(ddt), at(dA), at(db), at(dc), at(dskip),
+                            at(dgate), at(dbias), at(dh0), _ptr(workspace), ws_bytes, s)
+    _check(st, "la_ssm_bwd")
+    return dx, ddt, dA, db, dc, dskip, dgate, dbias, dh0
+
+
+def ssm_step(x, dt, A, b, c, h, *, skip=None, gate=None, dt_bias=None, softplus=True, out=None, h_out=None,
+             stream=None):
+    """One token of ssm_fwd: x, dt, gate [B,D], b, c [B,N] or [B,G,N]; the state h fp32
+    [B,D,N] moves on in place or into h_out.  Returns y [B,D]."""
+    N, G, code, dev, weights = _ssm_shape(x, dt, A, b, c, skip, gate, dt_bias, 2)
+    B, D = x.shape
+    f32, state = torch.float32, (B, D, N)
+    with _launch_on(dev, stream) as s:
+        out, y = _output(out, "out", (B, D), x.dtype, dev)
+        old = _dense(h, "h", state, f32, dev)
+        new = old if h_out is None else _dense(h_out, "h_out", state, f32, dev)
+        strides = _row_strides((("x", x), ("dt", dt), ("b", b), ("c", c), ("gate", gate)), 1)
+        a, k, bias = weights
+        st = _load().la_ssm_step(x.data_ptr(), dt.data_ptr(), a, b.data_ptr(), c.data_ptr(), k,
+                                 None if gate is None else gate.data_ptr(), bias, strides, code, B, D, N, G,
+                                 LA_SSM_SOFTPLUS if softplus else 0, old, new, y, s)
+    _check(st, "la_ssm_step")
+    return out
+
+
+def _block_args(o, residual, post_norm, post_weight, gate, pre_norm, pre_weight, center):
+    """Checked arguments of the block_norm calls: (type codes, residual's type, flags and the
+    addresses of the weights and the gate)."""
+    if o.dim() != 3:
+        raise ValueError(f"o is {tuple(o.shape)}; [B,T,D] is needed")
+    B, T, D = o.shape
+    dev, f32 = o.device, torch.float32
+    rty = o.dtype if residual is None else residual.dtype
+    if rty != o.dtype and rty != f32:
+        raise TypeError(f"the residual must be {o.dtype} or {f32}, not {rty}")
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight is given without post_norm")
+    if pre_weight is not None and not pre_norm:
+        raise ValueError("pre_weight is given without pre_norm")
+    each = gate is not None and gate.dim() == 2
+    flags = ((LA_BLOCK_POST_NORM if post_norm else 0) | (LA_BLOCK_PRE_NORM if pre_norm else 0)
+             | (LA_BLOCK_CENTER if center else 0) | (LA_BLOCK_GATE_EACH if each else 0))
+    code = _dtype_code(o)
+    return code, (LA_DTYPE_F32 if rty == f32 else LA_DTYPE_BF16), rty, flags, (
+        _dense(post_weight, "post_weight", (D,), f32, dev),
+        _dense(gate, "gate", (B, D) if each else (D,), f32, dev), _dense(pre_weight, "pre_weight", (D,), f32, dev))
+
+
+def block_norm_fwd(o, h=None, *, post_norm=False, post_weight=None, gate=None, scale=1.0, residual_scale=1.0,
+                   pre_norm=True, pre_weight=None, center=False, eps=1e-6, h_out=None, out=None, stream=None):
+    """The seam between two blocks of a residual stream, one pass over its rows:
+    h' = residual_scale h + scale gate p, with p = o or (post_norm) its norm times
+    post_weight, and y = norm(h') pre_weight.
+
+    o [B,T,D], h [B,T,D] of o's type or fp32 (None: no residual), rows dense, other strides
+    multiples of 16 bytes; D up to 8192.  post_weight, pre_weight fp32 [D]; gate fp32 [D] or one
+    for each sequence, [B,D].  norm: the row over the root of its mean square (plus eps), with
+    center its mean taken out first.  Returns (h', y); y is None with pre_norm False.  h_out may
+    be h."""
+    code, rcode, rty, flags, (wp, g, wq) = _block_args(o, h, post_norm, post_weight, gate, pre_norm, pre_weight, center)
+    B, T, D = o.shape
+    ty, dev, shape = o.dtype, o.device, (B, T, D)
+    if not pre_norm and out is not None:
+        raise ValueError("out is given without pre_norm")
+    if h is None and h_out is not None:
+        rty = h_out.dtype
+        if rty != ty and rty != torch.float32:
+            raise TypeError(f"the residual must be {ty} or {torch.float32}, not {rty}")
+        rcode = LA_DTYPE_F32 if rty == torch.float32 else LA_DTYPE_BF16
+    with _launch_on(dev, stream) as s:
+        h_out = _place(h_out, shape, rty, dev)
+        out = _place(out, shape, ty, dev) if pre_norm else None
+        st = _load().la_block_norm_fwd(*_tokens(o, "o", shape, ty, dev), code, *_tokens(h, "h", shape, rty, dev), rcode,
+                                       wp, g, wq, B, T, D, flags, float(scale), float(residual_scale), float(eps),
+                                       *_tokens(h_out, "h_out", shape, rty, dev), *_tokens(out, "out", shape, ty, dev),
+                                       s)
+    _check(st, "la_block_norm_fwd")
+    return h_out, out
+
+
+def block_norm_bwd(o, h_out, dy, dh_out=None, *, post_norm=False, post_weight=None, gate=None, scale=1.0,
+                   residual_scale=1.0, pre_norm=True, pre_weight=None, center=False, eps=1e-6, d_o=None, dh=None,
+                   residual_grad=True, weight_grads=True, workspace=None, stream=None):
+    """Gradients of block_norm_fwd from its input o and its output h_out, for dy (that of y;
+    None with pre_norm False) and dh_out (that of h_out, or None): (d_o [B,T,D], dh [B,T,D]
+    of h_out's type, dpost_weight [D], dgate like gate, dpre_weight [D]).  A gradient is None
+    where its input is; the last three with weight_grads False, dh with residual_grad False (a
+    call that had no residual).  d_o and dh may be given, with strides; dh may be dh_out."""
+    code, rcode, rty, flags, (wp, g, wq) = _block_args(o, h_out, post_norm, post_weight, gate, pre_norm, pre_weight,
+                                                       center)
+    B, T, D = o.shape
+    ty, dev, shape, f32 = o.dtype, o.device, (B, T, D), torch.float32
+    if (dy is not None) != bool(pre_norm):
+        raise ValueError("dy belongs to pre_norm: give both or neither")
+    lib = _load()
+    with _launch_on(dev, stream) as s:
+        d_o = _place(d_o, shape, ty, dev)
+        dh = _place(dh, shape, rty, dev) if residual_grad or dh is not None else None
+        small = lambda t: torch.empty_like(t) if weight_grads and t is not None else None
+        dwp, dg, dwq = small(post_weight), small(gate), small(pre_weight)
+        need = 0
+        if dwp is not None or dg is not None or dwq is not None:
+            need = int(lib.la_block_norm_bwd_workspace_size(B, T, D, code, flags))
+        workspace, ws_bytes = _scratch(workspace, need, dev)
+        st = lib.la_block_norm_bwd(*_tokens(o, "o", shape, ty, dev), code,
+                                   *_tokens(h_out, "h_out", shape, rty, dev), rcode,
+                                   *_tokens(dy, "dy", shape, ty, dev), *_tokens(dh_out, "dh_out", shape, rty, dev),
+                                   wp, g, wq, B, T, D, flags, float(scale), float(residual_scale), float(eps),
+                                   *_tokens(d_o, "d_o", shape, ty, dev), *_tokens(dh, "dh", shape, rty, dev),
+                                   _ptr(dwp), _ptr(dg), _ptr(dwq), _ptr(workspace), ws_bytes, s)
+    _check(st, "la_block_norm_bwd")
+    return d_o, dh, dwp, dg, dwq
+
+
+__all__ = ["short_conv_fwd", "short_conv_bwd", "short_conv_step", "ssm_fwd", "ssm_bwd", "ssm_step",
+           "block_norm_fwd", "block_norm_bwd", "LA_CONV_SILU", "LA_SSM_SOFTPLUS", "LA_BLOCK_POST_NORM",
+           "LA_BLOCK_PRE_NORM", "LA_BLOCK_CENTER", "LA_BLOCK_GATE_EACH",
+           "qk_rotate_fwd", "qk_rotate_bwd", "rotary_frequencies", "head_gate_fwd", "head_gate_bwd",
            "scan_fwd", "scan_bwd", "scan_step", "LA_QK_NORM", "LA_QK_ADJACENT", "LA_GATE_CENTER",
            "chunk_fwd", "chunk_bwd", "chunk_fwd_noalloc", "recurrent_step", "state_init", "workspace_size", "chunk_fwd_host",
            "host_arena_size",

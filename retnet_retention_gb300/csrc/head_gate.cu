@@ -64,18 +64,6 @@ struct Cursor {
     }
 };
 
-// sigma(g) = 1 / (1 + e^-g); e^-g may overflow to infinity, whose reciprocal is 0.  For
-// bf16 results e^-g is one 2^x of the scaled argument, off by (2 + 1.2 |g|) ulp of
-// fp32: below 2^-16 wherever sigma is not 0, against their 2^-9.  For fp32 it is expf.
-template <typename T>
-__device__ __forceinline__ float sigmoid(float g) {
-    float e, s;
-    if (sizeof(T) == 2) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    else e = expf(-g);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));  // 1 ulp
-    return s;
-}
-
 // x <- its normed row, returns r.  Lanes past the row hold zeros and keep them.
 template <int G>
 __device__ __forceinline__ float norm_row(float2 (&x)[4], bool on, int center, float inv_d, float eps) {

@@ -152,6 +152,58 @@ struct RecurrenceArgs {
     int* dev_status;                    // or null
 };
 
+// The short causal convolution over [B][T][D], its gradients or its single step;
+// validated by the ABI layer.  Strides in elements: batch, token.
+struct ShortConvArgs {
+    const void *x, *dy;
+    long long x_strides[2], dy_strides[2];
+    const float *weight, *bias;         // [D][W], [D] or null
+    int B, T, D, W;
+    bool bf16, silu;
+    const void *state, *dstate_T;       // [B][W-1][D] or null
+    const int* positions;               // device [B][T] or null
+    void *y, *state_out;                // state_out may be null
+    long long y_strides[2];
+    void *dx, *dstate;                  // dstate may be null
+    long long dx_strides[2];
+    float *dweight, *dbias;             // or null
+    void* workspace;
+};
+
+// The selective scan over [B][T][D], its gradients or its single step; validated by the
+// ABI layer.  Strides in elements: batch, token.
+struct SsmArgs {
+    const void *x, *dt, *bm, *cm, *gate, *dy;  // gate may be null
+    long long x_strides[2], dt_strides[2], b_strides[2], c_strides[2], gate_strides[2], dy_strides[2];
+    const float *A, *skip, *dt_bias;    // [D][N]; [D] or null
+    int B, T, D, N, G;
+    bool bf16, softplus;
+    const int* positions;               // device [B][T] or null
+    const float *h0, *dh_T;             // [B][D][N] or null
+    void* y;
+    long long y_strides[2];
+    float* h_out;                       // or null
+    void *dx, *ddt, *db, *dc, *dgate;
+    long long dx_strides[2], ddt_strides[2], db_strides[2], dc_strides[2], dgate_strides[2];
+    float *dA, *dskip, *ddt_bias, *dh0;  // or null
+    void* workspace;
+};
+
+// The norms after and before a block with its gate and the residual; validated by the
+// ABI layer.  Strides in elements: batch, token.
+struct BlockNormArgs {
+    const void *o, *h, *dy, *dh;        // h: the residual (may be null), backward h'; dh may be null
+    long long o_strides[2], h_strides[2], dy_strides[2], dh_strides[2];
+    const float *post_weight, *gate, *pre_weight;  // or null
+    int B, T, D;
+    bool bf16, residual_bf16, post, pre, center, gate_each;  // gate_each: [B][D], else [D]
+    float scale, residual_scale, eps;
+    void *h_out, *y, *d_o, *d_res;      // h_out, y, d_res may be null
+    long long h_out_strides[2], y_strides[2], d_o_strides[2], d_res_strides[2];
+    float *dpost_weight, *dgate, *dpre_weight;  // or null
+    void* workspace;
+};
+
 // The test and diagnostic switches of la_debug_set (abi.cu).
 int opt_path();           // 0 automatic, 1 CUDA cores, 2 tensor cores
 bool opt_tc_lockstep();   // the lockstep kernel instead of the pipelined one
@@ -219,5 +271,26 @@ cudaError_t launch_head_gate_bwd(const HeadGateArgs& a, cudaStream_t s);
 cudaError_t launch_scan_fwd(const RecurrenceArgs& a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const RecurrenceArgs& a, cudaStream_t s);
 cudaError_t launch_scan_step(const RecurrenceArgs& a, cudaStream_t s);
+
+// short_conv.cu: the short causal convolution, its gradients and its single step (T = 1
+// of x and state -> y, state_out)
+size_t short_conv_bwd_workspace_bytes(const ShortConvArgs& a);
+cudaError_t launch_short_conv_fwd(const ShortConvArgs& a, cudaStream_t s);
+cudaError_t launch_short_conv_bwd(const ShortConvArgs& a, cudaStream_t s);
+cudaError_t launch_short_conv_step(const ShortConvArgs& a, cudaStream_t s);
+
+// ssm.cu: the selective scan, its gradients and its single step (T = 1 of x, dt, b, c,
+// gate and h0 -> y, h_out)
+size_t ssm_workspace_bytes(const SsmArgs& a);
+size_t ssm_bwd_workspace_bytes(const SsmArgs& a);
+cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t s);
+cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t s);
+cudaError_t launch_ssm_step(const SsmArgs& a, cudaStream_t s);
+
+// block_norm.cu: the norms after and before a block with its gate and the residual, and
+// their gradients
+size_t block_norm_bwd_workspace_bytes(const BlockNormArgs& a);
+cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, cudaStream_t s);
+cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, cudaStream_t s);
 
 }  // namespace la

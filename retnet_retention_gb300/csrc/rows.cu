@@ -1,7 +1,7 @@
 // Sums of per-CTA partial rows: the second step of the weight gradients of
-// qk_rotate and head_gate.  Each CTA of the first kernel leaves one fp32 row; the
-// order of the additions is fixed by the launch shape, so results repeat bit for
-// bit (no atomics).
+// qk_rotate, head_gate, short_conv, ssm and block_norm.  Each CTA of the first kernel
+// leaves one fp32 row; the order of the additions is fixed by the launch shape, so
+// results repeat bit for bit (no atomics).
 #include "rows.cuh"
 #include "tc_ptx.cuh"
 #include "trace.h"
@@ -13,22 +13,19 @@ namespace {
 constexpr int kSumWarps = 32;
 
 struct Sums {
-    const float* part[2];
-    float* out[2];
-    int rows[2];
+    PartialSum of[kPartialSums];
 };
 
 // One CTA per 32 columns; warp w adds rows w, w + 32, ... of its lane's column.
-__global__ void __launch_bounds__(kSumWarps * 32) partial_sum_kernel(const __grid_constant__ Sums s,
-                                                                     int cols) {
+__global__ void __launch_bounds__(kSumWarps * 32) partial_sum_kernel(const __grid_constant__ Sums s) {
     __shared__ float red[kSumWarps][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, which = blockIdx.y;
     const int c = blockIdx.x * 32 + lane;
-    const float* part = s.part[which];
-    float* out = s.out[which];
-    const int rows = s.rows[which];
+    const float* part = s.of[which].part;
+    float* out = s.of[which].out;
+    const int rows = s.of[which].rows, cols = s.of[which].cols;
+    if (!out || (int)blockIdx.x * 32 >= cols) return;
     tc::griddep_wait();  // the rows come from the previous kernel in the stream
-    if (!out) return;
     float acc = 0.f;
     if (c < cols) {
         constexpr int kBatch = 24;  // loads in flight together
@@ -55,20 +52,32 @@ __global__ void __launch_bounds__(kSumWarps * 32) partial_sum_kernel(const __gri
 
 }  // namespace
 
-cudaError_t launch_partial_sum(const float* part0, int rows0, float* out0, const float* part1, int rows1,
-                               float* out1, int cols, cudaStream_t s) {
-    const Sums sums = {{part0, part1}, {out0, out1}, {rows0, rows1}};
+cudaError_t launch_partial_sums(const PartialSum* sums, int n, cudaStream_t s) {
+    Sums all = {};
+    int cols = 0, used = 0;
+    for (int i = 0; i < n; ++i) {
+        if (!sums[i].out) continue;
+        all.of[used++] = sums[i];
+        cols = sums[i].cols > cols ? sums[i].cols : cols;
+    }
+    if (used == 0) return cudaSuccess;
     TraceScope trace("partial_sum_kernel", s);
     cudaLaunchAttribute attr[1];  // scheduled while the kernel before it finishes
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((cols + 31) / 32, out1 ? 2 : 1);
+    cfg.gridDim = dim3((cols + 31) / 32, used);
     cfg.blockDim = dim3(kSumWarps * 32);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, partial_sum_kernel, sums, cols);
+    return cudaLaunchKernelEx(&cfg, partial_sum_kernel, all);
+}
+
+cudaError_t launch_partial_sum(const float* part0, int rows0, float* out0, const float* part1, int rows1,
+                               float* out1, int cols, cudaStream_t s) {
+    const PartialSum sums[2] = {{part0, out0, rows0, cols}, {part1, out1, rows1, cols}};
+    return launch_partial_sums(sums, 2, s);
 }
 
 int sm_count() {

@@ -184,6 +184,18 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
+// sigma(g) = 1 / (1 + e^-g); e^-g may overflow to infinity, whose reciprocal is 0.  For
+// bf16 results e^-g is one 2^x of the scaled argument, off by (2 + 1.2 |g|) ulp of
+// fp32: below 2^-16 wherever sigma is not 0, against their 2^-9.  For fp32 it is expf.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, s;
+    if (sizeof(T) == 2) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    else e = expf(-g);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));  // 1 ulp
+    return s;
+}
+
 // m / T by a multiplication, exact for m < 2^31.
 struct Divide {
     unsigned T, magic, shift;  // magic = ceil(2^shift / T), shift = 31 + ceil(log2 T)
@@ -207,7 +219,14 @@ inline int group_lanes(int d) {  // the smallest power of two >= d / 8
 }
 
 // rows.cu: out[c] = sum over the rows of part[rows][cols], in a fixed order, for up to
-// two such pairs at once (a null out is left out).
+// kPartialSums such sums at once (a null out is left out).
+struct PartialSum {
+    const float* part;
+    float* out;
+    int rows, cols;
+};
+constexpr int kPartialSums = 4;
+cudaError_t launch_partial_sums(const PartialSum* sums, int n, cudaStream_t s);
 cudaError_t launch_partial_sum(const float* part0, int rows0, float* out0, const float* part1, int rows1,
                                float* out1, int cols, cudaStream_t s);
 

@@ -1,0 +1,351 @@
+// The selective scan: a state of N numbers for each of D channels,
+//
+//   delta = softplus(dt + dt_bias),  h_t = exp(delta A) h_(t-1) + delta x b_t,
+//   y_t = (c_t . h_t + skip x) gate sigmoid(gate),
+//
+// with A [D][N], and b_t, c_t [N] shared by a group's channels; its gradients
+// (csrc/ssm_bwd.cuh) and its single step.  A document's first token (positions = 0) drops
+// the old state by a selection.
+//
+// Bound by the instructions of the state: for each of its entries and tokens one 2^x and four
+// fp32 operations (delta A, delta x b, h, c h); x, dt, gate and y are 8 bytes (bf16) for N of
+// them.  A walk goes token by token with the state in registers (csrc/ssm.cuh).  Where the
+// channels are too few for the card a sequence is cut into chunks: one walk leaves each
+// chunk's state from zero and its sum of delta (the decay over a chunk is exp(A sum)), a
+// small kernel puts them together, and a second walk writes y from the state entering each
+// chunk.  The gradients always work chunk by chunk.
+#include <algorithm>
+
+#include "ssm.cuh"
+
+namespace la {
+
+namespace ssm {
+
+namespace {
+
+// ---- the chunks of a sequence put together ---------------------------------------------
+
+constexpr int kJoinWarps = 32;
+
+// The state after a run of decay P (0: dropped) from s.
+__device__ __forceinline__ float after(float P, float b, float s) { return P == 0.f ? b : fmaf(P, s, b); }
+
+// v[b][chunk][D][N]: what a chunk adds becomes what enters it, in place; from the first
+// chunk with s0 before it, or from the last with s0 behind it.  A CTA per 32 columns of [D][N] of
+// a sequence; each warp puts a run of chunks together, then walks them again.
+__global__ void __launch_bounds__(kJoinWarps * 32) ssm_join_kernel(
+    float* forward, const float* forward_s0, float* backward, const float* backward_s0, const float* chunk_s,
+    const float* __restrict__ A, int D, int N, int chunks) {
+    __shared__ float2 runs[kJoinWarps][32];
+    const bool back = forward == nullptr || blockIdx.z == 1;
+    float* v = back ? backward : forward;
+    const float* s0 = back ? backward_s0 : forward_s0;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const long long col = (long long)blockIdx.x * 32 + lane, cols = (long long)D * N, b = blockIdx.y;
+    const int d = (int)(col / N);
+    const float a = A[col] * kLog2e;
+    const int each = (chunks + warps - 1) / warps;
+    const int k0 = min(w * each, chunks), k1 = min(k0 + each, chunks);
+    auto at = [&](int k) { return b * chunks + (back ? chunks - 1 - k : k); };
+    auto decay = [&](long long i) {
+        const float s = chunk_s[i * D + d];
+        return s == INFINITY ? 0.f : exp2_fast(s * a);
+    };
+    float P = 1.f, sum = 0.f;
+    if (warps > 1) {
+#pragma unroll 4
+        for (int k = k0; k < k1; ++k) {
+            const long long i = at(k);
+            const float e = decay(i);
+            sum = after(e, v[i * cols + col], sum);
+            P *= e;
+        }
+        runs[w][lane] = make_float2(P, sum);
+        __syncthreads();
+    }
+    float s = s0 ? s0[b * cols + col] : 0.f;
+    for (int k = 0; k < w; ++k) s = after(runs[k][lane].x, runs[k][lane].y, s);
+#pragma unroll 4
+    for (int k = k0; k < k1; ++k) {
+        const long long i = at(k);
+        const float e = decay(i), add = v[i * cols + col];
+        v[i * cols + col] = s;
+        s = after(e, add, s);
+    }
+}
+
+// ---- db, dc from the tiles' sums -------------------------------------------------------
+
+template <typename T>
+__global__ void __launch_bounds__(256) ssm_shared_grad_kernel(const float* part, long long tokens, int T_, int N,
+                                                              int tiles, SsmRows db, SsmRows dc) {
+    const int g = blockIdx.y;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // of [tokens][2 N / 4]
+    const int quads = 2 * N / 4;
+    if (i >= tokens * quads) return;
+    const long long m = i / quads, b = m / T_, t = m - b * T_;
+    const int col = (int)(i % quads) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < tiles; ++k) {
+        const float4 r = *reinterpret_cast<const float4*>(part + (((long long)g * tiles + k) * tokens + m) * (2 * N) + col);
+        v.x += r.x; v.y += r.y; v.z += r.z; v.w += r.w;
+    }
+    const SsmRows& to = col >= N ? dc : db;
+    T* out = (T*)to.p + b * to.b + t * to.t + g * N + col % N;
+    store_elem(out, 0, v.x);
+    store_elem(out, 1, v.y);
+    store_elem(out, 2, v.z);
+    store_elem(out, 3, v.w);
+}
+
+// ---- one token -------------------------------------------------------------------------
+
+// Four states a lane: a channel's N / 4 lanes lie side by side; a CTA keeps its channels
+// and walks sequences, so that A is read once.
+template <typename T>
+__global__ void __launch_bounds__(128) ssm_step_kernel(const __grid_constant__ SsmParams p) {
+    const int lanes = p.N / 4, j = threadIdx.x % lanes;
+    const int c = (int)((blockIdx.x * 128u + threadIdx.x) / (unsigned)lanes);
+    const bool on = c < p.D;
+    const int cc = on ? c : 0, g = cc / p.channels;
+    const float4 a4 = __ldg(reinterpret_cast<const float4*>(p.A + (size_t)cc * p.N) + j);
+    const float A[4] = {a4.x * kLog2e, a4.y * kLog2e, a4.z * kLog2e, a4.w * kLog2e};
+    const float skip = p.skip ? p.skip[cc] : 0.f, bias = p.bias ? p.bias[cc] : 0.f;
+    constexpr int R = 4;  // sequences whose loads are in flight
+    for (int b0 = blockIdx.y * R; b0 < p.B; b0 += gridDim.y * R) {
+        float4 h[R];
+        float x[R], dt[R], z[R], bv[R][4], cv[R][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const long long b = min(b0 + r, p.B - 1);
+            h[r] = *(reinterpret_cast<const float4*>(p.h0 + (b * p.D + cc) * p.N) + j);
+            x[r] = load_elem((const T*)p.x.p + b * p.x.b, cc);
+            dt[r] = load_elem((const T*)p.dt.p + b * p.dt.b, cc);
+            z[r] = p.gate.p ? load_elem((const T*)p.gate.p + b * p.gate.b, cc) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                bv[r][i] = load_elem((const T*)p.bm.p + b * p.bm.b, g * p.N + 4 * j + i);
+                cv[r][i] = load_elem((const T*)p.cm.p + b * p.cm.b, g * p.N + 4 * j + i);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float v = dt[r] + bias, delta = p.softplus ? softplus<T>(v) : v, in = delta * x[r];
+            float s[4] = {h[r].x, h[r].y, h[r].z, h[r].w}, y = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[i] = fmaf(exp2_fast(delta * A[i]), s[i], in * bv[r][i]);
+                y = fmaf(cv[r][i], s[i], y);
+            }
+            for (int gap = lanes / 2; gap > 0; gap /= 2) y += __shfl_xor_sync(0xffffffffu, y, gap);
+            y = fmaf(skip, x[r], y);
+            if (p.gate.p) y *= z[r] * sigmoid<T>(z[r]);
+            const long long b = b0 + r;
+            if (on && b < p.B) {
+                *(reinterpret_cast<float4*>(p.h_out + (b * p.D + cc) * p.N) + j) = make_float4(s[0], s[1], s[2], s[3]);
+                if (j == 0) store_elem((T*)p.y.p, b * p.D + cc, y);
+            }
+        }
+    }
+}
+
+// ---- plans -----------------------------------------------------------------------------
+
+SsmParams params(const SsmArgs& a) {
+    auto rows = [](const void* p, const long long* s) { return SsmRows{p, s[0], s[1]}; };
+    SsmParams p = {};
+    p.x = rows(a.x, a.x_strides);
+    p.dt = rows(a.dt, a.dt_strides);
+    p.gate = rows(a.gate, a.gate_strides);
+    p.bm = rows(a.bm, a.b_strides);
+    p.cm = rows(a.cm, a.c_strides);
+    p.dy = rows(a.dy, a.dy_strides);
+    p.y = rows(a.y, a.y_strides);
+    p.A = a.A; p.skip = a.skip; p.bias = a.dt_bias;
+    p.positions = a.positions;
+    p.h0 = a.h0; p.h_out = a.h_out;
+    p.B = a.B; p.T = a.T; p.D = a.D; p.N = a.N; p.G = a.G;
+    p.channels = a.D / a.G;
+    p.softplus = a.softplus;
+    return p;
+}
+
+// Lanes a channel, and chunks.  More lanes a channel cost little (120 to 128 instructions a
+// token and channel against 112), a cut costs a second walk (75): so first lanes, then chunks.
+struct Plan {
+    int lanes, tiles, chunks, chunk;
+};
+
+Plan forward_plan(const SsmArgs& a) {
+    Plan p;
+    const long long want = (long long)sm_count() * 8;  // warps
+    const int most = std::min(8, a.N / 4);
+    const long long channels = (long long)a.B * a.D;
+    p.lanes = std::max(1, a.N / 16);
+    while (p.lanes < most && channels * p.lanes < want * 32) p.lanes *= 2;
+    const int cta = channels_cta(p.lanes);
+    p.tiles = (a.D / a.G + cta - 1) / cta;
+    const long long warps = (long long)a.B * a.G * p.tiles * kWarps;
+    p.chunks = 1;
+    p.chunk = a.T;
+    if (warps < want && a.T >= 256) {
+        const long long cut = std::min<long long>((2 * want + warps - 1) / warps, a.T / 128);
+        p.chunk = (int)(((a.T + cut - 1) / cut + kTile - 1) / kTile * kTile);
+        p.chunks = (a.T + p.chunk - 1) / p.chunk;
+    }
+    return p;
+}
+
+Plan backward_plan(const SsmArgs& a, int channels) {
+    Plan p;
+    p.lanes = std::max(1, std::min(8, a.N / 8));
+    p.tiles = (a.D / a.G + channels - 1) / channels;
+    const long long ctas = (long long)a.B * a.G * p.tiles, want = (long long)sm_count() * 16;
+    const long long cut = std::max<long long>(1, std::min<long long>((want + ctas - 1) / ctas, a.T / 64));
+    p.chunk = (int)(((a.T + cut - 1) / cut + kTile - 1) / kTile * kTile);
+    p.chunks = (a.T + p.chunk - 1) / p.chunk;
+    return p;
+}
+
+void use(SsmParams* p, const Plan& plan) {
+    p->chunks = plan.chunks;
+    p->chunk = plan.chunk;
+    p->tiles = plan.tiles;
+}
+
+// Regions of a workspace, one behind the other, each at a multiple of 256 bytes.
+struct Workspace {
+    char* at;
+    size_t used = 0;
+    float* take(size_t floats) {
+        float* p = at ? (float*)(at + used) : nullptr;
+        used += (floats * sizeof(float) + 255) / 256 * 256;
+        return p;
+    }
+};
+
+size_t forward_workspace(const SsmArgs& a, const Plan& plan, SsmParams* p) {
+    Workspace w{(char*)a.workspace};
+    if (plan.chunks > 1) {
+        p->chunk_h = w.take((size_t)a.B * plan.chunks * a.D * a.N);
+        p->chunk_s = w.take((size_t)a.B * plan.chunks * a.D);
+    }
+    return w.used;
+}
+
+size_t backward_workspace(const SsmArgs& a, const Plan& plan, SsmBwdParams* bp) {
+    Workspace w{(char*)a.workspace};
+    SsmParams& p = bp->f;
+    const size_t chunks = (size_t)a.B * plan.chunks, D = a.D, N = a.N, blocks = (size_t)a.B * ((a.T + kBlock - 1) / kBlock);
+    p.chunk_h = w.take(chunks * D * N);
+    p.chunk_g = w.take(chunks * D * N);
+    p.chunk_s = w.take(chunks * D);
+    p.block_h = w.take(blocks * D * N);
+    p.block_s = w.take(blocks * D);
+    bp->part_A = w.take(chunks * D * N);
+    bp->part_skip = w.take(chunks * D);
+    bp->part_bias = w.take(chunks * D);
+    bp->part_bc = w.take((size_t)a.G * plan.tiles * a.B * a.T * 2 * N);
+    return w.used;
+}
+
+cudaError_t join(const SsmParams& p, bool forward, bool backward, const float* dh_T, cudaStream_t s) {
+    const int warps = std::min(kJoinWarps, std::max(1, p.chunks / 4));
+    const dim3 grid((unsigned)((long long)p.D * p.N / 32), p.B, forward && backward ? 2 : 1);
+    TraceScope trace("ssm_join_kernel", s);
+    ssm_join_kernel<<<grid, warps * 32, 0, s>>>(forward ? p.chunk_h : nullptr, p.h0, p.chunk_g, dh_T, p.chunk_s, p.A,
+                                                p.D, p.N, p.chunks);
+    return cudaGetLastError();
+}
+
+unsigned grid_of(const SsmParams& p) { return (unsigned)((long long)p.tiles * p.G * p.chunks * p.B); }
+
+int bwd_channels(int N) { return 4 * 2 * (128 / N); }  // of a CTA of the gradients' walk
+
+template <typename T>
+cudaError_t forward(const SsmArgs& a, cudaStream_t s) {
+    SsmParams p = params(a);
+    const Plan plan = forward_plan(a);
+    use(&p, plan);
+    forward_workspace(a, plan, &p);
+    if (plan.chunks > 1) {
+        cudaError_t e = launch_scan<T, kState>(p, plan.lanes, grid_of(p), s);
+        if (e == cudaSuccess) e = join(p, true, false, nullptr, s);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_scan<T, kForward>(p, plan.lanes, grid_of(p), s);
+}
+
+template <typename T>
+cudaError_t backward(const SsmArgs& a, cudaStream_t s) {
+    SsmBwdParams bp = {};
+    bp.f = params(a);
+    SsmParams& p = bp.f;
+    const Plan plan = backward_plan(a, bwd_channels(a.N));
+    use(&p, plan);
+    backward_workspace(a, plan, &bp);
+    p.blocks = (a.T + kBlock - 1) / kBlock;
+    SsmParams summary = p;
+    const int cta = channels_cta(plan.lanes);
+    summary.tiles = (p.channels + cta - 1) / cta;
+    cudaError_t e = launch_scan<T, kSummary>(summary, plan.lanes, grid_of(summary), s);
+    if (e == cudaSuccess) e = join(p, true, true, a.dh_T, s);
+    if (e != cudaSuccess) return e;
+    auto rows = [](void* q, const long long* st) { return SsmRows{q, st[0], st[1]}; };
+    bp.dx = rows(a.dx, a.dx_strides);
+    bp.ddt = rows(a.ddt, a.ddt_strides);
+    bp.dgate = rows(a.dgate, a.dgate_strides);
+    bp.dh0 = a.dh0;
+    if (!a.dA) bp.part_A = nullptr;
+    if (!a.dskip) bp.part_skip = nullptr;
+    if (!a.ddt_bias) bp.part_bias = nullptr;
+    e = launch_gradients<T>(bp, grid_of(p), s);
+    if (e != cudaSuccess) return e;
+    const int parts = p.B * p.chunks;
+    const PartialSum sums[3] = {{bp.part_A, a.dA, parts, a.D * a.N},
+                                {bp.part_skip, a.dskip, parts, a.D},
+                                {bp.part_bias, a.ddt_bias, parts, a.D}};
+    e = launch_partial_sums(sums, 3, s);
+    if (e != cudaSuccess) return e;
+    const long long tokens = (long long)a.B * a.T, quads = tokens * (2 * a.N / 4);
+    TraceScope trace("ssm_shared_grad_kernel", s);
+    ssm_shared_grad_kernel<T><<<dim3((unsigned)((quads + 255) / 256), a.G), 256, 0, s>>>(
+        bp.part_bc, tokens, a.T, a.N, p.tiles, rows(a.db, a.db_strides), rows(a.dc, a.dc_strides));
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace ssm
+
+size_t ssm_workspace_bytes(const SsmArgs& a) {
+    SsmParams p = {};
+    return ssm::forward_workspace(a, ssm::forward_plan(a), &p);
+}
+
+size_t ssm_bwd_workspace_bytes(const SsmArgs& a) {
+    SsmBwdParams p = {};
+    return ssm::backward_workspace(a, ssm::backward_plan(a, ssm::bwd_channels(a.N)), &p);
+}
+
+cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t s) {
+    return a.bf16 ? ssm::forward<__nv_bfloat16>(a, s) : ssm::forward<float>(a, s);
+}
+
+cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t s) {
+    return a.bf16 ? ssm::backward<__nv_bfloat16>(a, s) : ssm::backward<float>(a, s);
+}
+
+cudaError_t launch_ssm_step(const SsmArgs& a, cudaStream_t s) {
+    const SsmParams p = ssm::params(a);
+    const long long threads = (long long)a.D * (a.N / 4);
+    const unsigned blocks = (unsigned)((threads + 127) / 128);
+    const long long rows = (a.B + 3) / 4, want = ((long long)sm_count() * 16 + blocks - 1) / blocks;
+    const dim3 grid(blocks, (unsigned)std::max(1ll, std::min(rows, std::min(want, 65535ll))));
+    TraceScope trace("ssm_step_kernel", s);
+    if (a.bf16) ssm::ssm_step_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(p);
+    else ssm::ssm_step_kernel<float><<<grid, 128, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace la

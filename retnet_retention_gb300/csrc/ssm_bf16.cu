@@ -1,0 +1,19 @@
+// The selective scan's walks over bf16 tensors.
+#include "ssm.cuh"
+
+namespace la::ssm {
+
+template <>
+cudaError_t launch_scan<__nv_bfloat16, kForward>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<__nv_bfloat16, kForward>(p, lanes, grid, s);
+}
+template <>
+cudaError_t launch_scan<__nv_bfloat16, kState>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<__nv_bfloat16, kState>(p, lanes, grid, s);
+}
+template <>
+cudaError_t launch_scan<__nv_bfloat16, kSummary>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<__nv_bfloat16, kSummary>(p, lanes, grid, s);
+}
+
+}  // namespace la::ssm

@@ -1,0 +1,19 @@
+// The selective scan's walks over fp32 tensors.
+#include "ssm.cuh"
+
+namespace la::ssm {
+
+template <>
+cudaError_t launch_scan<float, kForward>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<float, kForward>(p, lanes, grid, s);
+}
+template <>
+cudaError_t launch_scan<float, kState>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<float, kState>(p, lanes, grid, s);
+}
+template <>
+cudaError_t launch_scan<float, kSummary>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<float, kSummary>(p, lanes, grid, s);
+}
+
+}  // namespace la::ssm
