@@ -570,8 +570,8 @@ LA_API la_status la_short_conv_step(const void* x, long long x_stride, la_dtype 
  *   y_t = c_t . h_t + skip x_t    [ times gate sigmoid(gate) ]
  *
  *   x, dt, gate, y  [B][T][D] dtype;  gate may be NULL
- *   b, c      [B][T][G][N] dtype, shared by the D / G channels of a group; G divides D,
- *             N is 8, 16, 32 or 64
+ *   b, c      [B][T][G][N] dtype, shared by the D / G channels of a group, a multiple
+ *             of 8; N is 8, 16, 32 or 64
  *   strides   HOST array of 6 pairs of strides (batch, token) in elements, for x, dt, b,
  *             c, gate and y in this order, or NULL (all dense): rows (of D or G N entries)
  *             dense, strides >= 0 and multiples of 16 bytes, y's rows apart.  The stride of a

@@ -1074,8 +1074,8 @@ def _ssm_shape(x, dt, A, b, c, skip, gate, dt_bias, dims: int):
         raise ValueError(f"x is {tuple(x.shape)}; its rows are not A's {D} channels")
     if N not in (8, 16, 32, 64):
         raise ValueError(f"A has {N} states a channel; 8, 16, 32 or 64 are supported")
-    if G < 1 or D % G:
-        raise ValueError(f"{G} groups do not divide {D} channels")
+    if G < 1 or D % G or D // G % 8:
+        raise ValueError(f"{G} groups do not divide {D} channels into multiples of 8")
     for name, t, shape in (("dt", dt, x.shape), ("gate", gate, x.shape), ("b", b, x.shape[:-1] + b.shape[dims - 1:]),
                            ("c", c, b.shape)):
         if t is not None and (t.shape != shape or t.dtype != ty or t.device != dev):

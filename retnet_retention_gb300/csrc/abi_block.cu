@@ -92,7 +92,7 @@ la_status conv_args(ShortConvArgs* a, const float* weight, const float* bias, la
 
 bool ssm_shape_ok(int B, int T, int D, int N, int G, la_dtype dtype) {
     return rows_shape_ok(B, T, D, dtype) && B <= 65535 && (N == 8 || N == 16 || N == 32 || N == 64) && G >= 1 &&
-           D % G == 0 && (long long)D * N <= INT_MAX && (long long)G * N <= INT_MAX &&
+           D % G == 0 && D / G % 8 == 0 && (long long)D * N <= INT_MAX && (long long)G * N <= INT_MAX &&
            (long long)B * D * N <= kMaxChannels;
 }
 

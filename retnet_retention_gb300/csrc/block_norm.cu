@@ -14,9 +14,11 @@
 //   norm'(v) = r (v - [mean v] - n mean(v n))
 //
 // Bound by HBM: o and h in, h' and y out.  A CTA holds a row in registers (a thread eight
-// neighbouring entries, once or twice), so that both norms cost no second read; the
-// next row's loads are in flight meanwhile.  y is the norm of h' before its rounding; the
-// gradients start from the rounded h' that the forward call left.
+// neighbouring entries, once or twice), so that both norms cost no second read, and the
+// weights of its columns.  The next rows come through a ring in shared memory, each thread's own
+// pieces, copied in the background.  dg and dw_post are one sum over the rows, of alpha dt p, times
+// w_post and g.  y is the norm of h' before its rounding; the gradients start from the rounded
+// h' that the forward call left.
 #include <algorithm>
 
 #include "rows.cuh"
@@ -39,38 +41,45 @@ struct BlockParams {
     float *part_post, *part_gate, *part_pre;  // backward: partial rows, or null
     int B, T, D;
     int rows_cta;                  // rows a CTA holds at once
+    Divide by_T;
     int seq_blocks;                // CTAs a sequence's rows are shared out to (0: of all sequences)
     int post, pre, center, gate_each;
     float alpha, beta, eps;
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float2 (&x)[4]) {
-    floats8<false>(raw8<true>(p, 0, 4), x);
-}
-
-// Sums of N values over the threads of a row, in a fixed order.  `red`: 2 x [warps][N] a
-// row in turn, so that one barrier a sum is enough.
+// Sums of N values over the threads of a row, in a fixed order.  `red`: [2][N][16] floats of
+// the row's slot, its halves in turn, so that one barrier a sum is enough; what a row has fewer than
+// 16 warps is zero from the start.
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* red, int& turn, int warps, int warp) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = group_sum<32>(v[i]);
     if (warps == 1) return;
-    float* to = red + turn * 16 * 2;
+    float* to = red + turn * 32;
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) to[warp * 2 + i] = v[i];
+        for (int i = 0; i < N; ++i) to[i * 16 + warp] = v[i];
     }
     __syncthreads();
-    float s[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = 0.f;
-    for (int k = 0; k < warps; ++k)
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] += to[k * 2 + i];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = s[i];
+    for (int i = 0; i < N; ++i) {
+        const float4* from = reinterpret_cast<const float4*>(to + i * 16);
+        float4 s = from[0];
+        for (int k = 1; k * 4 < warps; ++k) {
+            const float4 r = from[k];
+            s.x += r.x; s.y += r.y; s.z += r.z; s.w += r.w;
+        }
+        v[i] = (s.x + s.y) + (s.z + s.w);
+    }
+}
+
+// Two rows' slots at most share a CTA's barriers; one value's sum uses the first half's 16.
+constexpr int kRedFloats = 2 * 2 * 16;
+
+__device__ __forceinline__ void clear_red(float (*red)[kRedFloats], int slots) {
+    for (int i = threadIdx.x; i < slots * kRedFloats; i += blockDim.x) red[0][i] = 0.f;
+    __syncthreads();
 }
 
 __device__ __forceinline__ float sum8(const float2 (&x)[4]) {
@@ -90,14 +99,67 @@ struct Place {
     }
 };
 
+// A row's place, walking by a fixed number of rows.
+struct Walk {
+    unsigned b, t, leap_b, leap_t, T;
+    __device__ Walk(const Divide& by_T, unsigned row, unsigned leap) : T(by_T.T) {
+        by_T(row, &b, &t);
+        by_T(leap, &leap_b, &leap_t);
+    }
+    __device__ __forceinline__ void next() {
+        b += leap_b;
+        t += leap_t;
+        if (t >= T) t -= T, ++b;
+    }
+    template <typename E>
+    __device__ __forceinline__ E* at(const Rows& r) const {
+        return (E*)r.p + b * r.b + t * r.t;
+    }
+};
+
+// A thread's eight entries into its slot in the background.
+template <typename E>
+__device__ __forceinline__ void copy8(E* slot, const E* from) {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(E) / 2; ++k) copy16((char*)slot + 16 * k, (const char*)from + 16 * k, true);
+}
+
+template <bool MINUS_MEAN, int P>
+__device__ __forceinline__ float normed(float2 (&x)[P][4], const bool (&on)[P], float inv_d, float eps, float* red,
+                                        int& turn, const Place& at) {
+    if (MINUS_MEAN) {
+        float s[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < P; ++i) s[0] += sum8(x[i]);
+        row_sums<1>(s, red, turn, at.warps, at.warp);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (on[i])
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[i][j] = __fadd2_rn(x[i][j], both(-s[0] * inv_d));
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < P; ++i) q[0] += dot8(x[i], x[i]);
+    row_sums<1>(q, red, turn, at.warps, at.warp);
+    return rsqrtf(q[0] * inv_d + eps);
+}
+
+constexpr int kRing = 3;
+
 // T: o and y; R: the residual stream.  P pieces of eight entries a thread.
-template <typename T, typename R, int P>
-__global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__ BlockParams p) {
-    __shared__ float red[4][2 * 16 * 2];
+template <typename T, typename R, int P, int THREADS, bool CENTER>
+__global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_constant__ BlockParams p) {
+    __shared__ __align__(16) float red[4][kRedFloats];
+    clear_red(red, 4);
+    extern __shared__ __align__(16) unsigned char ring[];  // [kRing][P][threads] of T's eight, then of R's
     const Place at(p.rows_cta);
     const int width = at.warps * 32 * 8;  // entries of a piece of the row
-    const long long rows = (long long)p.B * p.T, leap = (long long)gridDim.x * p.rows_cta;
+    const unsigned rows = p.by_T.T * (unsigned)p.B, leap = gridDim.x * p.rows_cta;
     const float inv_d = 1.f / (float)p.D;
+    T* const slots_o = reinterpret_cast<T*>(ring) + threadIdx.x * 8;
+    R* const slots_h = reinterpret_cast<R*>(ring + (size_t)kRing * P * blockDim.x * 8 * sizeof(T)) + threadIdx.x * 8;
+    const int piece = blockDim.x * 8;
     int turn = 0;
     bool on[P];
     int e[P];
@@ -106,131 +168,168 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__
         e[i] = i * width + at.lane * 8;
         on[i] = e[i] < p.D;
     }
-    Raw8<T> o_next[P];
-    Raw8<R> h_next[P];
-    auto fetch = [&](long long m) {
-        if (m >= rows) return;
-        const long long b = m / p.T, t = m - b * p.T;
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (on[i]) {
-                o_next[i] = raw8<true>((const T*)p.o.p + b * p.o.b + t * p.o.t + e[i], 0, 4);
-                if (p.h.p) h_next[i] = raw8<true>((const R*)p.h.p + b * p.h.b + t * p.h.t + e[i], 0, 4);
-            }
-    };
-    long long m = (long long)blockIdx.x * p.rows_cta + at.slot;
-    fetch(m);
-    for (; m - at.slot < rows; m += leap) {  // the same for every slot
-        const bool row = m < rows;
-        const long long b = row ? m / p.T : 0, t = row ? m - b * p.T : 0;
-        float2 v[P][4], h[P][4];
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] = h[i][j] = make_float2(0.f, 0.f);
-        if (row) {
+    const unsigned first = blockIdx.x * p.rows_cta + at.slot;
+    Walk ahead(p.by_T, first, leap), here = ahead;
+    unsigned m_ahead = first;
+    auto fetch = [&](int slot) {
+        if (m_ahead < rows) {
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 if (on[i]) {
-                    floats8<false>(o_next[i], v[i]);
-                    if (p.h.p) floats8<false>(h_next[i], h[i]);
+                    copy8(slots_o + (slot * P + i) * piece, ahead.at<const T>(p.o) + e[i]);
+                    if (p.h.p) copy8(slots_h + (slot * P + i) * piece, ahead.at<const R>(p.h) + e[i]);
                 }
         }
-        fetch(m + leap);
-        auto normed = [&](float2 (&x)[P][4]) {
-            if (p.center) {
-                float s[1] = {0.f};
+        copies_commit();
+        m_ahead += leap;
+        ahead.next();
+    };
 #pragma unroll
-                for (int i = 0; i < P; ++i) s[0] += sum8(x[i]);
-                row_sums<1>(s, red[at.slot], turn, at.warps, at.warp);
+    for (int i = 0; i < kRing; ++i) fetch(i);
+    float2 gw[P][4], w_pre[P][4];  // alpha g w_post, w_pre
+    unsigned gate_of = 0xffffffffu;
 #pragma unroll
-                for (int i = 0; i < P; ++i)
-                    if (on[i])
+    for (int i = 0; i < P; ++i) row_weights<false>(p.w_pre, on[i], e[i], e[i] + 4, w_pre[i]);
+    int slot = 0;
+    for (unsigned m = first; m - at.slot < rows; m += leap) {  // the same for every slot
+        const bool row = m < rows;
+        const unsigned gate_now = p.gate_each && row ? here.b : 0;
+        if (gate_now != gate_of) {
+            gate_of = gate_now;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) x[i][j] = __fadd2_rn(x[i][j], both(-s[0] * inv_d));
+            for (int i = 0; i < P; ++i) {
+                float2 g[4];
+                row_weights<false>(p.w_post, on[i], e[i], e[i] + 4, gw[i]);
+                row_weights<false>(p.gate ? p.gate + (size_t)gate_of * p.D : nullptr, on[i], e[i], e[i] + 4, g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) gw[i][j] = __fmul2_rn(gw[i][j], __fmul2_rn(g[j], both(p.alpha)));
             }
-            float q[1] = {0.f};
-#pragma unroll
-            for (int i = 0; i < P; ++i) q[0] += dot8(x[i], x[i]);
-            row_sums<1>(q, red[at.slot], turn, at.warps, at.warp);
-            const float r = rsqrtf(q[0] * inv_d + p.eps);
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[i][j] = __fmul2_rn(x[i][j], both(r));
-        };
-        if (p.post) normed(v);
-        const float* gate = p.gate ? p.gate + (p.gate_each ? b * p.D : 0) : nullptr;
+        }
+        float2 v[P][4], h[P][4];
+        copies_wait<kRing - 1>();
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            float2 w[4], g[4];
-            row_weights<false>(p.w_post, on[i], e[i], e[i] + 4, w);
-            row_weights<false>(gate, on[i], e[i], e[i] + 4, g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = h[i][j] = make_float2(0.f, 0.f);
+            if (row && on[i]) {
+                floats8<false>(raw8<true>(slots_o + (slot * P + i) * piece, 0, 4), v[i]);
+                if (p.h.p) floats8<false>(raw8<true>(slots_h + (slot * P + i) * piece, 0, 4), h[i]);
+            }
+        }
+        fetch(slot);
+        slot = slot + 1 == kRing ? 0 : slot + 1;
+        float r = 1.f;
+        if (p.post) r = normed<CENTER, P>(v, on, inv_d, p.eps, red[at.slot], turn, at);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                v[i][j] = __fmul2_rn(__fmul2_rn(v[i][j], w[j]), __fmul2_rn(g[j], both(p.alpha)));
+                v[i][j] = __fmul2_rn(__fmul2_rn(v[i][j], both(r)), gw[i][j]);
                 v[i][j] = __ffma2_rn(h[i][j], both(p.beta), v[i][j]);
             }
-            if (row && on[i] && p.h_out.p)
-                store8<true, false>((R*)p.h_out.p + b * p.h_out.b + t * p.h_out.t + e[i], 0, 4, v[i]);
+            if (row && on[i] && p.h_out.p) store8<true, false>(here.at<R>(p.h_out) + e[i], 0, 4, v[i]);
         }
-        if (!p.pre) continue;
-        normed(v);
+        if (p.pre) {
+            r = normed<CENTER, P>(v, on, inv_d, p.eps, red[at.slot], turn, at);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            float2 w[4];
-            row_weights<false>(p.w_pre, on[i], e[i], e[i] + 4, w);
+            for (int i = 0; i < P; ++i) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(v[i][j], w[j]);
-            if (row && on[i]) store8<true, false>((T*)p.y.p + b * p.y.b + t * p.y.t + e[i], 0, 4, v[i]);
+                for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(__fmul2_rn(v[i][j], both(r)), w_pre[i][j]);
+                if (row && on[i]) store8<true, false>(here.at<T>(p.y) + e[i], 0, 4, v[i]);
+            }
         }
+        here.next();
     }
 }
 
+// Rows of the gradients' ring: one of fp32 entries where a CTA has 512 threads (two would not fit an
+// SM's shared memory).
+template <typename T, int THREADS>
+constexpr int kBwdRingOf = sizeof(T) == 4 && THREADS == 512 ? 1 : 2;
+
 // A CTA takes rows of one sequence where each sequence has its own gate (its sums then
 // belong to that sequence's gradient), else of all.
-template <typename T, typename R, int P>
-__global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_constant__ BlockParams p) {
+template <typename T, typename R, int P, int THREADS, bool CENTER>
+__global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const __grid_constant__ BlockParams p) {
     tc::griddep_launch_dependents();  // the sums' kernel may be scheduled (it waits itself)
-    __shared__ float red[4][2 * 16 * 2];
-    extern __shared__ float columns[];  // [rows_cta][D] for the sums over a CTA's row slots
+    __shared__ __align__(16) float red[4][kRedFloats];
+    clear_red(red, 4);
+    extern __shared__ __align__(16) unsigned char ring[];  // o, dy, h, dh; at the end [rows_cta][D] sums
+    constexpr int kBwdRing = kBwdRingOf<T, THREADS>;
     const Place at(p.rows_cta);
     const int width = at.warps * 32 * 8;
-    const long long first_row = p.seq_blocks ? (long long)(blockIdx.x / p.seq_blocks) * p.T : 0;
-    const long long end_row = p.seq_blocks ? first_row + p.T : (long long)p.B * p.T;
-    const long long block = p.seq_blocks ? blockIdx.x % p.seq_blocks : blockIdx.x;
-    const long long leap = (long long)(p.seq_blocks ? p.seq_blocks : gridDim.x) * p.rows_cta;
+    const unsigned begin = p.seq_blocks ? blockIdx.x / p.seq_blocks * p.by_T.T : 0;
+    const unsigned end = p.seq_blocks ? begin + p.by_T.T : p.by_T.T * (unsigned)p.B;
+    const unsigned leap = (p.seq_blocks ? p.seq_blocks : gridDim.x) * p.rows_cta;
+    const unsigned first = begin + (p.seq_blocks ? blockIdx.x % p.seq_blocks : blockIdx.x) * p.rows_cta + at.slot;
     const float inv_d = 1.f / (float)p.D;
+    const int piece = blockDim.x * 8;
+    T* const slots_t = reinterpret_cast<T*>(ring) + threadIdx.x * 8;  // [kBwdRing][2][P]
+    R* const slots_r = reinterpret_cast<R*>(ring + (size_t)kBwdRing * 2 * P * piece * sizeof(T)) + threadIdx.x * 8;
     int turn = 0;
     bool on[P];
     int e[P];
-    float2 s_post[P][4], s_gate[P][4], s_pre[P][4];
+    float2 s_post[P][4], s_pre[P][4], gw[P][4], w_pre[P][4];  // sums of alpha dt p and dy n; alpha g w_post
+    const float* gate = p.gate ? p.gate + (p.seq_blocks ? (size_t)(blockIdx.x / p.seq_blocks) * p.D : 0) : nullptr;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         e[i] = i * width + at.lane * 8;
         on[i] = e[i] < p.D;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s_post[i][j] = s_gate[i][j] = s_pre[i][j] = make_float2(0.f, 0.f);
+        for (int j = 0; j < 4; ++j) s_post[i][j] = s_pre[i][j] = make_float2(0.f, 0.f);
     }
-    for (long long m = first_row + block * p.rows_cta + at.slot; m - at.slot < end_row; m += leap) {
-        const bool row = m < end_row;
-        const long long b = row ? m / p.T : 0, t = row ? m - b * p.T : 0;
+    Walk ahead(p.by_T, first, leap), here = ahead;
+    unsigned m_ahead = first;
+    auto fetch = [&](int slot) {
+        if (m_ahead < end) {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                if (on[i]) {
+                    copy8(slots_t + (slot * 2 * P + i) * piece, ahead.at<const T>(p.o) + e[i]);
+                    if (p.pre) {
+                        copy8(slots_t + (slot * 2 * P + P + i) * piece, ahead.at<const T>(p.dy) + e[i]);
+                        copy8(slots_r + (slot * 2 * P + i) * piece, ahead.at<const R>(p.h) + e[i]);
+                    }
+                    if (p.dh.p) copy8(slots_r + (slot * 2 * P + P + i) * piece, ahead.at<const R>(p.dh) + e[i]);
+                }
+        }
+        copies_commit();
+        m_ahead += leap;
+        ahead.next();
+    };
+#pragma unroll
+    for (int i = 0; i < kBwdRing; ++i) fetch(i);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        float2 g[4];
+        row_weights<false>(p.w_pre, on[i], e[i], e[i] + 4, w_pre[i]);
+        row_weights<false>(p.w_post, on[i], e[i], e[i] + 4, gw[i]);
+        row_weights<false>(gate, on[i], e[i], e[i] + 4, g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) gw[i][j] = __fmul2_rn(gw[i][j], __fmul2_rn(g[j], both(p.alpha)));
+    }
+    int slot = 0;
+    for (unsigned m = first; m - at.slot < end; m += leap) {
+        const bool row = m < end;
         float2 n[P][4], q[P][4], d[P][4], dt[P][4];  // norm(h'), p, dy, dt
+        copies_wait<kBwdRing - 1>();
 #pragma unroll
         for (int i = 0; i < P; ++i) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) n[i][j] = q[i][j] = d[i][j] = dt[i][j] = make_float2(0.f, 0.f);
             if (row && on[i]) {
-                load8((const T*)p.o.p + b * p.o.b + t * p.o.t + e[i], q[i]);
+                floats8<false>(raw8<true>(slots_t + (slot * 2 * P + i) * piece, 0, 4), q[i]);
                 if (p.pre) {
-                    load8((const R*)p.h.p + b * p.h.b + t * p.h.t + e[i], n[i]);
-                    load8((const T*)p.dy.p + b * p.dy.b + t * p.dy.t + e[i], d[i]);
+                    floats8<false>(raw8<true>(slots_t + (slot * 2 * P + P + i) * piece, 0, 4), d[i]);
+                    floats8<false>(raw8<true>(slots_r + (slot * 2 * P + i) * piece, 0, 4), n[i]);
                 }
-                if (p.dh.p) load8((const R*)p.dh.p + b * p.dh.b + t * p.dh.t + e[i], dt[i]);
+                if (p.dh.p) floats8<false>(raw8<true>(slots_r + (slot * 2 * P + P + i) * piece, 0, 4), dt[i]);
             }
         }
+        fetch(slot);
+        slot = slot + 1 == kBwdRing ? 0 : slot + 1;
         // both rows' norms: means, then squares
-        if (p.center) {
+        if (CENTER) {
             float s[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < P; ++i) s[0] += sum8(n[i]), s[1] += sum8(q[i]);
@@ -254,19 +353,17 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_consta
             s[0] = s[1] = 0.f;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                float2 w[4];
-                row_weights<false>(p.w_pre, on[i], e[i], e[i] + 4, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     n[i][j] = __fmul2_rn(n[i][j], both(rh));
                     s_pre[i][j] = __ffma2_rn(d[i][j], n[i][j], s_pre[i][j]);
-                    d[i][j] = __fmul2_rn(d[i][j], w[j]);
+                    d[i][j] = __fmul2_rn(d[i][j], w_pre[i][j]);
                 }
                 s[0] += dot8(d[i], n[i]);
-                s[1] += sum8(d[i]);
+                if (CENTER) s[1] += sum8(d[i]);
             }
             row_sums<2>(s, red[at.slot], turn, at.warps, at.warp);
-            const float2 along = both(-s[0] * inv_d), mean = both(p.center ? -s[1] * inv_d : 0.f);
+            const float2 along = both(-s[0] * inv_d), mean = both(CENTER ? -s[1] * inv_d : 0.f);
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 if (on[i])
@@ -275,7 +372,6 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_consta
                         dt[i][j] = __ffma2_rn(both(rh), __ffma2_rn(n[i][j], along, __fadd2_rn(d[i][j], mean)),
                                               dt[i][j]);
         }
-        const float* gate = p.gate ? p.gate + (p.gate_each ? b * p.D : 0) : nullptr;
         s[0] = s[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -283,26 +379,20 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_consta
                 float2 out[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) out[j] = __fmul2_rn(dt[i][j], both(p.beta));
-                store8<true, false>((R*)p.d_res.p + b * p.d_res.b + t * p.d_res.t + e[i], 0, 4, out);
+                store8<true, false>(here.at<R>(p.d_res) + e[i], 0, 4, out);
             }
-            float2 w[4], g[4];
-            row_weights<false>(p.w_post, on[i], e[i], e[i] + 4, w);
-            row_weights<false>(gate, on[i], e[i], e[i] + 4, g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 q[i][j] = __fmul2_rn(q[i][j], both(ro));
-                dt[i][j] = __fmul2_rn(dt[i][j], both(p.alpha));
-                s_gate[i][j] = __ffma2_rn(dt[i][j], __fmul2_rn(q[i][j], w[j]), s_gate[i][j]);
-                dt[i][j] = __fmul2_rn(dt[i][j], g[j]);
-                s_post[i][j] = __ffma2_rn(dt[i][j], q[i][j], s_post[i][j]);
-                dt[i][j] = __fmul2_rn(dt[i][j], w[j]);
+                s_post[i][j] = __ffma2_rn(__fmul2_rn(dt[i][j], both(p.alpha)), q[i][j], s_post[i][j]);
+                dt[i][j] = __fmul2_rn(dt[i][j], gw[i][j]);
             }
             s[0] += dot8(dt[i], q[i]);
-            s[1] += sum8(dt[i]);
+            if (CENTER) s[1] += sum8(dt[i]);
         }
         if (p.post) {
             row_sums<2>(s, red[at.slot], turn, at.warps, at.warp);
-            const float2 along = both(-s[0] * inv_d), mean = both(p.center ? -s[1] * inv_d : 0.f);
+            const float2 along = both(-s[0] * inv_d), mean = both(CENTER ? -s[1] * inv_d : 0.f);
 #pragma unroll
             for (int i = 0; i < P; ++i)
 #pragma unroll
@@ -311,16 +401,24 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_consta
         }
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            if (row && on[i]) store8<true, false>((T*)p.d_o.p + b * p.d_o.b + t * p.d_o.t + e[i], 0, 4, dt[i]);
+            if (row && on[i]) store8<true, false>(here.at<T>(p.d_o) + e[i], 0, 4, dt[i]);
+        here.next();
     }
     // one partial row a CTA, over its row slots
-    auto leave = [&](const float2 (&sum)[P][4], float* part) {
+    copies_wait<0>();
+    float* const columns = reinterpret_cast<float*>(ring);
+    auto leave = [&](const float2 (&sum)[P][4], const float* times, float* part) {
         if (!part) return;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            if (on[i])
-                store8<true, false>(columns + (size_t)at.slot * p.D + e[i], 0, 4, sum[i]);
+            if (on[i]) {
+                float2 f[4];
+                row_weights<false>(times, on[i], e[i], e[i] + 4, f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = __fmul2_rn(f[j], sum[i][j]);
+                store8<true, false>(columns + (size_t)at.slot * p.D + e[i], 0, 4, f);
+            }
         __syncthreads();
         for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
             float v = 0.f;
@@ -328,9 +426,9 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(const __grid_consta
             part[(size_t)blockIdx.x * p.D + c] = v;
         }
     };
-    leave(s_post, p.part_post);
-    leave(s_gate, p.part_gate);
-    leave(s_pre, p.part_pre);
+    leave(s_post, gate, p.part_post);
+    leave(s_post, p.w_post, p.part_gate);
+    leave(s_pre, nullptr, p.part_pre);
 }
 
 // d(gate) of each sequence: its CTAs' partial rows, added in order.
@@ -348,21 +446,22 @@ struct Shape {
     int pieces, threads, rows;  // a row's pieces a thread and threads, rows a CTA
 };
 
+// Two pieces a thread above 256 entries: fewer warps a row, whose sums cost less.
 Shape shape(int D) {
     Shape s;
-    s.pieces = D <= 4096 ? 1 : 2;
+    s.pieces = D <= 256 ? 1 : 2;
     const int per = 8 * s.pieces;
     s.threads = ((D + per - 1) / per + 31) / 32 * 32;
     s.rows = s.threads <= 32 ? 4 : s.threads <= 64 ? 2 : 1;
     return s;
 }
 
-constexpr int kFwdThreadsPerSm = 2048, kBwdThreadsPerSm = 1024;
+constexpr int kFwdThreadsPerSm = 768, kBwdThreadsPerSm = 512;
 
 long long fwd_blocks(const BlockNormArgs& a) {
     const Shape sh = shape(a.D);
     const long long rows = ((long long)a.B * a.T + sh.rows - 1) / sh.rows;
-    return std::min(rows, (long long)sm_count() * (kFwdThreadsPerSm / (sh.threads * sh.rows)));
+    return std::min(rows, (long long)sm_count() * std::max(1, kFwdThreadsPerSm / (sh.threads * sh.rows)));
 }
 
 // CTAs of the gradients: (of each sequence, in all).
@@ -393,37 +492,44 @@ BlockParams params(const BlockNormArgs& a) {
     p.w_post = a.post_weight; p.gate = a.gate; p.w_pre = a.pre_weight;
     p.B = a.B; p.T = a.T; p.D = a.D;
     p.rows_cta = shape(a.D).rows;
+    p.by_T = Divide::by(a.T);
     p.post = a.post; p.pre = a.pre; p.center = a.center; p.gate_each = a.gate_each;
     p.alpha = a.scale; p.beta = a.residual_scale; p.eps = a.eps;
     return p;
 }
 
-template <typename T, typename R, int P>
-cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, int threads, size_t shared, cudaStream_t s) {
-    if (!bwd) {
-        block_norm_kernel<T, R, P><<<grid, threads, 0, s>>>(p);
-        return cudaGetLastError();
-    }
-    const cudaError_t e = cudaFuncSetAttribute(block_norm_bwd_kernel<T, R, P>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+template <typename T, typename R, int P, int THREADS, bool CENTER>
+cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, int threads, cudaStream_t s) {
+    const size_t piece = (size_t)P * threads * 8;
+    const size_t shared = bwd ? std::max(kBwdRingOf<T, THREADS> * 2 * piece * (sizeof(T) + sizeof(R)),
+                                         (size_t)p.rows_cta * p.D * sizeof(float))
+                              : kRing * piece * (sizeof(T) + sizeof(R));
+    const auto kernel = bwd ? block_norm_bwd_kernel<T, R, P, THREADS, CENTER> : block_norm_kernel<T, R, P, THREADS, CENTER>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
     if (e != cudaSuccess) return e;
-    block_norm_bwd_kernel<T, R, P><<<grid, threads, shared, s>>>(p);
+    kernel<<<grid, threads, shared, s>>>(p);
     return cudaGetLastError();
 }
 
-template <typename T, typename R>
-cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, size_t shared, cudaStream_t s) {
-    const Shape sh = shape(p.D);
-    const int threads = sh.threads * sh.rows;
-    return sh.pieces == 1 ? launch<T, R, 1>(p, bwd, grid, threads, shared, s)
-                          : launch<T, R, 2>(p, bwd, grid, threads, shared, s);
+template <typename T, typename R, int P, int THREADS>
+cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, int threads, cudaStream_t s) {
+    return p.center ? launch<T, R, P, THREADS, true>(p, bwd, grid, threads, s)
+                    : launch<T, R, P, THREADS, false>(p, bwd, grid, threads, s);
 }
 
-cudaError_t launch(const BlockNormArgs& a, const BlockParams& p, bool bwd, unsigned grid, size_t shared,
-                   cudaStream_t s) {
-    if (!a.bf16) return launch<float, float>(p, bwd, grid, shared, s);
-    if (a.residual_bf16) return launch<__nv_bfloat16, __nv_bfloat16>(p, bwd, grid, shared, s);
-    return launch<__nv_bfloat16, float>(p, bwd, grid, shared, s);
+template <typename T, typename R>
+cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, cudaStream_t s) {
+    const Shape sh = shape(p.D);
+    const int threads = sh.threads * sh.rows;
+    if (sh.pieces == 1) return launch<T, R, 1, 128>(p, bwd, grid, threads, s);
+    if (threads <= 256) return launch<T, R, 2, 256>(p, bwd, grid, threads, s);
+    return launch<T, R, 2, 512>(p, bwd, grid, threads, s);
+}
+
+cudaError_t launch(const BlockNormArgs& a, const BlockParams& p, bool bwd, unsigned grid, cudaStream_t s) {
+    if (!a.bf16) return launch<float, float>(p, bwd, grid, s);
+    if (a.residual_bf16) return launch<__nv_bfloat16, __nv_bfloat16>(p, bwd, grid, s);
+    return launch<__nv_bfloat16, float>(p, bwd, grid, s);
 }
 
 }  // namespace
@@ -437,7 +543,7 @@ size_t block_norm_bwd_workspace_bytes(const BlockNormArgs& a) {
 
 cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, cudaStream_t s) {
     TraceScope trace("block_norm_kernel", s);
-    return launch(a, params(a), false, (unsigned)fwd_blocks(a), 0, s);
+    return launch(a, params(a), false, (unsigned)fwd_blocks(a), s);
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, cudaStream_t s) {
@@ -454,7 +560,7 @@ cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, cudaStream_t s) {
     cudaError_t e;
     {
         TraceScope trace("block_norm_bwd_kernel", s);
-        e = launch(a, p, true, (unsigned)all, sums ? (size_t)p.rows_cta * a.D * sizeof(float) : 0, s);
+        e = launch(a, p, true, (unsigned)all, s);
     }
     if (e != cudaSuccess || !sums) return e;
     const PartialSum of[3] = {{p.part_post, a.dpost_weight, (int)all, a.D},

@@ -13,8 +13,10 @@
 // Bound by HBM: x in, y out, 2 W + 6 operations an entry.  A thread keeps a vector of
 // channels (16 bytes; backward four) and walks a run of tokens with the last W - 1 rows
 // in registers, so that x is read once but for the W - 1 rows before a run (and backward
-// behind it); the loads of the next rows are in flight meanwhile.
+// behind it).  The next eight rows come through a ring in shared memory, each thread's own
+// pieces, copied in the background: loads in flight cost no registers and there is no barrier.
 #include <algorithm>
+#include <type_traits>
 
 #include "rows.cuh"
 #include "tc_ptx.cuh"
@@ -49,25 +51,22 @@ struct Pack {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0;
     }
-    __device__ __forceinline__ void floats(float (&x)[V]) const {
-        if constexpr (sizeof(T) == 4) {
+    __device__ __forceinline__ void floats(float2 (&x)[V / 2]) const {
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = __uint_as_float(w[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (sizeof(T) == 4) x[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            else x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
         }
     }
-    __device__ __forceinline__ void round(const float (&x)[V]) {
-        if constexpr (sizeof(T) == 4) {
+    __device__ __forceinline__ void round(const float2 (&x)[V / 2]) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) w[i] = __float_as_uint(x[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) w[i] = bf16x2_bits(x[2 * i], x[2 * i + 1]);
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                w[2 * i] = __float_as_uint(x[i].x);
+                w[2 * i + 1] = __float_as_uint(x[i].y);
+            } else {
+                w[i] = bf16x2_bits(x[i].x, x[i].y);
+            }
         }
     }
 };
@@ -90,112 +89,167 @@ struct ConvParams {
     long long run_blocks;                      // CTAs below one another (backward: they stride)
 };
 
-// The W weights of V channels from c on.
+// The W weights of V channels from c on (V W neighbouring numbers, V a multiple of 4), as
+// pairs of channels for the packed arithmetic.
 template <int W, int V>
-__device__ __forceinline__ void load_weights(const ConvParams& p, int c, float (&w)[W][V], float (&bias)[V]) {
+__device__ __forceinline__ void load_weights(const ConvParams& p, int c, float2 (&w)[W][V / 2], float2 (&bias)[V / 2]) {
+    float all[V * W];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V * W; i += 4)
+        *reinterpret_cast<float4*>(all + i) = __ldg(reinterpret_cast<const float4*>(p.w + (size_t)c * W + i));
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = __ldg(p.w + (size_t)(c + i) * W + j);
-        bias[i] = p.bias ? __ldg(p.bias + c + i) : 0.f;
+    for (int i = 0; i < V / 2; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = make_float2(all[2 * i * W + j], all[(2 * i + 1) * W + j]);
+        bias[i] = p.bias ? __ldg(reinterpret_cast<const float2*>(p.bias + c) + i) : make_float2(0.f, 0.f);
     }
 }
 
 // Row `at` (below 0: of the state) of sequence b.
 template <typename T, int W, int V>
-__device__ __forceinline__ void row_before(const ConvParams& p, long long b, int at, int c, float (&x)[V]) {
+__device__ __forceinline__ Pack<T, V> row_before(const ConvParams& p, long long b, int at, int c) {
     Pack<T, V> r;
     r.zero();
     if (at >= 0) r.load((const T*)p.x + b * p.xb + at * p.xt + c);
     else if (p.state) r.load((const T*)p.state + (b * (W - 1) + at + (W - 1)) * p.D + c);
-    r.floats(x);
+    return r;
 }
 
-// u of a token whose row is `cur` behind the rows `before` (oldest first).
-template <int W, int V>
-__device__ __forceinline__ void convolve(const float (&w)[W][V], const float (&bias)[V],
-                                         const float (&before)[W - 1][V], const float (&cur)[V], int reach,
-                                         float (&u)[V]) {
+// u of a token from its row `cur` and those before it: row k back is before[(from - k) mod
+// (W - 1)], a place known when the loop is unrolled, so that the rows never move.
+template <int W, int V, int FROM>
+__device__ __forceinline__ void convolve(const float2 (&w)[W][V / 2], const float2 (&bias)[V / 2],
+                                         const float2 (&before)[W - 1][V / 2], const float2 (&cur)[V / 2], int reach,
+                                         float2 (&u)[V / 2]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) u[i] = fmaf(w[W - 1][i], cur[i], bias[i]);
-    if (reach >= W - 1) {
+    for (int i = 0; i < V / 2; ++i) u[i] = __ffma2_rn(w[W - 1][i], cur[i], bias[i]);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
+    for (int k = W - 1; k > 0; --k) {
+        if (k <= reach) {
+            constexpr int kMod = W - 1;
+            const int at = ((FROM - k) % kMod + kMod) % kMod;
 #pragma unroll
-            for (int i = 0; i < V; ++i) u[i] = fmaf(w[j][i], before[j][i], u[i]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-            if (W - 1 - j <= reach)
-#pragma unroll
-                for (int i = 0; i < V; ++i) u[i] = fmaf(w[j][i], before[j][i], u[i]);
+            for (int i = 0; i < V / 2; ++i) u[i] = __ffma2_rn(w[W - 1 - k][i], before[at][i], u[i]);
+        }
     }
 }
 
-template <int W, int V>
-__device__ __forceinline__ void push_row(float (&before)[W - 1][V], const float (&cur)[V]) {
-#pragma unroll
-    for (int j = 0; j < W - 2; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) before[j][i] = before[j + 1][i];
-#pragma unroll
-    for (int i = 0; i < V; ++i) before[W - 2][i] = cur[i];
+// sigma of both halves, as sigmoid<T>.
+template <typename T>
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+    if (sizeof(T) == 4) return make_float2(sigmoid<T>(v.x), sigmoid<T>(v.y));
+    const float2 s = __fmul2_rn(v, both(-1.4426950408889634f));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(s.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(s.y));
+    e = __fadd2_rn(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+    return e;
+}
+
+// Rows of the ring, and tokens of the unrolled loop: a multiple of the W - 1 rows kept.
+template <int W>
+constexpr int kAheadOf = W == 4 ? 9 : 8;
+
+// f(0), .. f(N - 1) with the index a constant.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(const F& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        each<N, I + 1>(f);
+    }
+}
+
+// A thread's V entries from global to shared memory in the background.
+template <typename T, int V>
+__device__ __forceinline__ void copy_pack(void* to, const T* from) {
+    constexpr int kBytes = V * (int)sizeof(T);
+    if constexpr (kBytes == 16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+                     : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                     "n"(kBytes)
+                     : "memory");
+    }
 }
 
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const __grid_constant__ ConvParams p) {
-    constexpr int V = 16 / (int)sizeof(T), kAhead = 8;  // rows whose loads are in flight
+    constexpr int V = 16 / (int)sizeof(T), kAhead = kAheadOf<W>;
+    __shared__ __align__(16) uint4 ring[kAhead][kThreads];
     const int tile = (int)(blockIdx.x % (unsigned)p.tiles);
     const int c = (tile * p.lanes + (int)threadIdx.x % p.lanes) * V;
     const long long run = (long long)(blockIdx.x / (unsigned)p.tiles) * (kThreads / p.lanes) + threadIdx.x / p.lanes;
     if (c >= p.D || run >= p.runs) return;
     const long long b = run / p.runs_per_seq;
     const int t0 = (int)(run - b * p.runs_per_seq) * p.run, t1 = (int)min((long long)t0 + p.run, (long long)p.T);
-    float w[W][V], bias[V], before[W - 1][V];
+    const int n = t1 - t0;
+    const T* ahead = (const T*)p.x + b * p.xb + (long long)t0 * p.xt + c;
+    T* y = (T*)p.y + b * p.yb + (long long)t0 * p.yt + c;
+    const int* pos = p.positions ? p.positions + b * p.T + t0 : nullptr;
+    auto fetch = [&](int m, int slot) {
+        if (m < n) copy_pack<T, V>(&ring[slot][threadIdx.x], ahead);
+        copies_commit();
+        ahead += p.xt;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(i, i);
+    float2 w[W][V / 2], bias[V / 2], before[W - 1][V / 2];
     load_weights<W, V>(p, c, w, bias);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) row_before<T, W, V>(p, b, t0 - (W - 1) + j, c, before[j]);
+    for (int j = 0; j < W - 1; ++j) row_before<T, W, V>(p, b, t0 - (W - 1) + j, c).floats(before[j]);
     if (t0 == 0 && p.state_out) {
         // the sequence's first thread has read the state and may write it in place: row j
         // is row T - W + 1 + j of the tokens behind it
-        float last[W - 1][V];
+        Pack<T, V> last[W - 1];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) row_before<T, W, V>(p, b, p.T - (W - 1) + j, c, last[j]);
+        for (int j = 0; j < W - 1; ++j) last[j] = row_before<T, W, V>(p, b, p.T - (W - 1) + j, c);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            Pack<T, V> r;
-            r.round(last[j]);  // exact: they are T's
-            r.store((T*)p.state_out + (b * (W - 1) + j) * p.D + c);
-        }
+        for (int j = 0; j < W - 1; ++j) last[j].store((T*)p.state_out + (b * (W - 1) + j) * p.D + c);
     }
-    const T* x = (const T*)p.x + b * p.xb + (long long)t0 * p.xt + c;
-    T* y = (T*)p.y + b * p.yb + (long long)t0 * p.yt + c;
-    const int* pos = p.positions ? p.positions + b * p.T + t0 : nullptr;
-    const int n = t1 - t0;
-    Pack<T, V> next[kAhead];
+    // The next kAhead tokens whose taps do not all count, a bit each.
+    auto shorts = [&](int m0) {
+        unsigned bits = 0;
+        if (pos) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (i < n) next[i].load(x + i * p.xt);
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
-        x += kAhead * p.xt;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (i0 + i < n) {
-                float cur[V], u[V];
-                next[i].floats(cur);
-                if (i0 + i + kAhead < n) next[i].load(x + i * p.xt);
-                convolve<W, V>(w, bias, before, cur, pos ? __ldg(pos + i0 + i) : W - 1, u);
-                push_row<W, V>(before, cur);
-                if (p.silu) {
-#pragma unroll
-                    for (int k = 0; k < V; ++k) u[k] *= sigmoid<T>(u[k]);
-                }
-                Pack<T, V> r;
-                r.round(u);
-                r.store(y);
-                y += p.yt;
-            }
+            for (int i = 0; i < kAhead; ++i)
+                if (m0 + i < n) bits |= (__ldg(pos + m0 + i) < W - 1 ? 1u : 0u) << i;
         }
+        return bits;
+    };
+    unsigned now = shorts(0);
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+        const unsigned next = shorts(i0 + kAhead);
+        auto token = [&](auto index, int reach) {
+            constexpr int i = decltype(index)::value;
+            copies_wait<kAhead - 1>();
+            Pack<T, V> r;
+            float2 cur[V / 2], u[V / 2];
+            r.load(reinterpret_cast<const T*>(&ring[i][threadIdx.x]));
+            r.floats(cur);
+            fetch(i0 + i + kAhead, i);
+            convolve<W, V, i>(w, bias, before, cur, reach, u);
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) before[i % (W - 1)][k] = cur[k];
+            if (p.silu) {
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) u[k] = __fmul2_rn(u[k], sigmoid2<T>(u[k]));
+            }
+            r.round(u);
+            r.store(y);
+            y += p.yt;
+        };
+        if (now == 0 && i0 + kAhead <= n) {
+            each<kAhead>([&](auto index) { token(index, W - 1); });
+        } else {
+            each<kAhead>([&](auto index) {
+                constexpr int i = decltype(index)::value;
+                if (i0 + i < n) token(index, now >> i & 1 ? __ldg(pos + i0 + i) : W - 1);
+            });
+        }
+        now = next;
     }
 }
 
@@ -203,126 +257,173 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const __grid_co
 // token t - W + 1.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __grid_constant__ ConvParams p) {
-    constexpr int V = 4, kAhead = 4;
+    constexpr int V = 4, kAhead = kAheadOf<W>;
     tc::griddep_launch_dependents();  // the sums' kernel may be scheduled (it waits itself)
-    __shared__ float red[kThreads][V + 1];
+    using Piece = std::conditional_t<sizeof(T) == 2, uint2, uint4>;
+    __shared__ __align__(16) Piece ring[kAhead][2][kThreads];  // x, dy
     const int tile = (int)(blockIdx.x % (unsigned)p.tiles), lane = (int)threadIdx.x % p.lanes;
     const int c = (tile * p.lanes + lane) * V, depth = kThreads / p.lanes, row = (int)threadIdx.x / p.lanes;
     const long long run_block = blockIdx.x / (unsigned)p.tiles;
-    float dw[W][V], db[V];
+    float2 dw[W][V / 2], db[V / 2];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        db[i] = 0.f;
+    for (int i = 0; i < V / 2; ++i) {
+        db[i] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][i] = make_float2(0.f, 0.f);
     }
     if (c < p.D) {
-        float w[W][V], bias[V];
+        float2 w[W][V / 2], bias[V / 2];
         load_weights<W, V>(p, c, w, bias);
         for (long long run = run_block * depth + row; run < p.runs; run += p.run_blocks * depth) {
             const long long b = run / p.runs_per_seq;
             const int t0 = (int)(run - b * p.runs_per_seq) * p.run;
             const int t1 = (int)min((long long)t0 + p.run, (long long)p.T), n = t1 - t0;
             const int there = min(p.T - t0, n + W - 1);  // tokens to read
-            float before[W - 1][V], acc[W][V];           // acc[k]: dx of token t - k so far
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) row_before<T, W, V>(p, b, t0 - (W - 1) + j, c, before[j]);
-#pragma unroll
-            for (int k = 0; k < W; ++k)
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
             const T* x = (const T*)p.x + b * p.xb + (long long)t0 * p.xt + c;
             const T* dy = (const T*)p.dy + b * p.gb + (long long)t0 * p.gt + c;
             T* dx = (T*)p.dx + b * p.db + (long long)t0 * p.dt + c;
             const int* pos = p.positions ? p.positions + b * p.T + t0 : nullptr;
-            Pack<T, V> next_x[kAhead], next_dy[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (i < there) {
-                    next_x[i].load(x + i * p.xt);
-                    next_dy[i].load(dy + i * p.gt);
+            auto fetch = [&](int m, int slot) {
+                if (m < there) {
+                    copy_pack<T, V>(&ring[slot][0][threadIdx.x], x);
+                    copy_pack<T, V>(&ring[slot][1][threadIdx.x], dy);
                 }
+                copies_commit();
+                x += p.xt;
+                dy += p.gt;
+            };
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) fetch(i, i);
+            float2 before[W - 1][V / 2], dus[W - 1][V / 2];  // the last rows, the last du
+            int reached[W - 1];                              // and how far their taps reached
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                row_before<T, W, V>(p, b, t0 - (W - 1) + j, c).floats(before[j]);
+                reached[j] = W - 1;
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) dus[j][e] = make_float2(0.f, 0.f);
+            }
+            auto shorts = [&](int m0) {  // as forward
+                unsigned bits = 0;
+                if (pos) {
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i)
+                        if (m0 + i < there) bits |= (__ldg(pos + m0 + i) < W - 1 ? 1u : 0u) << i;
+                }
+                return bits;
+            };
+            unsigned now = shorts(0);
+            bool clean = true;  // the last rows' taps all counted
             for (int i0 = 0; i0 < n + W - 1; i0 += kAhead) {
-                x += kAhead * p.xt;
-                dy += kAhead * p.gt;
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
+                const unsigned next = shorts(i0 + kAhead);
+                // WHOLE: a token of the run, as is the one it completes, every tap counts, and the
+                // sequence's last rows are not reached
+                auto token = [&](auto index, auto whole) {
+                    constexpr int i = decltype(index)::value;
+                    constexpr bool kWhole = decltype(whole)::value;
                     const int m = i0 + i;  // token t0 + m
-                    if (m < there) {
-                        float cur[V], du[V];
-                        next_x[i].floats(cur);
-                        next_dy[i].floats(du);
-                        if (m + kAhead < there) {
-                            next_x[i].load(x + i * p.xt);
-                            next_dy[i].load(dy + i * p.gt);
-                        }
-                        const int reach = pos ? __ldg(pos + m) : W - 1;
-                        if (p.silu) {
-                            float u[V];
-                            convolve<W, V>(w, bias, before, cur, reach, u);
+                    float2 cur[V / 2], du[V / 2];
+                    int reach = W - 1;
+                    copies_wait<kAhead - 1>();
 #pragma unroll
-                            for (int k = 0; k < V; ++k) {
-                                const float s = sigmoid<T>(u[k]), a = u[k] * s;
-                                du[k] *= fmaf(a, 1.f - s, s);
-                            }
+                    for (int e = 0; e < V / 2; ++e) cur[e] = du[e] = make_float2(0.f, 0.f);
+                    if (kWhole || m < there) {
+                        Pack<T, V> in;
+                        in.load(reinterpret_cast<const T*>(&ring[i][0][threadIdx.x]));
+                        in.floats(cur);
+                        in.load(reinterpret_cast<const T*>(&ring[i][1][threadIdx.x]));
+                        in.floats(du);
+                        if (!kWhole && now >> i & 1) reach = __ldg(pos + m);
+                    }
+                    fetch(m + kAhead, i);
+                    if (p.silu && (kWhole || m < there)) {
+                        float2 u[V / 2];
+                        convolve<W, V, i>(w, bias, before, cur, reach, u);
+#pragma unroll
+                        for (int e = 0; e < V / 2; ++e) {
+                            // the slope: sigma + u sigma (1 - sigma)
+                            const float2 s = sigmoid2<T>(u[e]), a = __fmul2_rn(u[e], s);
+                            du[e] = __fmul2_rn(du[e], __ffma2_rn(a, __ffma2_rn(s, both(-1.f), both(1.f)), s));
                         }
+                    }
+                    constexpr int kMod = W - 1;
+                    if (kWhole || m < n) {
 #pragma unroll
                         for (int k = 0; k < W; ++k) {
-                            if (k == 0 || k <= reach) {
+                            if (kWhole || k == 0 || k <= reach) {
+                                const int from = ((i - k) % kMod + kMod) % kMod;
 #pragma unroll
-                                for (int e = 0; e < V; ++e) {
-                                    acc[k][e] = fmaf(w[W - 1 - k][e], du[e], acc[k][e]);
-                                    const float at = k == 0 ? cur[e] : before[k == 0 ? 0 : W - 1 - k][e];
-                                    if (m < n) dw[W - 1 - k][e] = fmaf(du[e], at, dw[W - 1 - k][e]);
-                                }
+                                for (int e = 0; e < V / 2; ++e)
+                                    dw[W - 1 - k][e] = __ffma2_rn(du[e], k == 0 ? cur[e] : before[from][e], dw[W - 1 - k][e]);
                             }
                         }
-                        if (m < n) {
 #pragma unroll
-                            for (int e = 0; e < V; ++e) db[e] += du[e];
-                        }
-                        push_row<W, V>(before, cur);
+                        for (int e = 0; e < V / 2; ++e) db[e] = __fadd2_rn(db[e], du[e]);
                     }
                     const int s = m - (W - 1);  // token t0 + s has its whole sum
-                    if (s < n && (s >= 0 || t0 == 0)) {
-                        const int t = t0 + s, k = t - (p.T - (W - 1));
-                        if (p.dstate_T && k >= 0) {
-                            Pack<T, V> r;
-                            float tail[V];
-                            r.load((const T*)p.dstate_T + (b * (W - 1) + k) * p.D + c);
-                            r.floats(tail);
+                    if (kWhole || (s < n && (s >= 0 || t0 == 0))) {
+                        float2 sum[V / 2];
 #pragma unroll
-                            for (int e = 0; e < V; ++e) acc[W - 1][e] += tail[e];
+                        for (int e = 0; e < V / 2; ++e) sum[e] = make_float2(0.f, 0.f);
+                        const int t = t0 + s, k_last = t - (p.T - (W - 1));
+                        if (!kWhole && p.dstate_T && k_last >= 0) {
+                            Pack<T, V> r;
+                            r.load((const T*)p.dstate_T + (b * (W - 1) + k_last) * p.D + c);
+                            r.floats(sum);
+                        }
+#pragma unroll
+                        for (int k = 0; k < W; ++k) {  // du of token s + k, which lies W - 1 - k back
+                            const int from = ((i + k) % kMod + kMod) % kMod;
+                            const int far = k == W - 1 ? reach : reached[from];
+                            if (kWhole || k == 0 || far >= k) {
+#pragma unroll
+                                for (int e = 0; e < V / 2; ++e)
+                                    sum[e] = __ffma2_rn(w[W - 1 - k][e], k == W - 1 ? du[e] : dus[from][e], sum[e]);
+                            }
                         }
                         Pack<T, V> r;
-                        r.round(acc[W - 1]);
-                        if (s >= 0) r.store(dx + s * p.dt);
+                        r.round(sum);
+                        if (kWhole || s >= 0) r.store(dx);
                         else if (p.dstate) r.store((T*)p.dstate + (b * (W - 1) + m) * p.D + c);
                     }
+                    if (kWhole || s >= 0) dx += p.dt;
+                    reached[i % kMod] = reach;
 #pragma unroll
-                    for (int k = W - 1; k > 0; --k)
-#pragma unroll
-                        for (int e = 0; e < V; ++e) acc[k][e] = acc[k - 1][e];
-#pragma unroll
-                    for (int e = 0; e < V; ++e) acc[0][e] = 0.f;
+                    for (int e = 0; e < V / 2; ++e) {
+                        before[i % kMod][e] = cur[e];
+                        dus[i % kMod][e] = du[e];
+                    }
+                };
+                if (now == 0 && clean && i0 >= W - 1 && i0 + kAhead <= n) {
+                    each<kAhead>([&](auto index) { token(index, std::true_type()); });
+                } else {
+                    each<kAhead>([&](auto index) { token(index, std::false_type()); });
                 }
+                clean = now >> (kAhead - (W - 1)) == 0;
+                now = next;
             }
+            copies_wait<0>();
         }
     }
     // one partial row a block of runs: over the CTA's threads of the same channels
+    float2(*red)[V / 2] = reinterpret_cast<float2(*)[V / 2]>(&ring[0][0][0]);
+    static_assert(sizeof(ring) >= kThreads * V * sizeof(float), "a thread's sums of one tap fit the ring");
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         float* part = j < W ? p.part_w : p.part_b;
         if (!part) continue;
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < V; ++e) red[threadIdx.x][e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+        for (int e = 0; e < V / 2; ++e) red[threadIdx.x][e] = j < W ? dw[j < W ? j : 0][e] : db[e];
         __syncthreads();
         if (row == 0 && c < p.D) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 float sum = 0.f;
-                for (int r = 0; r < depth; ++r) sum += red[r * p.lanes + lane][e];
+                for (int r = 0; r < depth; ++r) {
+                    const float2 v = red[r * p.lanes + lane][e / 2];
+                    sum += e % 2 ? v.y : v.x;
+                }
                 if (j < W) part[(size_t)run_block * p.D * W + (size_t)(c + e) * W + j] = sum;
                 else part[(size_t)run_block * p.D + c + e] = sum;
             }
@@ -330,39 +431,41 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __gri
     }
 }
 
-// One token of each sequence: the state's rows move up by one.
+// One token of each sequence: the state's rows move up by one.  A thread keeps its channels'
+// weights (as many bytes as a sequence's rows) and walks sequences.
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const __grid_constant__ ConvParams p, unsigned vectors) {
+__global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const __grid_constant__ ConvParams p) {
     constexpr int V = 16 / (int)sizeof(T);
-    const unsigned i = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= vectors) return;
-    const unsigned per = (unsigned)p.D / V;
-    const long long b = i / per;
-    const int c = (int)(i - (unsigned)b * per) * V;
-    Pack<T, V> rows[W], out;
+    const int c = (int)(blockIdx.x * kThreads + threadIdx.x) * V;
+    if (c >= p.D) return;
+    Pack<T, V> rows[W], next[W];
+    auto load = [&](Pack<T, V>(&to)[W], long long b) {
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) rows[j].load((const T*)p.state + (b * (W - 1) + j) * p.D + c);
-    rows[W - 1].load((const T*)p.x + b * p.xb + c);
-    float w[W][V], u[V];
-    load_weights<W, V>(p, c, w, u);
+        for (int j = 0; j < W - 1; ++j) to[j].load((const T*)p.state + (b * (W - 1) + j) * p.D + c);
+        to[W - 1].load((const T*)p.x + b * p.xb + c);
+    };
+    load(rows, blockIdx.y);
+    float2 w[W][V / 2], bias[V / 2];
+    load_weights<W, V>(p, c, w, bias);
+    for (long long b = blockIdx.y; b < p.B; b += gridDim.y) {
+        if (b + gridDim.y < p.B) load(next, b + gridDim.y);
+        float2 u[V / 2], before[W - 1][V / 2], x[V / 2];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) rows[j + 1].store((T*)p.state_out + (b * (W - 1) + j) * p.D + c);
-    float x[V];
-    rows[W - 1].floats(x);
+        for (int j = 0; j < W - 1; ++j) rows[j].floats(before[j]);
+        rows[W - 1].floats(x);
 #pragma unroll
-    for (int k = 0; k < V; ++k) u[k] = fmaf(w[W - 1][k], x[k], u[k]);
+        for (int j = 1; j < W; ++j) rows[j].store((T*)p.state_out + (b * (W - 1) + j - 1) * p.D + c);
+        convolve<W, V, 0>(w, bias, before, x, W - 1, u);
+        if (p.silu) {
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        rows[j].floats(x);
+            for (int k = 0; k < V / 2; ++k) u[k] = __fmul2_rn(u[k], sigmoid2<T>(u[k]));
+        }
+        Pack<T, V> out;
+        out.round(u);
+        out.store((T*)p.y + b * p.D + c);
 #pragma unroll
-        for (int k = 0; k < V; ++k) u[k] = fmaf(w[j][k], x[k], u[k]);
+        for (int j = 0; j < W; ++j) rows[j] = next[j];
     }
-    if (p.silu) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) u[k] *= sigmoid<T>(u[k]);
-    }
-    out.round(u);
-    out.store((T*)p.y + b * p.D + c);
 }
 
 ConvParams params(const ShortConvArgs& a) {
@@ -397,7 +500,7 @@ void shape(ConvParams* p, int V, int most, int waves) {
     p->run_blocks = (p->runs + kThreads / p->lanes - 1) / (kThreads / p->lanes);
 }
 
-constexpr int kFwdRun = 64, kBwdRun = 64, kBwdBlocksPerSm = 4;
+constexpr int kFwdRun = 64, kBwdRun = 64, kBwdBlocksPerSm = 4, kStepBlocksPerSm = 4;
 
 ConvParams bwd_params(const ShortConvArgs& a) {
     ConvParams p = params(a);
@@ -456,14 +559,16 @@ cudaError_t launch_short_conv_bwd(const ShortConvArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_short_conv_step(const ShortConvArgs& a, cudaStream_t s) {
-    ConvParams p = params(a);
-    const unsigned vectors = (unsigned)((long long)a.B * a.D / (a.bf16 ? 8 : 4));
-    const unsigned grid = (vectors + kThreads - 1) / kThreads;
+    const ConvParams p = params(a);
+    const int vectors = a.D / (a.bf16 ? 8 : 4);
+    const unsigned blocks = (unsigned)((vectors + kThreads - 1) / kThreads);
+    const long long want = ((long long)sm_count() * kStepBlocksPerSm + blocks - 1) / blocks;
+    const dim3 grid(blocks, (unsigned)std::min<long long>(std::min<long long>(a.B, want), 65535));
     TraceScope trace("short_conv_step_kernel", s);
     return by_width(a.W, [&](auto w) {
         constexpr int W = decltype(w)::value;
-        if (a.bf16) short_conv_step_kernel<__nv_bfloat16, W><<<grid, kThreads, 0, s>>>(p, vectors);
-        else short_conv_step_kernel<float, W><<<grid, kThreads, 0, s>>>(p, vectors);
+        if (a.bf16) short_conv_step_kernel<__nv_bfloat16, W><<<grid, kThreads, 0, s>>>(p);
+        else short_conv_step_kernel<float, W><<<grid, kThreads, 0, s>>>(p);
     });
 }
 

@@ -15,6 +15,7 @@
 // small kernel puts them together, and a second walk writes y from the state entering each
 // chunk.  The gradients always work chunk by chunk.
 #include <algorithm>
+#include <climits>
 
 #include "ssm.cuh"
 
@@ -101,6 +102,17 @@ __global__ void __launch_bounds__(256) ssm_shared_grad_kernel(const float* part,
 
 // ---- one token -------------------------------------------------------------------------
 
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+    *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(p));
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
+    const uint2 r = __ldg(reinterpret_cast<const uint2*>(p));
+    v[0] = __uint_as_float(r.x << 16);
+    v[1] = __uint_as_float(r.x & 0xffff0000u);
+    v[2] = __uint_as_float(r.y << 16);
+    v[3] = __uint_as_float(r.y & 0xffff0000u);
+}
+
 // Four states a lane: a channel's N / 4 lanes lie side by side; a CTA keeps its channels
 // and walks sequences, so that A is read once.
 template <typename T>
@@ -123,11 +135,8 @@ __global__ void __launch_bounds__(128) ssm_step_kernel(const __grid_constant__ S
             x[r] = load_elem((const T*)p.x.p + b * p.x.b, cc);
             dt[r] = load_elem((const T*)p.dt.p + b * p.dt.b, cc);
             z[r] = p.gate.p ? load_elem((const T*)p.gate.p + b * p.gate.b, cc) : 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                bv[r][i] = load_elem((const T*)p.bm.p + b * p.bm.b, g * p.N + 4 * j + i);
-                cv[r][i] = load_elem((const T*)p.cm.p + b * p.cm.b, g * p.N + 4 * j + i);
-            }
+            load4((const T*)p.bm.p + b * p.bm.b + g * p.N + 4 * j, bv[r]);
+            load4((const T*)p.cm.p + b * p.cm.b + g * p.N + 4 * j, cv[r]);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -171,41 +180,46 @@ SsmParams params(const SsmArgs& a) {
     return p;
 }
 
-// Lanes a channel, and chunks.  More lanes a channel cost little (120 to 128 instructions a
-// token and channel against 112), a cut costs a second walk (75): so first lanes, then chunks.
+// How channels lie in warps, and chunks.
 struct Plan {
-    int lanes, tiles, chunks, chunk;
+    Split split;
+    int tiles, chunks, chunk;
 };
 
-Plan forward_plan(const SsmArgs& a) {
+// Sixteen states a lane in two channels (N = 8: eight in one).
+Split wide_split(int N) { return N == 8 ? Split{1, 1} : Split{N / 8, 2}; }
+
+Plan plan_of(const SsmArgs& a, Split split, int channels_cta, long long chunks) {
     Plan p;
-    const long long want = (long long)sm_count() * 8;  // warps
-    const int most = std::min(8, a.N / 4);
-    const long long channels = (long long)a.B * a.D;
-    p.lanes = std::max(1, a.N / 16);
-    while (p.lanes < most && channels * p.lanes < want * 32) p.lanes *= 2;
-    const int cta = channels_cta(p.lanes);
-    p.tiles = (a.D / a.G + cta - 1) / cta;
-    const long long warps = (long long)a.B * a.G * p.tiles * kWarps;
-    p.chunks = 1;
-    p.chunk = a.T;
-    if (warps < want && a.T >= 256) {
-        const long long cut = std::min<long long>((2 * want + warps - 1) / warps, a.T / 128);
-        p.chunk = (int)(((a.T + cut - 1) / cut + kTile - 1) / kTile * kTile);
-        p.chunks = (a.T + p.chunk - 1) / p.chunk;
-    }
+    p.split = split;
+    p.tiles = (a.D / a.G + channels_cta - 1) / channels_cta;
+    const long long chunk = ((a.T + chunks - 1) / chunks + kTile - 1) / kTile * kTile;
+    p.chunk = (int)std::min<long long>(chunk, INT_MAX / 2 / kTile * kTile);
+    p.chunks = (int)((a.T + (long long)p.chunk - 1) / p.chunk);
     return p;
 }
 
+// One walk where the channels give a scheduler nearly a warp: a warp alone takes 230 cycles
+// a token, two together 350.  With fewer the sequences are cut, down to chunks of 32 tokens, which
+// costs a second walk (8 x 2048 tokens of 16 states: 1024 channels 150 us cut, 222 not; 1536
+// 222 either way; 2048 271 cut, 223 not).  Where even that leaves few warps, four states a lane
+// (3 x 512 tokens of 208 channels: 14 us, with sixteen 19).
+Plan forward_plan(const SsmArgs& a) {
+    const long long sms = sm_count();
+    Split split = wide_split(a.N);
+    auto warps = [&](Split s) { return (long long)a.B * a.G * ((a.D / a.G + s.cta() - 1) / s.cta()) * kWarps; };
+    const long long w = warps(split);
+    long long chunks = 1;
+    if (2 * w < 5 * sms && a.T >= 128) chunks = std::min<long long>(a.T / 32, (24 * sms + w - 1) / w);
+    if (a.N < 64 && w * chunks <= 2 * sms) split = {a.N / 4, 1};
+    return plan_of(a, split, split.cta(), chunks);
+}
+
 Plan backward_plan(const SsmArgs& a, int channels) {
-    Plan p;
-    p.lanes = std::max(1, std::min(8, a.N / 8));
-    p.tiles = (a.D / a.G + channels - 1) / channels;
-    const long long ctas = (long long)a.B * a.G * p.tiles, want = (long long)sm_count() * 16;
-    const long long cut = std::max<long long>(1, std::min<long long>((want + ctas - 1) / ctas, a.T / 64));
-    p.chunk = (int)(((a.T + cut - 1) / cut + kTile - 1) / kTile * kTile);
-    p.chunks = (a.T + p.chunk - 1) / p.chunk;
-    return p;
+    const long long tiles = (a.D / a.G + channels - 1) / channels;
+    const long long ctas = (long long)a.B * a.G * tiles, want = (long long)sm_count() * 16;
+    const long long chunks = std::max<long long>(1, std::min<long long>((want + ctas - 1) / ctas, a.T / 64));
+    return plan_of(a, wide_split(a.N), channels, chunks);
 }
 
 void use(SsmParams* p, const Plan& plan) {
@@ -270,11 +284,11 @@ cudaError_t forward(const SsmArgs& a, cudaStream_t s) {
     use(&p, plan);
     forward_workspace(a, plan, &p);
     if (plan.chunks > 1) {
-        cudaError_t e = launch_scan<T, kState>(p, plan.lanes, grid_of(p), s);
+        cudaError_t e = launch_scan<T, kState>(p, plan.split, grid_of(p), s);
         if (e == cudaSuccess) e = join(p, true, false, nullptr, s);
         if (e != cudaSuccess) return e;
     }
-    return launch_scan<T, kForward>(p, plan.lanes, grid_of(p), s);
+    return launch_scan<T, kForward>(p, plan.split, grid_of(p), s);
 }
 
 template <typename T>
@@ -287,9 +301,9 @@ cudaError_t backward(const SsmArgs& a, cudaStream_t s) {
     backward_workspace(a, plan, &bp);
     p.blocks = (a.T + kBlock - 1) / kBlock;
     SsmParams summary = p;
-    const int cta = channels_cta(plan.lanes);
+    const int cta = plan.split.cta();
     summary.tiles = (p.channels + cta - 1) / cta;
-    cudaError_t e = launch_scan<T, kSummary>(summary, plan.lanes, grid_of(summary), s);
+    cudaError_t e = launch_scan<T, kSummary>(summary, plan.split, grid_of(summary), s);
     if (e == cudaSuccess) e = join(p, true, true, a.dh_T, s);
     if (e != cudaSuccess) return e;
     auto rows = [](void* q, const long long* st) { return SsmRows{q, st[0], st[1]}; };

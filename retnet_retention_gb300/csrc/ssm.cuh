@@ -5,6 +5,8 @@
 //   h_t = exp(delta A) h_(t-1) + delta x b_t,   y_t = (c_t . h_t + skip x) gate sigmoid(gate)
 #pragma once
 
+#include <type_traits>
+
 #include "rows.cuh"
 #include "tc_ptx.cuh"
 #include "trace.h"
@@ -48,7 +50,7 @@ struct SsmBwdParams {
 namespace ssm {
 
 constexpr int kBlock = 8;    // tokens a lane group works on at once
-constexpr int kTile = 32;    // tokens whose b and c lie in shared memory
+constexpr int kTile = 16;    // tokens whose rows lie in shared memory
 constexpr int kWarps = 4;
 
 // 2^v, 2 ulp; 0 below the fp32 range.
@@ -82,11 +84,6 @@ template <typename T>
 __device__ __forceinline__ float softplus(float v) {
     const float p = sizeof(T) == 2 ? exp2_fast(-fabsf(v) * kLog2e) : expf(-fabsf(v));
     return fmaxf(v, 0.f) + log1p_unit(p);
-}
-
-template <typename T>
-__device__ __forceinline__ float load_one(const T* p) {
-    return load_elem(p, 0);
 }
 
 // v[0 .. L-1] of the L lanes that lie `gap` apart, lane j keeps the sum of v[j].
@@ -140,224 +137,348 @@ struct SharedRows {
 
 enum Mode { kForward, kState, kSummary };  // kState: a chunk's state alone; kSummary: for the gradients
 
-// One walk over a chunk of tokens for a tile of channels.  A channel's N states lie with
-// L lanes, NS = N / L each, CW = 32 / L lanes apart; the elementwise work of kBlock tokens is shared
-// out to the L lanes token by token.  kForward writes y from the state entering the chunk;
-// kState leaves the state the chunk reaches from zero and the sum of delta; kSummary also what
-// it passes back, sum_t (prod_(s <= t) e_s) c_t du_t, and the local states every kBlock tokens.
-template <typename T, int NS, int L, Mode MODE>
+// A walk's shape: a channel's N states lie with L lanes, NS = N / L each; a lane holds CH
+// channels (1 or 2).  A warp has CL = 32 / L lanes side by side along WC = CH CL channels.
+template <typename T, int CH_, int NS_, int L_, Mode MODE_>
+struct Shape {
+    using Elem = T;
+    static constexpr int CH = CH_, NS = NS_, L = L_, N = NS * L, CL = 32 / L, WC = CH * CL;
+    static constexpr Mode MODE = MODE_;
+    static constexpr int M = L / CH, K = kBlock / M;  // a lane's own tokens: every M-th, K of a block
+    // the tile's rows of x, dt, gate and dy of a warp's channels in shared memory, in pieces
+    static constexpr int kTensors = MODE == kState ? 2 : MODE == kForward ? 3 : 4;
+    static constexpr int kPiece = WC * (int)sizeof(T) < 16 ? WC * (int)sizeof(T) : 16, kElems = kPiece / (int)sizeof(T);
+    static constexpr int kPieces = kTile * WC / kElems, kEach = (kPieces + 31) / 32;
+    static constexpr int kRows = kTile * WC;       // entries of one tensor's tile
+    static constexpr int kSharedRows = kTile * 2 * N;  // of b and c
+    static constexpr int kSharedPieces = kSharedRows * (int)sizeof(T) / 16;
+    static constexpr int kStage = kTensors * kRows + kSharedRows;  // entries of T
+    // a warp's two stages, and b and c as fp32 where they are not
+    static constexpr size_t kWarpShared =
+        2 * (size_t)kStage * sizeof(T) + (sizeof(T) == 4 ? 0 : kSharedRows * sizeof(float));
+    static constexpr size_t kShared = kWarps * kWarpShared;
+};
+
+// 8 or 16 bytes from global to shared memory in the background, or as many zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_piece(void* to, const void* from, bool valid) {
+    if constexpr (BYTES == 16) {
+        copy16(to, from, valid);
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                     "l"(from), "n"(BYTES), "r"(valid ? BYTES : 0)
+                     : "memory");
+    }
+}
+
+// One walk over a chunk of tokens for a tile of channels: kForward writes y from the state
+// entering the chunk; kState leaves the state the chunk reaches from zero and the sum of
+// delta; kSummary also what it passes back, sum_t (prod_(s <= t) e_s) c_t du_t, and the
+// local states every kBlock tokens.
+//
+// A warp copies the next tile's rows in the background, those of its channels and b and c (which
+// it brings to fp32 itself: 1.5 instructions a token, and no barrier among warps).  The elementwise work of a token and channel is
+// done by one lane: register 0 of CH = 2 is the lane's own channel (2 cl + (j & 1)), and its own
+// tokens are every M-th.  Tiles in which a document starts or the chunk ends, and for the summary those
+// behind a start, take the careful form of the loop.
+template <typename S>
 __global__ void __launch_bounds__(kWarps * 32) ssm_scan_kernel(const __grid_constant__ SsmParams p) {
-    constexpr int N = NS * L, CW = 32 / L, U = kBlock, K = U / L, kThreads = kWarps * 32;
-    constexpr bool kY = MODE == kForward, kBack = MODE == kSummary;
-    __shared__ __align__(16) float bc[2][kTile][2 * N];
-    __shared__ unsigned starts[2];  // tokens of the tile that start a document
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, j = lane / CW;
+    using T = typename S::Elem;
+    constexpr int CH = S::CH, NS = S::NS, N = S::N, CL = S::CL, WC = S::WC, U = kBlock, M = S::M, K = S::K;
+    constexpr bool kY = S::MODE == kForward, kBack = S::MODE == kSummary, kGate = S::MODE != kState;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, j = lane / CL, cl = lane % CL;
+    const int own = j / CH, mine = CH * cl + j % CH;  // the own tokens' place, the own channel's
     unsigned unit = blockIdx.x;
     const unsigned tile = unit % (unsigned)(p.tiles * p.G);
     unit /= (unsigned)(p.tiles * p.G);
     const int chunk = (int)(unit % (unsigned)p.chunks);
     const long long b = unit / (unsigned)p.chunks;
     const int g = (int)(tile / (unsigned)p.tiles);
-    const int in_group = (int)(tile % (unsigned)p.tiles) * (kWarps * CW) + w * CW + lane % CW;
-    const bool on = in_group < p.channels;
-    const int c = g * p.channels + (on ? in_group : 0);
-    const int t0 = chunk * p.chunk, t1 = (int)min((long long)t0 + p.chunk, (long long)p.T);
-    const long long state_at = ((b * p.chunks + chunk) * p.D + c) * N + j * NS;
-
-    float A[NS], h[NS];
+    const int first = (int)(tile % (unsigned)p.tiles) * (kWarps * WC) + w * WC;  // the warp's channels in the group
+    int c[CH];
+    bool on[CH];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        A[i] = __ldg(p.A + (size_t)c * N + j * NS + i) * kLog2e;
-        h[i] = 0.f;
+    for (int q = 0; q < CH; ++q) {
+        const int in_group = first + CH * cl + (CH == 1 ? 0 : q ^ (j & 1));
+        on[q] = in_group < p.channels;
+        c[q] = g * p.channels + (on[q] ? in_group : 0);
     }
-    if (MODE == kForward) {
-        const float* from = p.chunks > 1 ? p.chunk_h + state_at : p.h0 ? p.h0 + (b * p.D + c) * N + j * NS : nullptr;
-        if (from) {
+    const int t0 = chunk * p.chunk, t1 = (int)min((long long)t0 + p.chunk, (long long)p.T);
+    const bool gated = kGate && p.gate.p != nullptr;
+
+    float A[CH][NS], h[CH][NS];
+    float P[CH][kBack ? NS : 1], back[CH][kBack ? NS : 1], sum[CH];
+    bool cut = false;
 #pragma unroll
-            for (int i = 0; i < NS; ++i) h[i] = from[i];
+    for (int q = 0; q < CH; ++q) {
+        sum[q] = 0.f;
+        const float* from = nullptr;
+        if (kY) {
+            if (p.chunks > 1) from = p.chunk_h + ((b * p.chunks + chunk) * p.D + c[q]) * N + j * NS;
+            else if (p.h0) from = p.h0 + (b * p.D + c[q]) * N + j * NS;
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            A[q][i] = __ldg(p.A + (size_t)c[q] * N + j * NS + i) * kLog2e;
+            h[q][i] = from ? from[i] : 0.f;
+            if (kBack) P[q][kBack ? i : 0] = 1.f, back[q][kBack ? i : 0] = 0.f;
         }
     }
-    float P[kBack ? NS : 1], back[kBack ? NS : 1];
-    if (kBack) {
-#pragma unroll
-        for (int i = 0; i < NS; ++i) P[kBack ? i : 0] = 1.f, back[kBack ? i : 0] = 0.f;
-    }
-    float sum = 0.f;  // of delta
-    bool cut = false;
-    const float skip = p.skip ? p.skip[c] : 0.f, bias = p.bias ? p.bias[c] : 0.f;
+    const float skip = p.skip ? p.skip[c[0]] : 0.f, bias = p.bias ? p.bias[c[0]] : 0.f;
 
-    // the lane's own tokens of a block: t + k L + j
-    const T* x_at = (const T*)p.x.p + b * p.x.b + c;
-    const T* dt_at = (const T*)p.dt.p + b * p.dt.b + c;
-    const T* gate_at = p.gate.p && MODE != kState ? (const T*)p.gate.p + b * p.gate.b + c : nullptr;
-    const T* dy_at = kBack ? (const T*)p.dy.p + b * p.dy.b + c : nullptr;
-    T nx[K] = {}, ndt[K] = {}, ngate[K] = {}, ndy[K] = {};
-    auto fetch = [&](int t) {
+    T* const stages = reinterpret_cast<T*>(smem + (size_t)w * S::kWarpShared);
+    constexpr int kRows = S::kRows;
+    auto copy_tile = [&](int buf, int t) {
+        T* const stage = stages + buf * S::kStage;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int at = t + k * L + j;
-            if (on && at < t1) {
-                nx[k] = x_at[at * p.x.t];
-                ndt[k] = dt_at[at * p.dt.t];
-                if (gate_at) ngate[k] = gate_at[at * p.gate.t];
-                if (kBack) ndy[k] = dy_at[at * p.dy.t];
+        for (int i = 0; i < S::kEach; ++i) {
+            const int q = i * 32 + lane, row = q / (WC / S::kElems), at = q % (WC / S::kElems) * S::kElems;
+            if (S::kPieces % 32 == 0 || q < S::kPieces) {
+                const bool valid = t + row < t1 && first + at < p.channels;
+                const long long token = valid ? t + row : 0;
+                const int col = valid ? g * p.channels + first + at : 0;
+                auto copy = [&](int k, const SsmRows& r) {
+                    copy_piece<S::kPiece>(stage + k * kRows + row * WC + at,
+                                          (const T*)r.p + b * r.b + token * r.t + col, valid);
+                };
+                copy(0, p.x);
+                copy(1, p.dt);
+                if (gated) copy(2, p.gate);
+                if (kBack) copy(3, p.dy);
             }
         }
-    };
-    SharedRows<T, N, kThreads, kTile> rows;
-    int position = 1;
-    auto fetch_tile = [&](int t) {
-        rows.load(p, b, g, t, t1);
-        if (p.positions && w == 0) position = t + lane < t1 ? p.positions[b * p.T + t + lane] : 1;
-    };
-    auto store_tile = [&](int buf) {
-        rows.store(&bc[buf][0][0]);
-        if (w == 0) {
-            const unsigned m = __ballot_sync(0xffffffffu, position == 0);
-            if (lane == 0) starts[buf] = m;
+        constexpr int kRowPieces = N * (int)sizeof(T) / 16;  // of b's row, and of c's
+#pragma unroll
+        for (int i = 0; i < (S::kSharedPieces + 31) / 32; ++i) {
+            const int q = i * 32 + lane, row = q / (2 * kRowPieces), part = q % (2 * kRowPieces);
+            if (S::kSharedPieces % 32 == 0 || q < S::kSharedPieces) {
+                const SsmRows& r = part < kRowPieces ? p.bm : p.cm;
+                const bool valid = t + row < t1;
+                copy16(stage + S::kTensors * kRows + q * (16 / (int)sizeof(T)),
+                       (const T*)r.p + b * r.b + (valid ? t + row : 0) * r.t + g * N +
+                           part % kRowPieces * (16 / (int)sizeof(T)), valid);
+            }
         }
+        copies_commit();
     };
-    fetch_tile(t0);
-    fetch(t0);
-    store_tile(0);
-    __syncthreads();
+    int position = 1;  // of the lane's token of the next tile
+    auto load_position = [&](int t) {
+        if (p.positions) position = lane < kTile && t + lane < t1 ? p.positions[b * p.T + t + lane] : 1;
+    };
+    copy_tile(0, t0);
+    load_position(t0);
     int buf = 0;
     for (int tt = t0; tt < t1; tt += kTile, buf ^= 1) {
-        if (tt + kTile < t1) fetch_tile(tt + kTile);
-        const unsigned tile_starts = starts[buf];
-        for (int q = 0; q < kTile && tt + q < t1; q += U) {
-            const int t = tt + q;
-            if (kBack && t > t0) {  // the local state before this block of the chunk
-                const long long at = (b * p.blocks + t / U) * p.D + c;
-                if (on) {
+        const unsigned tile_starts = p.positions ? __ballot_sync(0xffffffffu, position == 0) : 0;
+        if (tt + kTile < t1) {
+            copy_tile(buf ^ 1, tt + kTile);
+            load_position(tt + kTile);
+        } else {
+            copies_commit();
+        }
+        copies_wait<1>();
+        __syncwarp();
+        T* const stage = stages + buf * S::kStage;
+        const float* bc = reinterpret_cast<const float*>(stage + S::kTensors * kRows);  // [kTile][2 N]
+        if constexpr (sizeof(T) == 2) {
+            float* const wide = reinterpret_cast<float*>(stages + 2 * S::kStage);
+            bc = wide;
 #pragma unroll
-                    for (int i = 0; i < NS; ++i) p.block_h[at * N + j * NS + i] = h[i];
-                    if (j == 0) p.block_s[at] = cut ? INFINITY : sum;
+            for (int i = 0; i < (S::kSharedPieces + 31) / 32; ++i) {
+                const int q = i * 32 + lane;
+                if (S::kSharedPieces % 32 == 0 || q < S::kSharedPieces) {
+                    float2 v[4];
+                    floats8<false>(raw8<true>(stage + S::kTensors * kRows + q * 8, 0, 4), v);
+                    store8<true, false>(wide + q * 8, 0, 4, v);
                 }
             }
-            float xs[K], d[K], dx[K], gate[K], du[K];
+            __syncwarp();
+        }
+        bc += j * NS;
+        T* const own_at = stage + own * WC + mine;
+        auto walk = [&](auto careful) {
+            constexpr bool kCareful = decltype(careful)::value;
+#pragma unroll 1
+            for (int q0 = 0; q0 < kTile; q0 += U) {
+                const int t = tt + q0;
+                if (kCareful && t >= t1) break;
+                if (kBack && t > t0) {  // the local state before this block of the chunk
+                    const long long block = b * p.blocks + t / U;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const bool there = on && t + k * L + j < t1;
-                xs[k] = there ? load_one(&nx[k]) : 0.f;
-                const float v = load_one(&ndt[k]) + bias;
-                d[k] = there ? (p.softplus ? softplus<T>(v) : v) : 0.f;
-                dx[k] = d[k] * xs[k];
-                gate[k] = there && gate_at ? load_one(&ngate[k]) : 0.f;
-                du[k] = kBack && there ? load_one(&ndy[k]) : 0.f;
-                if (kBack && gate_at) du[k] *= gate[k] * sigmoid<T>(gate[k]);
-            }
-            fetch(t + U);
-            const unsigned block_starts = tile_starts >> q & ((1u << U) - 1);
-            float acc[U];
+                    for (int q = 0; q < CH; ++q)
+                        if (on[q]) {
+                            const long long at = block * p.D + c[q];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int from = u % L * CW + lane % CW;
-                const float du_ = d[u / L], dxu_ = dx[u / L];
-                const float delta = L == 1 ? du_ : __shfl_sync(0xffffffffu, du_, from);
-                const float in = L == 1 ? dxu_ : __shfl_sync(0xffffffffu, dxu_, from);
-                float dut = 0.f;
-                if (kBack) dut = L == 1 ? du[u / L] : __shfl_sync(0xffffffffu, du[u / L], from);
-                float bv[NS], cv[NS];
-#pragma unroll
-                for (int i = 0; i < NS; i += 4) {
-                    *reinterpret_cast<float4*>(bv + i) = *reinterpret_cast<const float4*>(&bc[buf][q + u][j * NS + i]);
-                    if (MODE != kState)
-                        *reinterpret_cast<float4*>(cv + i) =
-                            *reinterpret_cast<const float4*>(&bc[buf][q + u][N + j * NS + i]);
+                            for (int i = 0; i < NS; i += 4)
+                                *reinterpret_cast<float4*>(p.block_h + at * N + j * NS + i) =
+                                    make_float4(h[q][i], h[q][i + 1], h[q][i + 2], h[q][i + 3]);
+                            if (j == 0) p.block_s[at] = cut ? INFINITY : sum[q];
+                        }
                 }
-                acc[u] = 0.f;
-                if (block_starts >> u & 1) {  // the old state is dropped, not multiplied by zero
+                T* const at = own_at + q0 * WC;
+                float xs[K], d[K], dx[K], du[K];
 #pragma unroll
-                    for (int i = 0; i < NS; ++i) {
-                        h[i] = in * bv[i];
-                        if (kBack) P[kBack ? i : 0] = 0.f;
+                for (int k = 0; k < K; ++k) {
+                    xs[k] = load_elem(at, k * M * WC);
+                    const float v = load_elem(at + kRows, k * M * WC) + bias;
+                    d[k] = p.softplus ? softplus<T>(v) : v;
+                    if (kCareful && t + k * M + own >= t1) d[k] = 0.f;
+                    dx[k] = d[k] * xs[k];
+                    if (kBack) {
+                        du[k] = load_elem(at + 3 * kRows, k * M * WC);
+                        if (gated) {
+                            const float z = load_elem(at + 2 * kRows, k * M * WC);
+                            du[k] *= z * sigmoid<T>(z);
+                        }
                     }
-                    cut = true;
-                } else {
+                }
+                const unsigned block_starts = kCareful ? tile_starts >> q0 & ((1u << U) - 1) : 0;
+                float acc[U];
 #pragma unroll
-                    for (int i = 0; i < NS; ++i) {
-                        const float e = exp2_fast(delta * A[i]);
-                        h[i] = fmaf(e, h[i], in * bv[i]);
-                        if (kBack) P[kBack ? i : 0] *= e;
+                for (int u = 0; u < U; ++u) {
+                    float bv[NS], cv[NS];
+#pragma unroll
+                    for (int i = 0; i < NS; i += 4) {
+                        *reinterpret_cast<float4*>(bv + i) = *reinterpret_cast<const float4*>(bc + (q0 + u) * 2 * N + i);
+                        if (S::MODE != kState)
+                            *reinterpret_cast<float4*>(cv + i) =
+                                *reinterpret_cast<const float4*>(bc + (q0 + u) * 2 * N + N + i);
                     }
+                    const bool start = kCareful && (block_starts >> u & 1);
+                    if (start) cut = true;
+                    float a[CH];
+#pragma unroll
+                    for (int q = 0; q < CH; ++q) {
+                        // from the lane whose own token and channel it is
+                        const int from = (u % M * CH + (CH == 1 ? 0 : q ^ (j & 1))) * CL + cl;
+                        auto get = [&](const float(&v)[K]) {
+                            return M == 1 && q == 0 ? v[u / M] : __shfl_sync(0xffffffffu, v[u / M], from);
+                        };
+                        const float delta = get(d), in = get(dx), dut = kBack ? get(du) : 0.f;
+                        float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < NS; i += 2) {
+                            // two states at a time: a packed operation takes two turns to issue, but
+                            // less beside the 2^x than two of its halves
+                            const float2 x = __fmul2_rn(both(delta), make_float2(A[q][i], A[q][i + 1]));
+                            const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                            const float2 add = __fmul2_rn(both(in), make_float2(bv[i], bv[i + 1]));
+                            float2 hh = __ffma2_rn(e, make_float2(h[q][i], h[q][i + 1]), add);
+                            if (start) hh = add;  // the old state is dropped, not multiplied by zero
+                            h[q][i] = hh.x;
+                            h[q][i + 1] = hh.y;
+                            if (kY) part = __ffma2_rn(make_float2(cv[i], cv[i + 1]), hh, part);
+                            if (kBack) {
+                                const int k = kBack ? i : 0, k1 = kBack ? i + 1 : 0;
+                                float2 pp = __fmul2_rn(make_float2(P[q][k], P[q][k1]), e);
+                                if (kCareful && cut) pp = make_float2(0.f, 0.f);
+                                P[q][k] = pp.x, P[q][k1] = pp.y;
+                                const float2 old = make_float2(back[q][k], back[q][k1]);
+                                float2 bb = __ffma2_rn(pp, __fmul2_rn(both(dut), make_float2(cv[i], cv[i + 1])), old);
+                                if (kCareful && cut) bb = old;
+                                back[q][k] = bb.x, back[q][k1] = bb.y;
+                            }
+                        }
+                        a[q] = part.x + part.y;
+                        if (!kY) sum[q] += delta;
+                    }
+                    if (kY) acc[u] = CH == 1 ? a[0] : a[0] + __shfl_xor_sync(0xffffffffu, a[CH - 1], CL);
                 }
                 if (kY) {
 #pragma unroll
-                    for (int i = 0; i < NS; ++i) acc[u] = fmaf(cv[i], h[i], acc[u]);
-                } else {
-                    sum += delta;
-                }
-                if (kBack) {
+                    for (int k = 0; k < K; ++k) {
+                        float v[M];
 #pragma unroll
-                    for (int i = 0; i < NS; ++i) {
-                        const int k = kBack ? i : 0;
-                        back[k] = cut ? back[k] : fmaf(P[k], dut * cv[i], back[k]);
+                        for (int i = 0; i < M; ++i) v[i] = acc[k * M + i];
+                        float u = fmaf(skip, xs[k], share_sums<M>(v, own, CH * CL));
+                        if (gated) {
+                            const float z = load_elem(at + 2 * kRows, k * M * WC);
+                            u *= z * sigmoid<T>(z);
+                        }
+                        store_elem(at, k * M * WC, u);  // in x's place
                     }
                 }
             }
-            if (kY) {
+        };
+        if (tile_starts == 0 && tt + kTile <= t1 && !(kBack && cut)) walk(std::false_type());
+        else walk(std::true_type());
+        if (kY) {
+            __syncwarp();
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    float v[L];
-#pragma unroll
-                    for (int i = 0; i < L; ++i) v[i] = acc[k * L + i];
-                    float u = fmaf(skip, xs[k], share_sums<L>(v, j, CW));
-                    if (gate_at) u *= gate[k] * sigmoid<T>(gate[k]);
-                    const int at = t + k * L + j;
-                    if (on && at < t1) store_elem((T*)p.y.p + b * p.y.b + at * p.y.t + c, 0, u);
+            for (int i = 0; i < S::kEach; ++i) {
+                const int q = i * 32 + lane, row = q / (WC / S::kElems), at = q % (WC / S::kElems) * S::kElems;
+                if ((S::kPieces % 32 == 0 || q < S::kPieces) && tt + row < t1 && first + at < p.channels) {
+                    const T* from = stage + row * WC + at;
+                    T* to = (T*)p.y.p + b * p.y.b + (tt + row) * p.y.t + g * p.channels + first + at;
+                    if constexpr (S::kPiece == 16) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+                    else *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
                 }
             }
         }
-        if (tt + kTile < t1) store_tile(buf ^ 1);
-        __syncthreads();
+        __syncwarp();
     }
-    if (!on) return;
-    if (MODE == kForward) {
-        if (p.h_out && t1 == p.T) {
 #pragma unroll
-            for (int i = 0; i < NS; ++i) p.h_out[(b * p.D + c) * N + j * NS + i] = h[i];
+    for (int q = 0; q < CH; ++q) {
+        if (!on[q]) continue;
+        if (kY) {
+            if (!p.h_out || t1 != p.T) continue;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) p.h_out[(b * p.D + c[q]) * N + j * NS + i] = h[q][i];
+        } else {
+            const long long at = (b * p.chunks + chunk) * p.D + c[q];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                p.chunk_h[at * N + j * NS + i] = h[q][i];
+                if (kBack) p.chunk_g[at * N + j * NS + i] = back[q][kBack ? i : 0];
+            }
+            if (j == 0) p.chunk_s[at] = cut ? INFINITY : sum[q];
         }
-        return;
     }
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        p.chunk_h[state_at + i] = h[i];
-        if (kBack) p.chunk_g[state_at + i] = back[kBack ? i : 0];
-    }
-    if (j == 0) p.chunk_s[(b * p.chunks + chunk) * p.D + c] = cut ? INFINITY : sum;
 }
 
 // ---- host ----------------------------------------------------------------------------
 
-// Launch the walk with `lanes` lanes a channel (N / lanes in {4, 8, 16}).
+// A walk's lanes a channel and channels a lane.
+struct Split {
+    int lanes, channels;
+    int cta() const { return kWarps * channels * 32 / lanes; }  // channels of a CTA
+};
+
 template <typename T, Mode MODE>
-cudaError_t launch_scan(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s);
+cudaError_t launch_scan(const SsmParams& p, Split split, unsigned grid, cudaStream_t s);
 
 // The gradients' second walk (csrc/ssm_bwd.cuh).
 template <typename T>
 cudaError_t launch_gradients(const SsmBwdParams& p, unsigned grid, cudaStream_t s);
 
-inline int channels_cta(int lanes) { return kWarps * (32 / lanes); }
+template <typename S>
+cudaError_t launch_shape(const SsmParams& p, unsigned grid, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(ssm_scan_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)S::kShared);
+    if (e != cudaSuccess) return e;
+    TraceScope trace(S::MODE == kForward ? "ssm_kernel" : S::MODE == kState ? "ssm_state_kernel" : "ssm_summary_kernel",
+                     s);
+    ssm_scan_kernel<S><<<grid, kWarps * 32, S::kShared, s>>>(p);
+    return cudaGetLastError();
+}
 
 template <typename T, Mode MODE>
-cudaError_t launch_scan_here(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
-    TraceScope trace(MODE == kForward ? "ssm_kernel" : MODE == kState ? "ssm_state_kernel" : "ssm_summary_kernel", s);
-    const int threads = kWarps * 32, ns = p.N / lanes;
-#define LA_SSM_CASE(NS, L) \
-    if (ns == NS && lanes == L) ssm_scan_kernel<T, NS, L, MODE><<<grid, threads, 0, s>>>(p);
-    LA_SSM_CASE(8, 1)
-    LA_SSM_CASE(4, 2)
-    LA_SSM_CASE(16, 1)
-    LA_SSM_CASE(8, 2)
-    LA_SSM_CASE(4, 4)
-    LA_SSM_CASE(16, 2)
-    LA_SSM_CASE(8, 4)
-    LA_SSM_CASE(4, 8)
-    LA_SSM_CASE(16, 4)
-    LA_SSM_CASE(8, 8)
-#undef LA_SSM_CASE
-    return cudaGetLastError();
+cudaError_t launch_scan_here(const SsmParams& p, Split split, unsigned grid, cudaStream_t s) {
+    const int ns = p.N / split.lanes;
+#define LA_SSM_SHAPE(CH, NS, L) \
+    if (split.channels == CH && ns == NS && split.lanes == L) return launch_shape<Shape<T, CH, NS, L, MODE>>(p, grid, s);
+    LA_SSM_SHAPE(1, 8, 1)
+    LA_SSM_SHAPE(2, 8, 2)
+    LA_SSM_SHAPE(2, 8, 4)
+    LA_SSM_SHAPE(2, 8, 8)
+    if constexpr (MODE != kSummary) {
+        LA_SSM_SHAPE(1, 4, 2)
+        LA_SSM_SHAPE(1, 4, 4)
+        LA_SSM_SHAPE(1, 4, 8)
+    }
+#undef LA_SSM_SHAPE
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace ssm

@@ -4,16 +4,16 @@
 namespace la::ssm {
 
 template <>
-cudaError_t launch_scan<__nv_bfloat16, kForward>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
-    return launch_scan_here<__nv_bfloat16, kForward>(p, lanes, grid, s);
+cudaError_t launch_scan<__nv_bfloat16, kForward>(const SsmParams& p, Split split, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<__nv_bfloat16, kForward>(p, split, grid, s);
 }
 template <>
-cudaError_t launch_scan<__nv_bfloat16, kState>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
-    return launch_scan_here<__nv_bfloat16, kState>(p, lanes, grid, s);
+cudaError_t launch_scan<__nv_bfloat16, kState>(const SsmParams& p, Split split, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<__nv_bfloat16, kState>(p, split, grid, s);
 }
 template <>
-cudaError_t launch_scan<__nv_bfloat16, kSummary>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
-    return launch_scan_here<__nv_bfloat16, kSummary>(p, lanes, grid, s);
+cudaError_t launch_scan<__nv_bfloat16, kSummary>(const SsmParams& p, Split split, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<__nv_bfloat16, kSummary>(p, split, grid, s);
 }
 
 }  // namespace la::ssm

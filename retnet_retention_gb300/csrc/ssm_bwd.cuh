@@ -160,14 +160,14 @@ __global__ void __launch_bounds__(kBwdWarps * 32) ssm_gradients_kernel(const __g
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const bool there = on[0] && t + k * M + own < t1;
-            xs[k] = there ? load_one(&nx[k]) : 0.f;
-            const float v = load_one(&ndt[k]) + bias;
+            xs[k] = there ? load_elem(nx, k) : 0.f;
+            const float v = load_elem(ndt, k) + bias;
             d[k] = there ? (p.softplus ? softplus<T>(v) : v) : 0.f;
             slope[k] = there ? (p.softplus ? sigmoid<T>(v) : 1.f) : 0.f;
-            du[k] = there ? load_one(&ndy[k]) : 0.f;
+            du[k] = there ? load_elem(ndy, k) : 0.f;
             f_gate[k] = 0.f;
             if (gated) {
-                const float z = there ? load_one(&ngate[k]) : 0.f, s = sigmoid<T>(z), a = z * s;
+                const float z = there ? load_elem(ngate, k) : 0.f, s = sigmoid<T>(z), a = z * s;
                 f_gate[k] = du[k] * fmaf(a, 1.f - s, s);
                 du[k] *= a;
             }

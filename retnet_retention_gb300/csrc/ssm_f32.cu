@@ -4,16 +4,16 @@
 namespace la::ssm {
 
 template <>
-cudaError_t launch_scan<float, kForward>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
-    return launch_scan_here<float, kForward>(p, lanes, grid, s);
+cudaError_t launch_scan<float, kForward>(const SsmParams& p, Split split, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<float, kForward>(p, split, grid, s);
 }
 template <>
-cudaError_t launch_scan<float, kState>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
-    return launch_scan_here<float, kState>(p, lanes, grid, s);
+cudaError_t launch_scan<float, kState>(const SsmParams& p, Split split, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<float, kState>(p, split, grid, s);
 }
 template <>
-cudaError_t launch_scan<float, kSummary>(const SsmParams& p, int lanes, unsigned grid, cudaStream_t s) {
-    return launch_scan_here<float, kSummary>(p, lanes, grid, s);
+cudaError_t launch_scan<float, kSummary>(const SsmParams& p, Split split, unsigned grid, cudaStream_t s) {
+    return launch_scan_here<float, kSummary>(p, split, grid, s);
 }
 
 }  // namespace la::ssm

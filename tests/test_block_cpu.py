@@ -185,7 +185,7 @@ def pairs(count, **over):
     return arr(*[s for p in v for s in p])
 
 
-SSM_ALL = [dict(B=-1), dict(B=65536), dict(D=0), dict(D=24), dict(N=4), dict(N=12), dict(N=128), dict(G=0), dict(G=3),
+SSM_ALL = [dict(B=-1), dict(B=65536), dict(D=0), dict(D=24), dict(N=4), dict(N=12), dict(N=128), dict(G=0), dict(G=3), dict(G=16),
            dict(ty=2), dict(flags=2), dict(x=None), dict(dt=None), dict(A=None), dict(b=None), dict(c=None),
            dict(x=at(0) + 8), dict(A=at(2) + 4), dict(b=at(3) + 2), dict(k=at(5) + 4), dict(bias=at(7) + 8),
            dict(g=at(6) + 8), dict(h0=at(8) + 4)]
