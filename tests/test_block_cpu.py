@@ -193,9 +193,6 @@ SSM_FWD = SSM_ALL + [dict(T=-1), dict(y=None), dict(y=at(0)), dict(y=at(3)), dic
                      dict(h=at(10) + 4), dict(y=at(9) + 2), dict(pos=at(9)), dict(pos=at(23) + 4),
                      dict(st=pairs(6, _0=(192, 60))), dict(st=pairs(6, _2=(96, -32))), dict(st=pairs(6, _5=(192, 32))),
                      dict(st=pairs(6, _5=(0, 64))), dict(st=pairs(6, _4=(1 << 50, 64)))]
-# long sequences of few channels are cut: a workspace is needed
-LONG = dict(B=1, T=4096, D=16, N=8, G=1)
-SSM_FWD += [dict(LONG, ws=None, wb=0), dict(LONG, ws=at(11) + 4), dict(LONG, wb=16), dict(LONG, ws=at(9))]
 SSM_BWD = SSM_ALL + [dict(T=-1), dict(dy=None), dict(dx=None), dict(ddt=None), dict(db=None), dict(dc=None), dict(dg=None),
                      dict(g=None), dict(dx=at(0)), dict(ddt=at(1)), dict(db=at(4)), dict(dA=at(2)), dict(dk=at(5)),
                      dict(dbias=at(19)), dict(dh0=at(13)), dict(dh0=at(8)), dict(dx=at(15)), dict(ws=None), dict(wb=0),
@@ -266,7 +263,6 @@ def test_workspaces_are_asked_for_sizes_that_hold(lib):
     for bad in ((2, 9, 24, 16, 1, 1), (2, 9, 64, 7, 1, 1), (2, 9, 64, 16, 3, 1), (2, 9, 64, 16, 1, 5), (-1, 9, 64, 16, 1, 1)):
         assert lib.la_ssm_workspace_size(*bad) == lib.la_ssm_bwd_workspace_size(*bad) == 0
     assert lib.la_short_conv_bwd_workspace_size(2, 9, 64, 5, 1) == lib.la_block_norm_bwd_workspace_size(2, 9, 24, 1, 2) == 0
-    assert lib.la_ssm_workspace_size(1, 65536, 16, 8, 1, 1) > 0
     small, large = (lib.la_ssm_bwd_workspace_size(2, T, 64, 16, 1, 1) for T in (64, 640))
     assert 0 < small < large
 

@@ -214,6 +214,26 @@ def test_outputs_end_where_they_end():
     assert bool((gw[..., 3 * D:3 * D + 16] == 3).all()) and bool((gw[..., 3 * D + 48:] == 3).all())
 
 
+def test_a_cut_sequence_needs_its_workspace():
+    """Long sequences of few channels are cut: without room for the chunks' states the call
+    is refused (on the host, its pointers untouched)."""
+    import ctypes
+    lib, at = la.library(), lambda k: 0x10000000 + 0x100000 * k
+    need = lib.la_ssm_workspace_size(1, 4096, 16, 8, 1, 1)
+    assert need > 0
+
+    def call(ws, size):
+        return lib.la_ssm_fwd(at(0), at(1), at(2), at(3), at(4), None, None, None, None, 1, 1, 4096, 16, 8, 1, 1, None,
+                              None, at(9), None, ws, size, None)
+
+    for ws, size in ((None, 0), (at(11) + 4, need), (at(11), need - 1), (at(9), need), (at(3), need)):
+        assert call(ws, ctypes.c_size_t(size)) == la.LA_ERR_INVALID_ARG
+    x = torch.zeros(1, 4096, 16, device=DEV)
+    with pytest.raises(ValueError, match="workspace"):
+        la.ssm_fwd(x, x, torch.zeros(16, 8, device=DEV), x[..., :8], x[..., 8:],
+                   workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
 def test_no_tokens():
     x, A = torch.zeros(2, 0, 32, device=DEV), torch.ones(32, 8, device=DEV)
     b, h0 = torch.zeros(2, 0, 8, device=DEV), torch.randn(2, 32, 8, device=DEV)
