@@ -53,26 +53,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32) ssm_join_kernel(
         const float s = chunk_s[i * D + d];
         return s == INFINITY ? 0.f : exp2_fast(s * a);
     };
-    float P = 1.f, sum = 0.f;
+    // batches of kBatch chunks, their loads in flight together (a store in between would hold
+    // the next one's back)
+    constexpr int kBatch = 8;
+    float e[kBatch], add[kBatch];
+    auto load = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            e[i] = 1.f, add[i] = 0.f;
+            if (k + i < k1) {
+                e[i] = decay(at(k + i));
+                add[i] = v[at(k + i) * cols + col];
+            }
+        }
+    };
+    load(k0);
+    float s = s0 ? s0[b * cols + col] : 0.f;
     if (warps > 1) {
-#pragma unroll 4
-        for (int k = k0; k < k1; ++k) {
-            const long long i = at(k);
-            const float e = decay(i);
-            sum = after(e, v[i * cols + col], sum);
-            P *= e;
+        float P = 1.f, sum = 0.f;
+        for (int k = k0; k < k1; k += kBatch) {
+            if (k > k0) load(k);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                sum = after(e[i], add[i], sum);
+                P *= e[i];
+            }
         }
         runs[w][lane] = make_float2(P, sum);
         __syncthreads();
+        for (int k = 0; k < w; ++k) s = after(runs[k][lane].x, runs[k][lane].y, s);
     }
-    float s = s0 ? s0[b * cols + col] : 0.f;
-    for (int k = 0; k < w; ++k) s = after(runs[k][lane].x, runs[k][lane].y, s);
-#pragma unroll 4
-    for (int k = k0; k < k1; ++k) {
-        const long long i = at(k);
-        const float e = decay(i), add = v[i * cols + col];
-        v[i * cols + col] = s;
-        s = after(e, add, s);
+    for (int k = k0; k < k1; k += kBatch) {
+        if (k > k0 || k1 - k0 > kBatch) load(k);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (k + i < k1) {
+                v[at(k + i) * cols + col] = s;
+                s = after(e[i], add[i], s);
+            }
     }
 }
 
@@ -217,7 +235,7 @@ Plan forward_plan(const SsmArgs& a) {
 
 Plan backward_plan(const SsmArgs& a, int channels) {
     const long long tiles = (a.D / a.G + channels - 1) / channels;
-    const long long ctas = (long long)a.B * a.G * tiles, want = (long long)sm_count() * 16;
+    const long long ctas = (long long)a.B * a.G * tiles, want = (long long)sm_count() * 28;
     const long long chunks = std::max<long long>(1, std::min<long long>((want + ctas - 1) / ctas, a.T / 64));
     return plan_of(a, wide_split(a.N), channels, chunks);
 }
@@ -265,7 +283,7 @@ size_t backward_workspace(const SsmArgs& a, const Plan& plan, SsmBwdParams* bp) 
 }
 
 cudaError_t join(const SsmParams& p, bool forward, bool backward, const float* dh_T, cudaStream_t s) {
-    const int warps = std::min(kJoinWarps, std::max(1, p.chunks / 4));
+    const int warps = std::min(kJoinWarps, (p.chunks + 7) / 8);
     const dim3 grid((unsigned)((long long)p.D * p.N / 32), p.B, forward && backward ? 2 : 1);
     TraceScope trace("ssm_join_kernel", s);
     ssm_join_kernel<<<grid, warps * 32, 0, s>>>(forward ? p.chunk_h : nullptr, p.h0, p.chunk_g, dh_T, p.chunk_s, p.A,

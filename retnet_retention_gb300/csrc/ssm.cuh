@@ -78,11 +78,16 @@ __device__ __forceinline__ float log1p_unit(float p) {
     return q * p;
 }
 
-// softplus(v) = max(v, 0) + log(1 + e^-|v|); the bf16 form takes 2^x of the scaled
-// argument (its error, relative, 2^-22 |v|), fp32 expf.
+// softplus(v) = max(v, 0) + log(1 + e^-|v|), and its slope 1 / (1 + e^-v) where asked for; the
+// bf16 form takes 2^x of the scaled argument (its error, relative, 2^-22 |v|), fp32 expf.
 template <typename T>
-__device__ __forceinline__ float softplus(float v) {
+__device__ __forceinline__ float softplus(float v, float* slope = nullptr) {
     const float p = sizeof(T) == 2 ? exp2_fast(-fabsf(v) * kLog2e) : expf(-fabsf(v));
+    if (slope) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + p));  // 1 ulp
+        *slope = v >= 0.f ? r : p * r;
+    }
     return fmaxf(v, 0.f) + log1p_unit(p);
 }
 
