@@ -475,6 +475,7 @@ size_t la_block_norm_bwd_workspace_size(int B, int T, int D, la_dtype dtype, uns
     BlockNormArgs a;
     std::memset(&a, 0, sizeof(a));
     a.B = B; a.T = T; a.D = D;
+    a.bf16 = dtype == LA_DTYPE_BF16;
     a.gate_each = (flags & LA_BLOCK_GATE_EACH) != 0;
     static const float present = 1.f;
     a.gate = a.gate_each ? &present : nullptr;  // only whether there is one counts

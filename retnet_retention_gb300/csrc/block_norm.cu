@@ -149,7 +149,7 @@ constexpr int kRing = 3;
 
 // T: o and y; R: the residual stream.  P pieces of eight entries a thread.
 template <typename T, typename R, int P, int THREADS, bool CENTER>
-__global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_constant__ BlockParams p) {
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS) block_norm_kernel(const __grid_constant__ BlockParams p) {
     __shared__ __align__(16) float red[4][kRedFloats];
     clear_red(red, 4);
     extern __shared__ __align__(16) unsigned char ring[];  // [kRing][P][threads] of T's eight, then of R's
@@ -205,30 +205,29 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
                 for (int j = 0; j < 4; ++j) gw[i][j] = __fmul2_rn(gw[i][j], __fmul2_rn(g[j], both(p.alpha)));
             }
         }
-        float2 v[P][4], h[P][4];
+        float2 v[P][4];
         copies_wait<kRing - 1>();
 #pragma unroll
         for (int i = 0; i < P; ++i) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] = h[i][j] = make_float2(0.f, 0.f);
-            if (row && on[i]) {
-                floats8<false>(raw8<true>(slots_o + (slot * P + i) * piece, 0, 4), v[i]);
-                if (p.h.p) floats8<false>(raw8<true>(slots_h + (slot * P + i) * piece, 0, 4), h[i]);
-            }
+            for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.f, 0.f);
+            if (row && on[i]) floats8<false>(raw8<true>(slots_o + (slot * P + i) * piece, 0, 4), v[i]);
         }
-        fetch(slot);
-        slot = slot + 1 == kRing ? 0 : slot + 1;
         float r = 1.f;
         if (p.post) r = normed<CENTER, P>(v, on, inv_d, p.eps, red[at.slot], turn, at);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
+            float2 h[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+            if (row && on[i] && p.h.p) floats8<false>(raw8<true>(slots_h + (slot * P + i) * piece, 0, 4), h);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 v[i][j] = __fmul2_rn(__fmul2_rn(v[i][j], both(r)), gw[i][j]);
-                v[i][j] = __ffma2_rn(h[i][j], both(p.beta), v[i][j]);
+                v[i][j] = __ffma2_rn(h[j], both(p.beta), v[i][j]);
             }
             if (row && on[i] && p.h_out.p) store8<true, false>(here.at<R>(p.h_out) + e[i], 0, 4, v[i]);
         }
+        fetch(slot);
+        slot = slot + 1 == kRing ? 0 : slot + 1;
         if (p.pre) {
             r = normed<CENTER, P>(v, on, inv_d, p.eps, red[at.slot], turn, at);
 #pragma unroll
@@ -242,20 +241,19 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
     }
 }
 
-// Rows of the gradients' ring: one of fp32 entries where a CTA has 512 threads (two would not fit an
-// SM's shared memory).
-template <typename T, int THREADS>
-constexpr int kBwdRingOf = sizeof(T) == 4 && THREADS == 512 ? 1 : 2;
+// Rows of the gradients' ring: one where a CTA has 512 threads (two of fp32 entries would not fit
+// an SM's shared memory).
+constexpr int bwd_ring(int threads) { return threads > 256 ? 1 : 2; }
 
 // A CTA takes rows of one sequence where each sequence has its own gate (its sums then
 // belong to that sequence's gradient), else of all.
 template <typename T, typename R, int P, int THREADS, bool CENTER>
-__global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const __grid_constant__ BlockParams p) {
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(const __grid_constant__ BlockParams p) {
     tc::griddep_launch_dependents();  // the sums' kernel may be scheduled (it waits itself)
     __shared__ __align__(16) float red[4][kRedFloats];
     clear_red(red, 4);
     extern __shared__ __align__(16) unsigned char ring[];  // o, dy, h, dh; at the end [rows_cta][D] sums
-    constexpr int kBwdRing = kBwdRingOf<T, THREADS>;
+    constexpr int kBwdRing = bwd_ring(THREADS);
     const Place at(p.rows_cta);
     const int width = at.warps * 32 * 8;
     const unsigned begin = p.seq_blocks ? blockIdx.x / p.seq_blocks * p.by_T.T : 0;
@@ -269,8 +267,12 @@ __global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const __grid_co
     int turn = 0;
     bool on[P];
     int e[P];
-    float2 s_post[P][4], s_pre[P][4], gw[P][4], w_pre[P][4];  // sums of alpha dt p and dy n; alpha g w_post
+    float2 s_post[P][4], s_pre[P][4];  // sums of alpha dt p and dy n
     const float* gate = p.gate ? p.gate + (p.seq_blocks ? (size_t)(blockIdx.x / p.seq_blocks) * p.D : 0) : nullptr;
+    // the thread's entries of alpha g w_post and of w_pre, in shared memory: two quads of each
+    float4* const gws = reinterpret_cast<float4*>(reinterpret_cast<R*>(ring + (size_t)kBwdRing * 2 * P * piece * sizeof(T)) +
+                                                  (size_t)kBwdRing * 2 * P * piece) + threadIdx.x;
+    float4* const w_pres = gws + 2 * P * blockDim.x;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         e[i] = i * width + at.lane * 8;
@@ -301,36 +303,52 @@ __global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const __grid_co
     for (int i = 0; i < kBwdRing; ++i) fetch(i);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        float2 g[4];
-        row_weights<false>(p.w_pre, on[i], e[i], e[i] + 4, w_pre[i]);
-        row_weights<false>(p.w_post, on[i], e[i], e[i] + 4, gw[i]);
+        float2 g[4], w[4];
+        row_weights<false>(p.w_post, on[i], e[i], e[i] + 4, w);
         row_weights<false>(gate, on[i], e[i], e[i] + 4, g);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) gw[i][j] = __fmul2_rn(gw[i][j], __fmul2_rn(g[j], both(p.alpha)));
+        for (int j = 0; j < 4; ++j) g[j] = __fmul2_rn(w[j], __fmul2_rn(g[j], both(p.alpha)));
+        row_weights<false>(p.w_pre, on[i], e[i], e[i] + 4, w);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            gws[(2 * i + k) * blockDim.x] = make_float4(g[2 * k].x, g[2 * k].y, g[2 * k + 1].x, g[2 * k + 1].y);
+            w_pres[(2 * i + k) * blockDim.x] = make_float4(w[2 * k].x, w[2 * k].y, w[2 * k + 1].x, w[2 * k + 1].y);
+        }
     }
+    auto weights = [&](const float4* from, int i, float2 (&w)[4]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float4 f = from[(2 * i + k) * blockDim.x];
+            w[2 * k] = make_float2(f.x, f.y);
+            w[2 * k + 1] = make_float2(f.z, f.w);
+        }
+    };
     int slot = 0;
     for (unsigned m = first; m - at.slot < end; m += leap) {
         const bool row = m < end;
-        float2 n[P][4], q[P][4], d[P][4], dt[P][4];  // norm(h'), p, dy, dt
+        float2 n[P][4], q[P][4], dt[P][4];  // norm(h'), p, and dy on its way to dt
         copies_wait<kBwdRing - 1>();
+        auto take = [&](auto* slots, int which, int i, float2 (&to)[4]) {  // zeros where there is nothing
+            if (row && on[i]) {
+                floats8<false>(raw8<true>(slots + (slot * 2 * P + which * P + i) * piece, 0, 4), to);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) to[j] = make_float2(0.f, 0.f);
+            }
+        };
+        // both rows' norms: means, then squares
+        float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < P; ++i) {
+            take(slots_t, 0, i, q[i]);
+            if (p.pre) {
+                take(slots_r, 0, i, n[i]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) n[i][j] = q[i][j] = d[i][j] = dt[i][j] = make_float2(0.f, 0.f);
-            if (row && on[i]) {
-                floats8<false>(raw8<true>(slots_t + (slot * 2 * P + i) * piece, 0, 4), q[i]);
-                if (p.pre) {
-                    floats8<false>(raw8<true>(slots_t + (slot * 2 * P + P + i) * piece, 0, 4), d[i]);
-                    floats8<false>(raw8<true>(slots_r + (slot * 2 * P + i) * piece, 0, 4), n[i]);
-                }
-                if (p.dh.p) floats8<false>(raw8<true>(slots_r + (slot * 2 * P + P + i) * piece, 0, 4), dt[i]);
+                for (int j = 0; j < 4; ++j) n[i][j] = make_float2(0.f, 0.f);
             }
         }
-        fetch(slot);
-        slot = slot + 1 == kBwdRing ? 0 : slot + 1;
-        // both rows' norms: means, then squares
         if (CENTER) {
-            float s[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < P; ++i) s[0] += sum8(n[i]), s[1] += sum8(q[i]);
             row_sums<2>(s, red[at.slot], turn, at.warps, at.warp);
@@ -343,8 +361,8 @@ __global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const __grid_co
                         n[i][j] = __fadd2_rn(n[i][j], mh);
                         q[i][j] = __fadd2_rn(q[i][j], mo);
                     }
+            s[0] = s[1] = 0.f;
         }
-        float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < P; ++i) s[0] += dot8(n[i], n[i]), s[1] += dot8(q[i], q[i]);
         row_sums<2>(s, red[at.slot], turn, at.warps, at.warp);
@@ -353,43 +371,54 @@ __global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const __grid_co
             s[0] = s[1] = 0.f;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
+                float2 w[4];
+                take(slots_t, 1, i, dt[i]);
+                weights(w_pres, i, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     n[i][j] = __fmul2_rn(n[i][j], both(rh));
-                    s_pre[i][j] = __ffma2_rn(d[i][j], n[i][j], s_pre[i][j]);
-                    d[i][j] = __fmul2_rn(d[i][j], w_pre[i][j]);
+                    s_pre[i][j] = __ffma2_rn(dt[i][j], n[i][j], s_pre[i][j]);
+                    dt[i][j] = __fmul2_rn(dt[i][j], w[j]);
                 }
-                s[0] += dot8(d[i], n[i]);
-                if (CENTER) s[1] += sum8(d[i]);
+                s[0] += dot8(dt[i], n[i]);
+                if (CENTER) s[1] += sum8(dt[i]);
             }
             row_sums<2>(s, red[at.slot], turn, at.warps, at.warp);
-            const float2 along = both(-s[0] * inv_d), mean = both(CENTER ? -s[1] * inv_d : 0.f);
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (on[i])
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        dt[i][j] = __ffma2_rn(both(rh), __ffma2_rn(n[i][j], along, __fadd2_rn(d[i][j], mean)),
-                                              dt[i][j]);
         }
+        const float2 along_h = both(-s[0] * inv_d), mean_h = both(CENTER ? -s[1] * inv_d : 0.f);
         s[0] = s[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            if (row && on[i] && p.d_res.p) {
-                float2 out[4];
+            float2 into[4], w[4];
+            if (p.dh.p) {
+                take(slots_r, 1, i, into);
+            } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) out[j] = __fmul2_rn(dt[i][j], both(p.beta));
-                store8<true, false>(here.at<R>(p.d_res) + e[i], 0, 4, out);
+                for (int j = 0; j < 4; ++j) into[j] = make_float2(0.f, 0.f);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (p.pre && on[i])
+                    into[j] = __ffma2_rn(both(rh), __ffma2_rn(n[i][j], along_h, __fadd2_rn(dt[i][j], mean_h)), into[j]);
+                dt[i][j] = into[j];
+            }
+            if (row && on[i] && p.d_res.p) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) into[j] = __fmul2_rn(into[j], both(p.beta));
+                store8<true, false>(here.at<R>(p.d_res) + e[i], 0, 4, into);
+            }
+            weights(gws, i, w);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 q[i][j] = __fmul2_rn(q[i][j], both(ro));
                 s_post[i][j] = __ffma2_rn(__fmul2_rn(dt[i][j], both(p.alpha)), q[i][j], s_post[i][j]);
-                dt[i][j] = __fmul2_rn(dt[i][j], gw[i][j]);
+                dt[i][j] = __fmul2_rn(dt[i][j], w[j]);
             }
             s[0] += dot8(dt[i], q[i]);
             if (CENTER) s[1] += sum8(dt[i]);
         }
+        fetch(slot);
+        slot = slot + 1 == kBwdRing ? 0 : slot + 1;
         if (p.post) {
             row_sums<2>(s, red[at.slot], turn, at.warps, at.warp);
             const float2 along = both(-s[0] * inv_d), mean = both(CENTER ? -s[1] * inv_d : 0.f);
@@ -456,18 +485,33 @@ Shape shape(int D) {
     return s;
 }
 
-constexpr int kFwdThreadsPerSm = 768, kBwdThreadsPerSm = 512;
+// Bytes of a CTA's shared memory, T and R the sizes of an entry of o and of the residual.
+size_t fwd_shared(const Shape& sh, size_t T, size_t R) { return (size_t)kRing * sh.pieces * sh.threads * sh.rows * 8 * (T + R); }
+size_t bwd_shared(const Shape& sh, size_t T, size_t R) {
+    const size_t entries = (size_t)sh.pieces * sh.threads * sh.rows * 8;
+    return entries * (bwd_ring(sh.threads * sh.rows) * 2 * (T + R) + 2 * sizeof(float));  // the sums at the end fit in the ring
+}
+
+// CTAs an SM holds: by the registers the launch bounds leave a thread, and by shared memory.
+long long resident(const Shape& sh, int threads_per_sm, size_t shared) {
+    const long long by_threads = threads_per_sm / (sh.threads * sh.rows), by_shared = (long long)((224u << 10) / (shared + 2048));
+    return std::max(1ll, std::min(by_threads, by_shared));
+}
+
+size_t entry_size(bool bf16) { return bf16 ? 2 : 4; }
 
 long long fwd_blocks(const BlockNormArgs& a) {
     const Shape sh = shape(a.D);
     const long long rows = ((long long)a.B * a.T + sh.rows - 1) / sh.rows;
-    return std::min(rows, (long long)sm_count() * std::max(1, kFwdThreadsPerSm / (sh.threads * sh.rows)));
+    const size_t shared = fwd_shared(sh, entry_size(a.bf16), entry_size(a.residual_bf16));
+    return std::min(rows, sm_count() * resident(sh, sh.threads > 256 ? 512 : 768, shared));
 }
 
 // CTAs of the gradients: (of each sequence, in all).
 void bwd_blocks(const BlockNormArgs& a, int* each, long long* all) {
     const Shape sh = shape(a.D);
-    const long long most = (long long)sm_count() * std::max(1, kBwdThreadsPerSm / (sh.threads * sh.rows));
+    // as many for either type of the residual: the workspace's size is asked for without it
+    const long long most = sm_count() * resident(sh, 512, bwd_shared(sh, entry_size(a.bf16), 4));
     if (a.gate && a.gate_each) {
         const long long rows = ((long long)a.T + sh.rows - 1) / sh.rows;
         *each = (int)std::max(1ll, std::min(rows, most / a.B));
@@ -500,10 +544,8 @@ BlockParams params(const BlockNormArgs& a) {
 
 template <typename T, typename R, int P, int THREADS, bool CENTER>
 cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, int threads, cudaStream_t s) {
-    const size_t piece = (size_t)P * threads * 8;
-    const size_t shared = bwd ? std::max(kBwdRingOf<T, THREADS> * 2 * piece * (sizeof(T) + sizeof(R)),
-                                         (size_t)p.rows_cta * p.D * sizeof(float))
-                              : kRing * piece * (sizeof(T) + sizeof(R));
+    const Shape sh = shape(p.D);
+    const size_t shared = bwd ? bwd_shared(sh, sizeof(T), sizeof(R)) : fwd_shared(sh, sizeof(T), sizeof(R));
     const auto kernel = bwd ? block_norm_bwd_kernel<T, R, P, THREADS, CENTER> : block_norm_kernel<T, R, P, THREADS, CENTER>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
     if (e != cudaSuccess) return e;

@@ -148,9 +148,34 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
     return e;
 }
 
-// Rows of the ring, and tokens of the unrolled loop: a multiple of the W - 1 rows kept.
+// Tokens of the unrolled loop, a multiple of the W - 1 rows kept (a long loop does not stay in
+// the instruction cache: nine tokens of the gradients took 119 us where three take 100), and
+// rows of the ring, a multiple of those.
+template <int W>
+constexpr int kUnrollOf = W == 4 ? 3 : 4;
 template <int W>
 constexpr int kAheadOf = W == 4 ? 9 : 8;
+
+// How far the taps of the next tokens reach, loaded a turn of the loop before it is looked at.
+template <int W>
+struct Reaches {
+    static constexpr int U = kUnrollOf<W>;
+    int next[U], now[U];
+    bool full;  // all of now's taps count
+
+    __device__ __forceinline__ void load(const int* pos, int m0, int n) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) next[i] = pos && m0 + i < n ? __ldg(pos + m0 + i) : W - 1;
+    }
+    __device__ __forceinline__ void turn() {
+        full = true;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            now[i] = next[i];
+            full = full && now[i] >= W - 1;
+        }
+    }
+};
 
 // f(0), .. f(N - 1) with the index a constant.
 template <int N, int I = 0, typename F>
@@ -177,7 +202,7 @@ __device__ __forceinline__ void copy_pack(void* to, const T* from) {
 
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const __grid_constant__ ConvParams p) {
-    constexpr int V = 16 / (int)sizeof(T), kAhead = kAheadOf<W>;
+    constexpr int V = 16 / (int)sizeof(T), kAhead = kAheadOf<W>, U = kUnrollOf<W>;
     __shared__ __align__(16) uint4 ring[kAhead][kThreads];
     const int tile = (int)(blockIdx.x % (unsigned)p.tiles);
     const int c = (tile * p.lanes + (int)threadIdx.x % p.lanes) * V;
@@ -209,27 +234,19 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const __grid_co
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) last[j].store((T*)p.state_out + (b * (W - 1) + j) * p.D + c);
     }
-    // The next kAhead tokens whose taps do not all count, a bit each.
-    auto shorts = [&](int m0) {
-        unsigned bits = 0;
-        if (pos) {
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (m0 + i < n) bits |= (__ldg(pos + m0 + i) < W - 1 ? 1u : 0u) << i;
-        }
-        return bits;
-    };
-    unsigned now = shorts(0);
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
-        const unsigned next = shorts(i0 + kAhead);
+    Reaches<W> reaches;
+    reaches.load(pos, 0, n);
+    for (int i0 = 0, slot = 0; i0 < n; i0 += U, slot = slot + U == kAhead ? 0 : slot + U) {
+        reaches.turn();
+        reaches.load(pos, i0 + U, n);
         auto token = [&](auto index, int reach) {
             constexpr int i = decltype(index)::value;
             copies_wait<kAhead - 1>();
             Pack<T, V> r;
             float2 cur[V / 2], u[V / 2];
-            r.load(reinterpret_cast<const T*>(&ring[i][threadIdx.x]));
+            r.load(reinterpret_cast<const T*>(&ring[slot + i][threadIdx.x]));
             r.floats(cur);
-            fetch(i0 + i + kAhead, i);
+            fetch(i0 + i + kAhead, slot + i);
             convolve<W, V, i>(w, bias, before, cur, reach, u);
 #pragma unroll
             for (int k = 0; k < V / 2; ++k) before[i % (W - 1)][k] = cur[k];
@@ -241,15 +258,14 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const __grid_co
             r.store(y);
             y += p.yt;
         };
-        if (now == 0 && i0 + kAhead <= n) {
-            each<kAhead>([&](auto index) { token(index, W - 1); });
+        if (reaches.full && i0 + U <= n) {
+            each<U>([&](auto index) { token(index, W - 1); });
         } else {
-            each<kAhead>([&](auto index) {
+            each<U>([&](auto index) {
                 constexpr int i = decltype(index)::value;
-                if (i0 + i < n) token(index, now >> i & 1 ? __ldg(pos + i0 + i) : W - 1);
+                if (i0 + i < n) token(index, reaches.now[i]);
             });
         }
-        now = next;
     }
 }
 
@@ -257,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const __grid_co
 // token t - W + 1.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __grid_constant__ ConvParams p) {
-    constexpr int V = 4, kAhead = kAheadOf<W>;
+    constexpr int V = 4, kAhead = kAheadOf<W>, U = kUnrollOf<W>;
     tc::griddep_launch_dependents();  // the sums' kernel may be scheduled (it waits itself)
     using Piece = std::conditional_t<sizeof(T) == 2, uint2, uint4>;
     __shared__ __align__(16) Piece ring[kAhead][2][kThreads];  // x, dy
@@ -303,19 +319,12 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __gri
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) dus[j][e] = make_float2(0.f, 0.f);
             }
-            auto shorts = [&](int m0) {  // as forward
-                unsigned bits = 0;
-                if (pos) {
-#pragma unroll
-                    for (int i = 0; i < kAhead; ++i)
-                        if (m0 + i < there) bits |= (__ldg(pos + m0 + i) < W - 1 ? 1u : 0u) << i;
-                }
-                return bits;
-            };
-            unsigned now = shorts(0);
+            Reaches<W> reaches;
+            reaches.load(pos, 0, there);
             bool clean = true;  // the last rows' taps all counted
-            for (int i0 = 0; i0 < n + W - 1; i0 += kAhead) {
-                const unsigned next = shorts(i0 + kAhead);
+            for (int i0 = 0, slot = 0; i0 < n + W - 1; i0 += U, slot = slot + U == kAhead ? 0 : slot + U) {
+                reaches.turn();
+                reaches.load(pos, i0 + U, there);
                 // WHOLE: a token of the run, as is the one it completes, every tap counts, and the
                 // sequence's last rows are not reached
                 auto token = [&](auto index, auto whole) {
@@ -329,13 +338,13 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __gri
                     for (int e = 0; e < V / 2; ++e) cur[e] = du[e] = make_float2(0.f, 0.f);
                     if (kWhole || m < there) {
                         Pack<T, V> in;
-                        in.load(reinterpret_cast<const T*>(&ring[i][0][threadIdx.x]));
+                        in.load(reinterpret_cast<const T*>(&ring[slot + i][0][threadIdx.x]));
                         in.floats(cur);
-                        in.load(reinterpret_cast<const T*>(&ring[i][1][threadIdx.x]));
+                        in.load(reinterpret_cast<const T*>(&ring[slot + i][1][threadIdx.x]));
                         in.floats(du);
-                        if (!kWhole && now >> i & 1) reach = __ldg(pos + m);
+                        if (!kWhole) reach = reaches.now[i];
                     }
-                    fetch(m + kAhead, i);
+                    fetch(m + kAhead, slot + i);
                     if (p.silu && (kWhole || m < there)) {
                         float2 u[V / 2];
                         convolve<W, V, i>(w, bias, before, cur, reach, u);
@@ -394,13 +403,12 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __gri
                         dus[i % kMod][e] = du[e];
                     }
                 };
-                if (now == 0 && clean && i0 >= W - 1 && i0 + kAhead <= n) {
-                    each<kAhead>([&](auto index) { token(index, std::true_type()); });
+                if (reaches.full && clean && i0 >= W - 1 && i0 + U <= n) {
+                    each<U>([&](auto index) { token(index, std::true_type()); });
                 } else {
-                    each<kAhead>([&](auto index) { token(index, std::false_type()); });
+                    each<U>([&](auto index) { token(index, std::false_type()); });
                 }
-                clean = now >> (kAhead - (W - 1)) == 0;
-                now = next;
+                clean = reaches.full;  // U is at least W - 1
             }
             copies_wait<0>();
         }

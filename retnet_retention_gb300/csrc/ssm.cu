@@ -131,50 +131,86 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
     v[3] = __uint_as_float(r.y & 0xffff0000u);
 }
 
-// Four states a lane: a channel's N / 4 lanes lie side by side; a CTA keeps its channels
-// and walks sequences, so that A is read once.
-template <typename T>
+// Four states a lane: a channel's L = N / 4 lanes lie side by side; a CTA keeps its channels and
+// walks sequences, four at a time, so that A is read once.  The elementwise work of a sequence's
+// channel is one lane's, as in the walk over tokens.
+template <typename T, int N>
 __global__ void __launch_bounds__(128) ssm_step_kernel(const __grid_constant__ SsmParams p) {
-    const int lanes = p.N / 4, j = threadIdx.x % lanes;
-    const int c = (int)((blockIdx.x * 128u + threadIdx.x) / (unsigned)lanes);
+    constexpr int L = N / 4, R = 4, M = L < R ? L : R, K = R / M;  // own sequences: every M-th of R
+    const int j = threadIdx.x % L, own = j % M, base = (threadIdx.x & 31) - j;
+    const int c = (int)((blockIdx.x * 128u + threadIdx.x) / (unsigned)L);
     const bool on = c < p.D;
     const int cc = on ? c : 0, g = cc / p.channels;
-    const float4 a4 = __ldg(reinterpret_cast<const float4*>(p.A + (size_t)cc * p.N) + j);
-    const float A[4] = {a4.x * kLog2e, a4.y * kLog2e, a4.z * kLog2e, a4.w * kLog2e};
+    float A[4];
+    load4(p.A + (size_t)cc * N + 4 * j, A);
     const float skip = p.skip ? p.skip[cc] : 0.f, bias = p.bias ? p.bias[cc] : 0.f;
-    constexpr int R = 4;  // sequences whose loads are in flight
+#pragma unroll
+    for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
+    const T* const bm = (const T*)p.bm.p + g * N + 4 * j;
+    const T* const cm = (const T*)p.cm.p + g * N + 4 * j;
     for (int b0 = blockIdx.y * R; b0 < p.B; b0 += gridDim.y * R) {
-        float4 h[R];
-        float x[R], dt[R], z[R], bv[R][4], cv[R][4];
+        float h[R][4], bv[R][4], cv[R][4], x[K], dt[K], z[K], d[K], dx[K];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const long long b = min(b0 + r, p.B - 1);
-            h[r] = *(reinterpret_cast<const float4*>(p.h0 + (b * p.D + cc) * p.N) + j);
-            x[r] = load_elem((const T*)p.x.p + b * p.x.b, cc);
-            dt[r] = load_elem((const T*)p.dt.p + b * p.dt.b, cc);
-            z[r] = p.gate.p ? load_elem((const T*)p.gate.p + b * p.gate.b, cc) : 0.f;
-            load4((const T*)p.bm.p + b * p.bm.b + g * p.N + 4 * j, bv[r]);
-            load4((const T*)p.cm.p + b * p.cm.b + g * p.N + 4 * j, cv[r]);
+            *reinterpret_cast<float4*>(h[r]) = *reinterpret_cast<const float4*>(p.h0 + (b * p.D + cc) * N + 4 * j);
+            load4(bm + b * p.bm.b, bv[r]);
+            load4(cm + b * p.cm.b, cv[r]);
         }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const long long b = min(b0 + k * M + own, p.B - 1);
+            x[k] = load_elem((const T*)p.x.p + b * p.x.b, cc);
+            dt[k] = load_elem((const T*)p.dt.p + b * p.dt.b, cc);
+            z[k] = p.gate.p ? load_elem((const T*)p.gate.p + b * p.gate.b, cc) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float v = dt[k] + bias;
+            d[k] = p.softplus ? softplus<T>(v) : v;
+            dx[k] = d[k] * x[k];
+            if (p.gate.p) z[k] *= sigmoid<T>(z[k]);
+        }
+        float y[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float v = dt[r] + bias, delta = p.softplus ? softplus<T>(v) : v, in = delta * x[r];
-            float s[4] = {h[r].x, h[r].y, h[r].z, h[r].w}, y = 0.f;
+            const float delta = __shfl_sync(0xffffffffu, d[r / M], base + r % M);
+            const float in = __shfl_sync(0xffffffffu, dx[r / M], base + r % M);
+            y[r] = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[i] = fmaf(exp2_fast(delta * A[i]), s[i], in * bv[r][i]);
-                y = fmaf(cv[r][i], s[i], y);
+                h[r][i] = fmaf(exp2_fast(delta * A[i]), h[r][i], in * bv[r][i]);
+                y[r] = fmaf(cv[r][i], h[r][i], y[r]);
             }
-            for (int gap = lanes / 2; gap > 0; gap /= 2) y += __shfl_xor_sync(0xffffffffu, y, gap);
-            y = fmaf(skip, x[r], y);
-            if (p.gate.p) y *= z[r] * sigmoid<T>(z[r]);
-            const long long b = b0 + r;
-            if (on && b < p.B) {
-                *(reinterpret_cast<float4*>(p.h_out + (b * p.D + cc) * p.N) + j) = make_float4(s[0], s[1], s[2], s[3]);
-                if (j == 0) store_elem((T*)p.y.p, b * p.D + cc, y);
-            }
+            if (on && b0 + r < p.B)
+                *reinterpret_cast<float4*>(p.h_out + ((long long)(b0 + r) * p.D + cc) * N + 4 * j) =
+                    *reinterpret_cast<float4*>(h[r]);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float v[M];
+#pragma unroll
+            for (int i = 0; i < M; ++i) v[i] = y[k * M + i];
+            float u = share_sums<M>(v, own, 1);
+#pragma unroll
+            for (int gap = M; gap < L; gap *= 2) u += __shfl_xor_sync(0xffffffffu, u, gap);
+            u = fmaf(skip, x[k], u);
+            if (p.gate.p) u *= z[k];
+            const int b = b0 + k * M + own;
+            if (on && j < M && b < p.B) store_elem((T*)p.y.p, (long long)b * p.D + c, u);
         }
     }
+}
+
+template <typename T>
+cudaError_t launch_step(const SsmParams& p, dim3 grid, cudaStream_t s) {
+    switch (p.N) {
+        case 8: ssm_step_kernel<T, 8><<<grid, 128, 0, s>>>(p); break;
+        case 16: ssm_step_kernel<T, 16><<<grid, 128, 0, s>>>(p); break;
+        case 32: ssm_step_kernel<T, 32><<<grid, 128, 0, s>>>(p); break;
+        default: ssm_step_kernel<T, 64><<<grid, 128, 0, s>>>(p); break;
+    }
+    return cudaGetLastError();
 }
 
 // ---- plans -----------------------------------------------------------------------------
@@ -375,9 +411,7 @@ cudaError_t launch_ssm_step(const SsmArgs& a, cudaStream_t s) {
     const long long rows = (a.B + 3) / 4, want = ((long long)sm_count() * 16 + blocks - 1) / blocks;
     const dim3 grid(blocks, (unsigned)std::max(1ll, std::min(rows, std::min(want, 65535ll))));
     TraceScope trace("ssm_step_kernel", s);
-    if (a.bf16) ssm::ssm_step_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(p);
-    else ssm::ssm_step_kernel<float><<<grid, 128, 0, s>>>(p);
-    return cudaGetLastError();
+    return a.bf16 ? ssm::launch_step<__nv_bfloat16>(p, grid, s) : ssm::launch_step<float>(p, grid, s);
 }
 
 }  // namespace la
