@@ -52,15 +52,24 @@ struct BlockParams {
 // 16 warps is zero from the start.
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* red, int& turn, int warps, int warp) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = group_sum<32>(v[i]);
-    if (warps == 1) return;
+    const int lane = threadIdx.x & 31;
     float* to = red + turn * 32;
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) to[i * 16 + warp] = v[i];
+    if (N == 1) {
+        v[0] = group_sum<32>(v[0]);
+        if (warps == 1) return;
+        if (lane == 0) to[warp] = v[0];
+    } else {  // the lower half of the warp takes the first value, the upper half the second
+        const bool hi = lane & 16;
+        const float keep = hi ? v[N - 1] : v[0], send = hi ? v[0] : v[N - 1];
+        const float sum = group_sum<16>(keep + __shfl_xor_sync(0xffffffffu, send, 16));
+        if (warps == 1) {
+            v[0] = __shfl_sync(0xffffffffu, sum, 0);
+            v[N - 1] = __shfl_sync(0xffffffffu, sum, 16);
+            return;
+        }
+        if ((lane & 15) == 0) to[lane + warp] = sum;
     }
+    turn ^= 1;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {

@@ -492,31 +492,50 @@ ConvParams params(const ShortConvArgs& a) {
     return p;
 }
 
-// Tiles of up to 32 vectors of V channels; runs of `most` tokens where that leaves
-// `waves` CTAs a place, shorter ones (down to 8) where it does not.
-void shape(ConvParams* p, int V, int most, int waves) {
+// Tiles of up to 32 vectors of V channels.
+void tile(ConvParams* p, int V) {
     const int vectors = p->D / V;
     p->lanes = 32;
     while (p->lanes / 2 >= vectors) p->lanes /= 2;
     p->tiles = (vectors + p->lanes - 1) / p->lanes;
-    const long long want = (long long)sm_count() * 4 * waves * (kThreads / p->lanes);  // runs, of all tiles
-    const long long tokens = (long long)p->B * p->T * p->tiles;
-    long long run = std::min<long long>(std::max<long long>(tokens / want / 8 * 8, 8), most);
+}
+
+void cut(ConvParams* p, long long run) {
     p->run = (int)run;
     p->runs_per_seq = (int)((p->T + run - 1) / run);
     p->runs = (long long)p->B * p->runs_per_seq;
-    p->run_blocks = (p->runs + kThreads / p->lanes - 1) / (kThreads / p->lanes);
+    const int depth = kThreads / p->lanes;  // runs of a CTA
+    p->run_blocks = (p->runs + depth - 1) / depth;
 }
 
-constexpr int kFwdRun = 64, kBwdRun = 64, kBwdBlocksPerSm = 4, kStepBlocksPerSm = 4;
+constexpr int kRun = 64, kCtasPerSm = 4;
 
-ConvParams bwd_params(const ShortConvArgs& a) {
+// Forward: runs of kRun tokens where that leaves every SM four times the CTAs it holds,
+// shorter ones (down to 8) where it does not.
+ConvParams fwd_params(const ShortConvArgs& a) {
     ConvParams p = params(a);
-    shape(&p, 4, kBwdRun, 1);
-    const long long most = ((long long)sm_count() * kBwdBlocksPerSm + p.tiles - 1) / p.tiles;
-    p.run_blocks = std::min(p.run_blocks, most);
+    tile(&p, a.bf16 ? 8 : 4);
+    const long long want = (long long)sm_count() * kCtasPerSm * 4 * (kThreads / p.lanes);  // runs, of all tiles
+    const long long tokens = (long long)p.B * p.T * p.tiles;
+    cut(&p, std::min<long long>(std::max<long long>(tokens / want / 8 * 8, 8), kRun));
     return p;
 }
+
+// Backward: the CTAs that fit at once, each as many runs of about kRun tokens as the others
+// (4 x 4093 tokens of 4096 channels: 304 runs of 54 for 304 places; 256 of 64 took a sixth longer).
+ConvParams bwd_params(const ShortConvArgs& a) {
+    ConvParams p = params(a);
+    tile(&p, 4);
+    const long long blocks = ((long long)sm_count() * kCtasPerSm + p.tiles - 1) / p.tiles;
+    const long long places = blocks * (kThreads / p.lanes), tokens = (long long)p.B * p.T;
+    const long long turns = std::max<long long>(1, (tokens + places * kRun / 2) / (places * kRun));
+    const long long per_seq = std::max<long long>(1, places * turns / p.B);
+    cut(&p, std::max<long long>(8, (p.T + per_seq - 1) / per_seq));
+    p.run_blocks = std::min(p.run_blocks, blocks);
+    return p;
+}
+
+constexpr int kStepBlocksPerSm = 4;
 
 template <typename F>
 cudaError_t by_width(int W, const F& f) {
@@ -535,8 +554,7 @@ size_t short_conv_bwd_workspace_bytes(const ShortConvArgs& a) {
 }
 
 cudaError_t launch_short_conv_fwd(const ShortConvArgs& a, cudaStream_t s) {
-    ConvParams p = params(a);
-    shape(&p, a.bf16 ? 8 : 4, kFwdRun, 4);
+    const ConvParams p = fwd_params(a);
     const dim3 grid((unsigned)(p.run_blocks * p.tiles));
     TraceScope trace("short_conv_kernel", s);
     return by_width(a.W, [&](auto w) {
