@@ -10,42 +10,49 @@ namespace la {
 
 namespace {
 
-constexpr int kSumWarps = 32;
+constexpr int kSumWarps = 32, kQuadColumns = 32768;
 
 struct Sums {
     PartialSum of[kPartialSums];
 };
 
-// One CTA per 32 columns; warp w adds rows w, w + 32, ... of its lane's column.
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float4 plus(float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+// One CTA per 32 columns (or 32 quads of them: V a float4, the same sums in the same order);
+// warp w adds rows w, w + 32, ... of its lane's column.
+template <typename V, int kBatch>
 __global__ void __launch_bounds__(kSumWarps * 32) partial_sum_kernel(const __grid_constant__ Sums s) {
-    __shared__ float red[kSumWarps][32];
+    __shared__ V red[kSumWarps][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, which = blockIdx.y;
     const int c = blockIdx.x * 32 + lane;
-    const float* part = s.of[which].part;
-    float* out = s.of[which].out;
-    const int rows = s.of[which].rows, cols = s.of[which].cols;
+    const V* part = reinterpret_cast<const V*>(s.of[which].part);
+    V* out = reinterpret_cast<V*>(s.of[which].out);
+    const int rows = s.of[which].rows, cols = s.of[which].cols / (int)(sizeof(V) / sizeof(float));
     if (!out || (int)blockIdx.x * 32 >= cols) return;
     tc::griddep_wait();  // the rows come from the previous kernel in the stream
-    float acc = 0.f;
+    V acc = {};
     if (c < cols) {
-        constexpr int kBatch = 24;  // loads in flight together
         for (int r0 = w; r0 < rows; r0 += kBatch * kSumWarps) {
-            float v[kBatch];
+            V v[kBatch];  // loads in flight together
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int r = r0 + i * kSumWarps;
-                v[i] = r < rows ? part[(size_t)r * cols + c] : 0.f;
+                v[i] = V{};
+                if (r < rows) v[i] = part[(size_t)r * cols + c];
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) acc += v[i];
+            for (int i = 0; i < kBatch; ++i) acc = plus(acc, v[i]);
         }
     }
     red[w][lane] = acc;
     __syncthreads();
     if (w == 0 && c < cols) {
-        float sum = 0.f;
+        V sum = {};
 #pragma unroll
-        for (int i = 0; i < kSumWarps; ++i) sum += red[i][lane];
+        for (int i = 0; i < kSumWarps; ++i) sum = plus(sum, red[i][lane]);
         out[c] = sum;
     }
 }
@@ -66,12 +73,15 @@ cudaError_t launch_partial_sums(const PartialSum* sums, int n, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((cols + 31) / 32, used);
+    // many columns: four a lane, a quarter of the CTAs
+    const bool quads = cols >= kQuadColumns;
+    cfg.gridDim = dim3(quads ? (cols / 4 + 31) / 32 : (cols + 31) / 32, used);
     cfg.blockDim = dim3(kSumWarps * 32);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, partial_sum_kernel, all);
+    return quads ? cudaLaunchKernelEx(&cfg, partial_sum_kernel<float4, 4>, all)
+                 : cudaLaunchKernelEx(&cfg, partial_sum_kernel<float, 24>, all);
 }
 
 cudaError_t launch_partial_sum(const float* part0, int rows0, float* out0, const float* part1, int rows1,

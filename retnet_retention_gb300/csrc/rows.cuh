@@ -196,6 +196,20 @@ __device__ __forceinline__ float sigmoid(float g) {
     return s;
 }
 
+// sigma of both halves, as sigmoid<T>.
+template <typename T>
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+    if (sizeof(T) == 4) return make_float2(sigmoid<T>(v.x), sigmoid<T>(v.y));
+    const float2 s = __fmul2_rn(v, both(-1.4426950408889634f));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(s.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(s.y));
+    e = __fadd2_rn(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+    return e;
+}
+
 // m / T by a multiplication, exact for m < 2^31.
 struct Divide {
     unsigned T, magic, shift;  // magic = ceil(2^shift / T), shift = 31 + ceil(log2 T)

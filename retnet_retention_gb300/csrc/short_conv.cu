@@ -134,20 +134,6 @@ __device__ __forceinline__ void convolve(const float2 (&w)[W][V / 2], const floa
     }
 }
 
-// sigma of both halves, as sigmoid<T>.
-template <typename T>
-__device__ __forceinline__ float2 sigmoid2(float2 v) {
-    if (sizeof(T) == 4) return make_float2(sigmoid<T>(v.x), sigmoid<T>(v.y));
-    const float2 s = __fmul2_rn(v, both(-1.4426950408889634f));
-    float2 e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(s.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(s.y));
-    e = __fadd2_rn(e, both(1.f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
-    return e;
-}
-
 // Tokens of the unrolled loop, a multiple of the W - 1 rows kept (a long loop does not stay in
 // the instruction cache: nine tokens of the gradients took 119 us where three take 100), and
 // rows of the ring, a multiple of those.

@@ -32,64 +32,73 @@ constexpr int kJoinWarps = 32;
 // The state after a run of decay P (0: dropped) from s.
 __device__ __forceinline__ float after(float P, float b, float s) { return P == 0.f ? b : fmaf(P, s, b); }
 
+struct Run4 {
+    float4 P, b;
+};
+
 // v[b][chunk][D][N]: what a chunk adds becomes what enters it, in place; from the first
-// chunk with s0 before it, or from the last with s0 behind it.  A CTA per 32 columns of [D][N] of
-// a sequence; each warp puts a run of chunks together, then walks them again.
+// chunk with s0 before it, or from the last with s0 behind it.  A CTA per 128 columns of [D][N] of
+// a sequence, four a lane (of one channel); each warp puts a run of chunks together, then walks
+// them again.  Chunks come in batches whose loads are in flight together (a store in between
+// would hold the next one's back).
 __global__ void __launch_bounds__(kJoinWarps * 32) ssm_join_kernel(
     float* forward, const float* forward_s0, float* backward, const float* backward_s0, const float* chunk_s,
     const float* __restrict__ A, int D, int N, int chunks) {
-    __shared__ float2 runs[kJoinWarps][32];
+    __shared__ Run4 runs[kJoinWarps][32];
     const bool back = forward == nullptr || blockIdx.z == 1;
-    float* v = back ? backward : forward;
-    const float* s0 = back ? backward_s0 : forward_s0;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const long long col = (long long)blockIdx.x * 32 + lane, cols = (long long)D * N, b = blockIdx.y;
-    const int d = (int)(col / N);
-    const float a = A[col] * kLog2e;
+    const long long quad = (long long)blockIdx.x * 32 + lane, quads = (long long)D * N / 4, b = blockIdx.y;
+    float4* const v = reinterpret_cast<float4*>(back ? backward : forward);
+    const float4* const s0 = reinterpret_cast<const float4*>(back ? backward_s0 : forward_s0);
+    const int d = (int)(quad * 4 / N);
+    const float4 a = __ldg(reinterpret_cast<const float4*>(A) + quad);
     const int each = (chunks + warps - 1) / warps;
     const int k0 = min(w * each, chunks), k1 = min(k0 + each, chunks);
     auto at = [&](int k) { return b * chunks + (back ? chunks - 1 - k : k); };
-    auto decay = [&](long long i) {
-        const float s = chunk_s[i * D + d];
-        return s == INFINITY ? 0.f : exp2_fast(s * a);
-    };
-    // batches of kBatch chunks, their loads in flight together (a store in between would hold
-    // the next one's back)
     constexpr int kBatch = 8;
-    float e[kBatch], add[kBatch];
+    float sum[kBatch];
+    float4 add[kBatch];
     auto load = [&](int k) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            e[i] = 1.f, add[i] = 0.f;
+            sum[i] = 0.f, add[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (k + i < k1) {
-                e[i] = decay(at(k + i));
-                add[i] = v[at(k + i) * cols + col];
+                sum[i] = chunk_s[at(k + i) * D + d] * kLog2e;
+                add[i] = v[at(k + i) * quads + quad];
             }
         }
     };
+    auto decay = [&](float s) {  // of a chunk: 0 where a document starts in it
+        if (s == INFINITY) return make_float4(0.f, 0.f, 0.f, 0.f);
+        return make_float4(exp2_fast(s * a.x), exp2_fast(s * a.y), exp2_fast(s * a.z), exp2_fast(s * a.w));
+    };
+    auto step = [&](const float4& e, const float4& b4, const float4& s) {
+        return make_float4(after(e.x, b4.x, s.x), after(e.y, b4.y, s.y), after(e.z, b4.z, s.z), after(e.w, b4.w, s.w));
+    };
     load(k0);
-    float s = s0 ? s0[b * cols + col] : 0.f;
+    float4 s = s0 ? s0[b * quads + quad] : make_float4(0.f, 0.f, 0.f, 0.f);
     if (warps > 1) {
-        float P = 1.f, sum = 0.f;
+        Run4 run = {make_float4(1.f, 1.f, 1.f, 1.f), make_float4(0.f, 0.f, 0.f, 0.f)};
         for (int k = k0; k < k1; k += kBatch) {
             if (k > k0) load(k);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                sum = after(e[i], add[i], sum);
-                P *= e[i];
+                const float4 e = decay(sum[i]);
+                run.b = step(e, add[i], run.b);
+                run.P.x *= e.x; run.P.y *= e.y; run.P.z *= e.z; run.P.w *= e.w;
             }
         }
-        runs[w][lane] = make_float2(P, sum);
+        runs[w][lane] = run;
         __syncthreads();
-        for (int k = 0; k < w; ++k) s = after(runs[k][lane].x, runs[k][lane].y, s);
+        for (int k = 0; k < w; ++k) s = step(runs[k][lane].P, runs[k][lane].b, s);
     }
     for (int k = k0; k < k1; k += kBatch) {
         if (k > k0 || k1 - k0 > kBatch) load(k);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
             if (k + i < k1) {
-                v[at(k + i) * cols + col] = s;
-                s = after(e[i], add[i], s);
+                v[at(k + i) * quads + quad] = s;
+                s = step(decay(sum[i]), add[i], s);
             }
     }
 }
@@ -106,9 +115,16 @@ __global__ void __launch_bounds__(256) ssm_shared_grad_kernel(const float* part,
     const long long m = i / quads, b = m / T_, t = m - b * T_;
     const int col = (int)(i % quads) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < tiles; ++k) {
-        const float4 r = *reinterpret_cast<const float4*>(part + (((long long)g * tiles + k) * tokens + m) * (2 * N) + col);
-        v.x += r.x; v.y += r.y; v.z += r.z; v.w += r.w;
+    const float* const from = part + ((long long)g * tiles * tokens + m) * (2 * N) + col;
+    for (int k0 = 0; k0 < tiles; k0 += 8) {
+        float4 r[8];  // loads in flight together
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            r[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + k < tiles) r[k] = __ldcs(reinterpret_cast<const float4*>(from + (k0 + k) * tokens * (2 * N)));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v.x += r[k].x, v.y += r[k].y, v.z += r[k].z, v.w += r[k].w;
     }
     const SsmRows& to = col >= N ? dc : db;
     T* out = (T*)to.p + b * to.b + t * to.t + g * N + col % N;
@@ -264,7 +280,7 @@ Plan forward_plan(const SsmArgs& a) {
     auto warps = [&](Split s) { return (long long)a.B * a.G * ((a.D / a.G + s.cta() - 1) / s.cta()) * kWarps; };
     const long long w = warps(split);
     long long chunks = 1;
-    if (2 * w < 5 * sms && a.T >= 128) chunks = std::min<long long>(a.T / 32, (24 * sms + w - 1) / w);
+    if (2 * w < 5 * sms && a.T >= 128) chunks = std::min<long long>(a.T / 32, (16 * sms + w - 1) / w);
     if (a.N < 64 && w * chunks <= 2 * sms) split = {a.N / 4, 1};
     return plan_of(a, split, split.cta(), chunks);
 }
@@ -320,7 +336,7 @@ size_t backward_workspace(const SsmArgs& a, const Plan& plan, SsmBwdParams* bp) 
 
 cudaError_t join(const SsmParams& p, bool forward, bool backward, const float* dh_T, cudaStream_t s) {
     const int warps = std::min(kJoinWarps, (p.chunks + 7) / 8);
-    const dim3 grid((unsigned)((long long)p.D * p.N / 32), p.B, forward && backward ? 2 : 1);
+    const dim3 grid((unsigned)((long long)p.D * p.N / 128), p.B, forward && backward ? 2 : 1);
     TraceScope trace("ssm_join_kernel", s);
     ssm_join_kernel<<<grid, warps * 32, 0, s>>>(forward ? p.chunk_h : nullptr, p.h0, p.chunk_g, dh_T, p.chunk_s, p.A,
                                                 p.D, p.N, p.chunks);

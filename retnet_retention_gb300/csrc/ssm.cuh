@@ -51,6 +51,7 @@ namespace ssm {
 
 constexpr int kBlock = 8;    // tokens a lane group works on at once
 constexpr int kTile = 16;    // tokens whose rows lie in shared memory
+constexpr int kUnroll = 8;   // tokens of the walk's unrolled loop
 constexpr int kWarps = 4;
 
 // 2^v, 2 ulp; 0 below the fp32 range.
@@ -65,17 +66,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // log(1 + p) for p in [0, 1], 1.7e-7 relative (p = 0 included): p times a polynomial of
 // degree 8 fitted to log(1 + p) / p in the relative maximum norm.  No logarithm, so that
 // small steps keep all their digits.
-__device__ __forceinline__ float log1p_unit(float p) {
-    float q = 0.00523269409f;
-    q = fmaf(q, p, -0.0295052379f);
-    q = fmaf(q, p, 0.0782259554f);
-    q = fmaf(q, p, -0.136632457f);
-    q = fmaf(q, p, 0.191060066f);
-    q = fmaf(q, p, -0.24842982f);
-    q = fmaf(q, p, 0.333190978f);
-    q = fmaf(q, p, -0.499994934f);
-    q = fmaf(q, p, 0.99999994f);
-    return q * p;
+__device__ __forceinline__ float log1p_coefficient(int i) {
+    constexpr float k[9] = {0.00523269409f, -0.0295052379f, 0.0782259554f, -0.136632457f, 0.191060066f,
+                            -0.24842982f, 0.333190978f, -0.499994934f, 0.99999994f};
+    return k[i];
 }
 
 // softplus(v) = max(v, 0) + log(1 + e^-|v|), and its slope 1 / (1 + e^-v) where asked for; the
@@ -88,7 +82,34 @@ __device__ __forceinline__ float softplus(float v, float* slope = nullptr) {
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + p));  // 1 ulp
         *slope = v >= 0.f ? r : p * r;
     }
-    return fmaxf(v, 0.f) + log1p_unit(p);
+    float q = log1p_coefficient(0);
+#pragma unroll
+    for (int i = 1; i < 9; ++i) q = fmaf(q, p, log1p_coefficient(i));
+    return fmaf(q, p, fmaxf(v, 0.f));
+}
+
+// The same of two values, packed.
+template <typename T>
+__device__ __forceinline__ float2 softplus2(float2 v, float2* slope = nullptr) {
+    float2 p;
+    if (sizeof(T) == 2) {
+        const float2 s = __fmul2_rn(make_float2(fabsf(v.x), fabsf(v.y)), both(-kLog2e));
+        p = make_float2(exp2_fast(s.x), exp2_fast(s.y));
+    } else {
+        p = make_float2(expf(-fabsf(v.x)), expf(-fabsf(v.y)));
+    }
+    if (slope) {
+        const float2 one = __fadd2_rn(p, both(1.f));
+        float2 r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(one.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(one.y));
+        const float2 pr = __fmul2_rn(p, r);
+        *slope = make_float2(v.x >= 0.f ? r.x : pr.x, v.y >= 0.f ? r.y : pr.y);
+    }
+    float2 q = both(log1p_coefficient(0));
+#pragma unroll
+    for (int i = 1; i < 9; ++i) q = __ffma2_rn(q, p, both(log1p_coefficient(i)));
+    return __ffma2_rn(q, p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 
 // v[0 .. L-1] of the L lanes that lie `gap` apart, lane j keeps the sum of v[j].
@@ -149,7 +170,7 @@ struct Shape {
     using Elem = T;
     static constexpr int CH = CH_, NS = NS_, L = L_, N = NS * L, CL = 32 / L, WC = CH * CL;
     static constexpr Mode MODE = MODE_;
-    static constexpr int M = L / CH, K = kBlock / M;  // a lane's own tokens: every M-th, K of a block
+    static constexpr int M = L / CH, U = M < kUnroll ? kUnroll : M, K = U / M;  // a lane's own tokens: every M-th, K of U
     // the tile's rows of x, dt, gate and dy of a warp's channels in shared memory, in pieces
     static constexpr int kTensors = MODE == kState ? 2 : MODE == kForward ? 3 : 4;
     static constexpr int kPiece = WC * (int)sizeof(T) < 16 ? WC * (int)sizeof(T) : 16, kElems = kPiece / (int)sizeof(T);
@@ -187,9 +208,9 @@ __device__ __forceinline__ void copy_piece(void* to, const void* from, bool vali
 // tokens are every M-th.  Tiles in which a document starts or the chunk ends, and for the summary those
 // behind a start, take the careful form of the loop.
 template <typename S>
-__global__ void __launch_bounds__(kWarps * 32) ssm_scan_kernel(const __grid_constant__ SsmParams p) {
+__global__ void __launch_bounds__(kWarps * 32, S::MODE == kState ? 4 : 3) ssm_scan_kernel(const __grid_constant__ SsmParams p) {
     using T = typename S::Elem;
-    constexpr int CH = S::CH, NS = S::NS, N = S::N, CL = S::CL, WC = S::WC, U = kBlock, M = S::M, K = S::K;
+    constexpr int CH = S::CH, NS = S::NS, N = S::N, CL = S::CL, WC = S::WC, U = S::U, M = S::M, K = S::K;
     constexpr bool kY = S::MODE == kForward, kBack = S::MODE == kSummary, kGate = S::MODE != kState;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, j = lane / CL, cl = lane % CL;
@@ -234,37 +255,52 @@ __global__ void __launch_bounds__(kWarps * 32) ssm_scan_kernel(const __grid_cons
 
     T* const stages = reinterpret_cast<T*>(smem + (size_t)w * S::kWarpShared);
     constexpr int kRows = S::kRows;
+    // A lane's piece of a tile's first rows, in each tensor: its place from the tile's start in global
+    // memory and in shared memory.  A tile that is all there needs no more than its start.
+    constexpr int kPerRow = WC / S::kElems, kPass = 32 / kPerRow;       // pieces of a row, rows a pass
+    constexpr int kSharedPerRow = 2 * N * (int)sizeof(T) / 16, kSharedPass = 32 / kSharedPerRow;
+    const int row = lane / kPerRow, at = lane % kPerRow * S::kElems;
+    const long long col = g * p.channels + first + at;
+    const long long x_off = row * p.x.t + col, dt_off = row * p.dt.t + col;
+    const long long gate_off = gated ? row * p.gate.t + col : 0, dy_off = kBack ? row * p.dy.t + col : 0;
+    const int shared_row = lane / kSharedPerRow, shared_part = lane % kSharedPerRow;
+    const bool of_c = shared_part >= kSharedPerRow / 2;
+    const SsmRows& shared_rows = of_c ? p.cm : p.bm;
+    const T* const shared_from = (const T*)shared_rows.p + b * shared_rows.b + shared_row * shared_rows.t + g * N +
+                                 shared_part % (kSharedPerRow / 2) * (16 / (int)sizeof(T));
+    const long long shared_t = shared_rows.t;
+    const bool whole_channels = first + WC <= p.channels;
+    const long long y_off = kY ? row * p.y.t + col : 0;
     auto copy_tile = [&](int buf, int t) {
         T* const stage = stages + buf * S::kStage;
+        auto copy_rows = [&](auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
-        for (int i = 0; i < S::kEach; ++i) {
-            const int q = i * 32 + lane, row = q / (WC / S::kElems), at = q % (WC / S::kElems) * S::kElems;
-            if (S::kPieces % 32 == 0 || q < S::kPieces) {
-                const bool valid = t + row < t1 && first + at < p.channels;
-                const long long token = valid ? t + row : 0;
-                const int col = valid ? g * p.channels + first + at : 0;
-                auto copy = [&](int k, const SsmRows& r) {
-                    copy_piece<S::kPiece>(stage + k * kRows + row * WC + at,
-                                          (const T*)r.p + b * r.b + token * r.t + col, valid);
-                };
-                copy(0, p.x);
-                copy(1, p.dt);
-                if (gated) copy(2, p.gate);
-                if (kBack) copy(3, p.dy);
+            for (int i = 0; i < S::kEach; ++i) {
+                if (S::kPieces >= 32 || lane < S::kPieces) {
+                    const bool valid = kWhole || (t + i * kPass + row < t1 && first + at < p.channels);
+                    auto copy = [&](int k, const SsmRows& r, long long off) {
+                        const T* const from = (const T*)r.p + b * r.b + (t + i * kPass) * r.t;
+                        copy_piece<S::kPiece>(stage + k * kRows + (i * kPass + row) * WC + at, valid ? from + off : (const T*)r.p,
+                                              valid);
+                    };
+                    copy(0, p.x, x_off);
+                    copy(1, p.dt, dt_off);
+                    if (gated) copy(2, p.gate, gate_off);
+                    if (kBack) copy(3, p.dy, dy_off);
+                }
             }
-        }
-        constexpr int kRowPieces = N * (int)sizeof(T) / 16;  // of b's row, and of c's
 #pragma unroll
-        for (int i = 0; i < (S::kSharedPieces + 31) / 32; ++i) {
-            const int q = i * 32 + lane, row = q / (2 * kRowPieces), part = q % (2 * kRowPieces);
-            if (S::kSharedPieces % 32 == 0 || q < S::kSharedPieces) {
-                const SsmRows& r = part < kRowPieces ? p.bm : p.cm;
-                const bool valid = t + row < t1;
-                copy16(stage + S::kTensors * kRows + q * (16 / (int)sizeof(T)),
-                       (const T*)r.p + b * r.b + (valid ? t + row : 0) * r.t + g * N +
-                           part % kRowPieces * (16 / (int)sizeof(T)), valid);
+            for (int i = 0; i < (S::kSharedPieces + 31) / 32; ++i) {
+                if (S::kSharedPieces >= 32 || lane < S::kSharedPieces) {
+                    const bool valid = kWhole || t + i * kSharedPass + shared_row < t1;
+                    copy16(stage + S::kTensors * kRows + (i * 32 + lane) * (16 / (int)sizeof(T)),
+                           valid ? shared_from + (t + i * kSharedPass) * shared_t : (const T*)shared_rows.p, valid);
+                }
             }
-        }
+        };
+        if (whole_channels && t + kTile <= t1) copy_rows(std::true_type());
+        else copy_rows(std::false_type());
         copies_commit();
     };
     int position = 1;  // of the lane's token of the next tile
@@ -308,8 +344,8 @@ __global__ void __launch_bounds__(kWarps * 32) ssm_scan_kernel(const __grid_cons
             for (int q0 = 0; q0 < kTile; q0 += U) {
                 const int t = tt + q0;
                 if (kCareful && t >= t1) break;
-                if (kBack && t > t0) {  // the local state before this block of the chunk
-                    const long long block = b * p.blocks + t / U;
+                if (kBack && t > t0 && t % kBlock == 0) {  // the local state before this block of the chunk
+                    const long long block = b * p.blocks + t / kBlock;
 #pragma unroll
                     for (int q = 0; q < CH; ++q)
                         if (on[q]) {
@@ -321,21 +357,31 @@ __global__ void __launch_bounds__(kWarps * 32) ssm_scan_kernel(const __grid_cons
                             if (j == 0) p.block_s[at] = cut ? INFINITY : sum[q];
                         }
                 }
-                T* const at = own_at + q0 * WC;
-                float xs[K], d[K], dx[K], du[K];
+                T* const own_rows = own_at + q0 * WC;
+                // two own tokens at a time (one, where it is the only one)
+                constexpr int kPairs = (K + 1) / 2;
+                float2 xs[kPairs], d[kPairs], dx[kPairs], du[kPairs];
+                auto own_pair = [&](int tensor, int k) {
+                    return make_float2(load_elem(own_rows + tensor * kRows, 2 * k * M * WC),
+                                       K == 1 ? 0.f : load_elem(own_rows + tensor * kRows, (2 * k + 1) * M * WC));
+                };
+                auto silu = [&](int k) {
+                    const float2 z = own_pair(2, k);
+                    return __fmul2_rn(z, K == 1 ? make_float2(sigmoid<T>(z.x), 0.f) : sigmoid2<T>(z));
+                };
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    xs[k] = load_elem(at, k * M * WC);
-                    const float v = load_elem(at + kRows, k * M * WC) + bias;
-                    d[k] = p.softplus ? softplus<T>(v) : v;
-                    if (kCareful && t + k * M + own >= t1) d[k] = 0.f;
-                    dx[k] = d[k] * xs[k];
+                for (int k = 0; k < kPairs; ++k) {
+                    xs[k] = own_pair(0, k);
+                    const float2 v = __fadd2_rn(own_pair(1, k), both(bias));
+                    d[k] = !p.softplus ? v : K == 1 ? make_float2(softplus<T>(v.x), 0.f) : softplus2<T>(v);
+                    if (kCareful) {
+                        if (t + 2 * k * M + own >= t1) d[k].x = 0.f;
+                        if (t + (2 * k + 1) * M + own >= t1) d[k].y = 0.f;
+                    }
+                    dx[k] = __fmul2_rn(d[k], xs[k]);
                     if (kBack) {
-                        du[k] = load_elem(at + 3 * kRows, k * M * WC);
-                        if (gated) {
-                            const float z = load_elem(at + 2 * kRows, k * M * WC);
-                            du[k] *= z * sigmoid<T>(z);
-                        }
+                        du[k] = own_pair(3, k);
+                        if (gated) du[k] = __fmul2_rn(du[k], silu(k));
                     }
                 }
                 const unsigned block_starts = kCareful ? tile_starts >> q0 & ((1u << U) - 1) : 0;
@@ -357,8 +403,9 @@ __global__ void __launch_bounds__(kWarps * 32) ssm_scan_kernel(const __grid_cons
                     for (int q = 0; q < CH; ++q) {
                         // from the lane whose own token and channel it is
                         const int from = (u % M * CH + (CH == 1 ? 0 : q ^ (j & 1))) * CL + cl;
-                        auto get = [&](const float(&v)[K]) {
-                            return M == 1 && q == 0 ? v[u / M] : __shfl_sync(0xffffffffu, v[u / M], from);
+                        auto get = [&](const float2(&v)[kPairs]) {
+                            const float f = u / M % 2 ? v[u / M / 2].y : v[u / M / 2].x;
+                            return M == 1 && q == 0 ? f : __shfl_sync(0xffffffffu, f, from);
                         };
                         const float delta = get(d), in = get(dx), dut = kBack ? get(du) : 0.f;
                         float2 part = make_float2(0.f, 0.f);
@@ -391,17 +438,19 @@ __global__ void __launch_bounds__(kWarps * 32) ssm_scan_kernel(const __grid_cons
                     if (kY) acc[u] = CH == 1 ? a[0] : a[0] + __shfl_xor_sync(0xffffffffu, a[CH - 1], CL);
                 }
                 if (kY) {
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
+                    auto total = [&](int k) {
                         float v[M];
 #pragma unroll
                         for (int i = 0; i < M; ++i) v[i] = acc[k * M + i];
-                        float u = fmaf(skip, xs[k], share_sums<M>(v, own, CH * CL));
-                        if (gated) {
-                            const float z = load_elem(at + 2 * kRows, k * M * WC);
-                            u *= z * sigmoid<T>(z);
-                        }
-                        store_elem(at, k * M * WC, u);  // in x's place
+                        return share_sums<M>(v, own, CH * CL);
+                    };
+#pragma unroll
+                    for (int k = 0; k < kPairs; ++k) {
+                        float2 u = make_float2(total(2 * k), K == 1 ? 0.f : total(K == 1 ? 0 : 2 * k + 1));
+                        u = __ffma2_rn(both(skip), xs[k], u);
+                        if (gated) u = __fmul2_rn(u, silu(k));
+                        store_elem(own_rows, 2 * k * M * WC, u.x);  // in x's place
+                        if (K > 1) store_elem(own_rows, (2 * k + 1) * M * WC, u.y);
                     }
                 }
             }
@@ -410,16 +459,21 @@ __global__ void __launch_bounds__(kWarps * 32) ssm_scan_kernel(const __grid_cons
         else walk(std::true_type());
         if (kY) {
             __syncwarp();
+            auto put_rows = [&](auto whole) {
+                constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
-            for (int i = 0; i < S::kEach; ++i) {
-                const int q = i * 32 + lane, row = q / (WC / S::kElems), at = q % (WC / S::kElems) * S::kElems;
-                if ((S::kPieces % 32 == 0 || q < S::kPieces) && tt + row < t1 && first + at < p.channels) {
-                    const T* from = stage + row * WC + at;
-                    T* to = (T*)p.y.p + b * p.y.b + (tt + row) * p.y.t + g * p.channels + first + at;
-                    if constexpr (S::kPiece == 16) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
-                    else *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
+                for (int i = 0; i < S::kEach; ++i) {
+                    const bool valid = kWhole || (tt + i * kPass + row < t1 && first + at < p.channels);
+                    if ((S::kPieces >= 32 || lane < S::kPieces) && valid) {
+                        const T* const from = stage + (i * kPass + row) * WC + at;
+                        T* const to = (T*)p.y.p + b * p.y.b + (tt + i * kPass) * p.y.t + y_off;
+                        if constexpr (S::kPiece == 16) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+                        else *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
+                    }
                 }
-            }
+            };
+            if (whole_channels && tt + kTile <= t1) put_rows(std::true_type());
+            else put_rows(std::false_type());
         }
         __syncwarp();
     }

@@ -192,24 +192,36 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) ssm_gradients_kernel(const 
         __syncwarp();
         unsigned char* const stage = mine + buf * S::kStage;
         // the block's own elementwise values
+        constexpr int kPairs = (K + 1) / 2;  // two own tokens at a time (one, where it is the only one)
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int row = (k * M + own) * WC;
-            const T* const from = (const T*)stage + row + mine_c;
-            const float x = load_elem(from, 0), v = load_elem(from, S::kRows) + bias;
-            float d = v, du = load_elem(from, 3 * S::kRows);
-            float2 slope = make_float2(1.f, 0.f);
-            if (p.softplus) d = softplus<T>(v, &slope.x);
-            if (t + k * M + own >= t1) d = 0.f;  // no token: the state stays as it is (x, dy and so on are zeros)
+        for (int k = 0; k < kPairs; ++k) {
+            const int row = (2 * k * M + own) * WC, row2 = K == 1 ? row : row + M * WC;
+            const T* const from = (const T*)stage + mine_c;
+            auto pair = [&](int tensor) {
+                return make_float2(load_elem(from + tensor * S::kRows, row), load_elem(from + tensor * S::kRows, row2));
+            };
+            const float2 x = pair(0), v = __fadd2_rn(pair(1), both(bias));
+            float2 d = v, du = pair(3), slope = both(1.f), gate_slope = both(0.f);
+            if (p.softplus) d = softplus2<T>(v, &slope);
+            // no token: the state stays as it is (x, dy and so on are zeros)
+            if (t + 2 * k * M + own >= t1) d.x = 0.f;
+            if (t + (2 * k + 1) * M + own >= t1) d.y = 0.f;
             if (gated) {
-                const float z = load_elem(from, 2 * S::kRows), s = sigmoid<T>(z), a = z * s;
-                slope.y = du * fmaf(a, 1.f - s, s);
-                du *= a;
+                const float2 z = pair(2), s = sigmoid2<T>(z), a = __fmul2_rn(z, s);
+                gate_slope = __fmul2_rn(du, __ffma2_rn(a, __ffma2_rn(s, both(-1.f), both(1.f)), s));
+                du = __fmul2_rn(du, a);
             }
-            steps[row + mine_at] = make_float2(d, d * x);
-            slopes[row + mine_at] = slope;
-            dus[row + mine_at] = du;
-            xs[row + mine_at] = x;
+            const float2 dx = __fmul2_rn(d, x);
+            steps[row + mine_at] = make_float2(d.x, dx.x);
+            slopes[row + mine_at] = make_float2(slope.x, gate_slope.x);
+            dus[row + mine_at] = du.x;
+            xs[row + mine_at] = x.x;
+            if (K > 1) {
+                steps[row2 + mine_at] = make_float2(d.y, dx.y);
+                slopes[row2 + mine_at] = make_float2(slope.y, gate_slope.y);
+                dus[row2 + mine_at] = du.y;
+                xs[row2 + mine_at] = x.y;
+            }
         }
         // b and c to fp32, a copy for each turn: entry i of a group of four is entry i ^ turn
         float* const wide = wides + buf * S::kWide;

@@ -108,9 +108,9 @@ def test_block_reference_gradients(post, pre, center, each):
 def test_log1p_polynomial():
     """The kernel's coefficients, in fp32 with fused steps: 3 U of log(1 + p)."""
     src = open(os.path.join(os.path.dirname(la.__file__), "csrc", "ssm.cuh")).read()
-    body = src[src.index("log1p_unit(float p)"):]
-    body = body[:body.index("return q * p")]
-    c = [np.float32(m) for m in re.findall(r"(-?\d+\.\d+)f[;)]", body)]
+    body = src[src.index("k[9] = {"):]
+    body = body[:body.index("};")]
+    c = [np.float32(m) for m in re.findall(r"(-?\d+\.\d+)f", body)]
     assert len(c) == 9
     p = np.concatenate((np.linspace(0, 1, 100001), 2.0 ** -np.arange(1, 120.0))).astype(np.float32)
     q = np.full_like(p, c[0])
