@@ -1086,23 +1086,30 @@ def _ssm_shape(x, dt, A, b, c, skip, gate, dt_bias, dims: int):
                                        _dense(dt_bias, "dt_bias", (D,), f32, dev))
 
 
-def _row_strides(named, outer: int):
-    """The host array of the outer strides of tensors whose rows are dense (None: all are
-    wholly dense); named: (name, tensor) pairs, absent tensors get zeros."""
-    if all(t is None or t.is_contiguous() for _, t in named):
+def _row_strides(names, tensors, outer: int):
+    """The host array of the outer strides of tensors whose rows (one dimension, or groups
+    of entries) are dense; absent tensors get zeros.  None: all are wholly dense."""
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            break
+    else:
         return None
     strides = []
-    for name, t in named:
+    for name, t in zip(names, tensors):
         if t is None:
-            strides += [0] * outer
+            strides += (0,) * outer
             continue
-        width = 1
-        for size, step in zip(reversed(t.shape[outer:]), reversed(t.stride()[outer:])):
-            if size > 1 and step != width:
-                raise ValueError(f"{name}: the entries of a row must lie one after another")
-            width *= size
-        strides += t.stride()[:outer]
+        step = t.stride()
+        if step[-1] != 1 and t.shape[-1] > 1 or (
+                len(step) > outer + 1 and step[-2] != t.shape[-1] and t.shape[-2] > 1):
+            raise ValueError(f"{name}: the entries of a row must lie one after another")
+        strides += step[:outer]
     return (ctypes.c_longlong * len(strides))(*strides)
+
+
+@functools.lru_cache(maxsize=256)
+def _ssm_workspace(device: int, *shape) -> int:
+    return int(_load().la_ssm_workspace_size(*shape))
 
 
 def ssm_fwd(x, dt, A, b, c, *, skip=None, gate=None, dt_bias=None, softplus=True, h0=None, positions=None,
@@ -1127,8 +1134,8 @@ def ssm_fwd(x, dt, A, b, c, *, skip=None, gate=None, dt_bias=None, softplus=True
         last = None
         if return_state or h_out is not None:
             h_out, last = _output(h_out, "h_out", state, f32, dev)
-        strides = _row_strides((("x", x), ("dt", dt), ("b", b), ("c", c), ("gate", gate), ("out", out)), 2)
-        workspace, ws_bytes = _scratch(workspace, int(lib.la_ssm_workspace_size(B, T, D, N, G, code)), dev)
+        strides = _row_strides(("x", "dt", "b", "c", "gate", "out"), (x, dt, b, c, gate, out), 2)
+        workspace, ws_bytes = _scratch(workspace, _ssm_workspace(dev.index, B, T, D, N, G, code), dev)
         positions = _aligned(positions)
         a, k, bias = weights
         st = lib.la_ssm_fwd(x.data_ptr(), dt.data_ptr(), a, b.data_ptr(), c.data_ptr(), k,
@@ -1171,8 +1178,8 @@ def ssm_bwd(x, dt, A, b, c, dy, *, skip=None, gate=None, dt_bias=None, softplus=
         dskip = small(weight_grads and skip is not None, D)
         dbias = small(weight_grads and dt_bias is not None, D)
         dh0 = small(state_grads, *state)
-        strides = _row_strides((("x", x), ("dt", dt), ("b", b), ("c", c), ("gate", gate), ("dy", dy), ("dx", dx),
-                                ("ddt", ddt), ("db", db), ("dc", dc), ("dgate", dgate)), 2)
+        strides = _row_strides(("x", "dt", "b", "c", "gate", "dy", "dx", "ddt", "db", "dc", "dgate"),
+                               (x, dt, b, c, gate, dy, dx, ddt, db, dc, dgate), 2)
         workspace, ws_bytes = _scratch(workspace, int(lib.la_ssm_bwd_workspace_size(B, T, D, N, G, code)), dev)
         positions = _aligned(positions)
         a, k, bias = weights
@@ -1197,7 +1204,7 @@ def ssm_step(x, dt, A, b, c, h, *, skip=None, gate=None, dt_bias=None, softplus=
         out, y = _output(out, "out", (B, D), x.dtype, dev)
         old = _dense(h, "h", state, f32, dev)
         new = old if h_out is None else _dense(h_out, "h_out", state, f32, dev)
-        strides = _row_strides((("x", x), ("dt", dt), ("b", b), ("c", c), ("gate", gate)), 1)
+        strides = _row_strides(("x", "dt", "b", "c", "gate"), (x, dt, b, c, gate), 1)
         a, k, bias = weights
         st = _load().la_ssm_step(x.data_ptr(), dt.data_ptr(), a, b.data_ptr(), c.data_ptr(), k,
                                  None if gate is None else gate.data_ptr(), bias, strides, code, B, D, N, G,

@@ -556,8 +556,10 @@ cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, int threads, c
     const Shape sh = shape(p.D);
     const size_t shared = bwd ? bwd_shared(sh, sizeof(T), sizeof(R)) : fwd_shared(sh, sizeof(T), sizeof(R));
     const auto kernel = bwd ? block_norm_bwd_kernel<T, R, P, THREADS, CENTER> : block_norm_kernel<T, R, P, THREADS, CENTER>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
-    if (e != cudaSuccess) return e;
+    if (shared > 44 * 1024) {  // less, with the static part, a kernel has without asking
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+        if (e != cudaSuccess) return e;
+    }
     kernel<<<grid, threads, shared, s>>>(p);
     return cudaGetLastError();
 }

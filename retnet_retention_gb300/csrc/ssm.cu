@@ -115,16 +115,9 @@ __global__ void __launch_bounds__(256) ssm_shared_grad_kernel(const float* part,
     const long long m = i / quads, b = m / T_, t = m - b * T_;
     const int col = (int)(i % quads) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* const from = part + ((long long)g * tiles * tokens + m) * (2 * N) + col;
-    for (int k0 = 0; k0 < tiles; k0 += 8) {
-        float4 r[8];  // loads in flight together
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            r[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k0 + k < tiles) r[k] = __ldcs(reinterpret_cast<const float4*>(from + (k0 + k) * tokens * (2 * N)));
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v.x += r[k].x, v.y += r[k].y, v.z += r[k].z, v.w += r[k].w;
+    for (int k = 0; k < tiles; ++k) {
+        const float4 r = *reinterpret_cast<const float4*>(part + (((long long)g * tiles + k) * tokens + m) * (2 * N) + col);
+        v.x += r.x; v.y += r.y; v.z += r.z; v.w += r.w;
     }
     const SsmRows& to = col >= N ? dc : db;
     T* out = (T*)to.p + b * to.b + t * to.t + g * N + col % N;
@@ -195,7 +188,7 @@ __global__ void __launch_bounds__(128) ssm_step_kernel(const __grid_constant__ S
             y[r] = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                h[r][i] = fmaf(exp2_fast(delta * A[i]), h[r][i], in * bv[r][i]);
+                h[r][i] = fmaf(exp2_fast(fmaf(delta, A[i], kRaise)), h[r][i], in * bv[r][i]);
                 y[r] = fmaf(cv[r][i], h[r][i], y[r]);
             }
             if (on && b0 + r < p.B)
@@ -280,7 +273,7 @@ Plan forward_plan(const SsmArgs& a) {
     auto warps = [&](Split s) { return (long long)a.B * a.G * ((a.D / a.G + s.cta() - 1) / s.cta()) * kWarps; };
     const long long w = warps(split);
     long long chunks = 1;
-    if (2 * w < 5 * sms && a.T >= 128) chunks = std::min<long long>(a.T / 32, (16 * sms + w - 1) / w);
+    if (2 * w < 5 * sms && a.T >= 512) chunks = std::min<long long>(a.T / 32, (16 * sms + w - 1) / w);
     if (a.N < 64 && w * chunks <= 2 * sms) split = {a.N / 4, 1};
     return plan_of(a, split, split.cta(), chunks);
 }

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) ssm_gradients_kernel(const 
                     const float2 v = steps[u * WC + (q == 0 ? mine_at : other_at)];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 x = __fmul2_rn(both(v.x), A[q][i]), add = __fmul2_rn(both(v.y), b2[i]);
+                        const float2 x = __ffma2_rn(both(v.x), A[q][i], both(kRaise)), add = __fmul2_rn(both(v.y), b2[i]);
                         to[q][i] = __ffma2_rn(make_float2(exp2_fast(x.x), exp2_fast(x.y)), from[q][i], add);
                         if (start) to[q][i] = add;
                     }
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) ssm_gradients_kernel(const 
                             y[q] = i == 0 ? __fmul2_rn(h, c2[i]) : __ffma2_rn(h, c2[i], y[q]);
                             db2[i] = q == 0 ? __fmul2_rn(g[q][i], both(val.y)) : __ffma2_rn(g[q][i], both(val.y), db2[i]);
                             dc2[i] = q == 0 ? __fmul2_rn(h, both(du)) : __ffma2_rn(h, both(du), dc2[i]);
-                            const float2 x = __fmul2_rn(both(val.x), A[q][i]);
+                            const float2 x = __ffma2_rn(both(val.x), A[q][i], both(kRaise));
                             g[q][i] = __fmul2_rn(g[q][i], make_float2(exp2_fast(x.x), exp2_fast(x.y)));
                             if (start) g[q][i] = zero;
                             float2 qq = __fmul2_rn(g[q][i], hs[u][q][i]);

@@ -261,6 +261,39 @@ def test_steps_of_any_size():
         assert (np.abs(ref.f64(y) - want) <= rel * want + 1e-37).all()
 
 
+def test_a_step_of_zero_leaves_the_state():
+    """delta = 0 and rates of 0: the state's bits stay as they are, for thousands of tokens."""
+    T, D = 3001, 48
+    x, b = torch.ones(1, T, D, device=DEV), torch.ones(1, T, 16, device=DEV)
+    h0 = torch.randn(1, D, 16, generator=torch.Generator().manual_seed(3)).to(DEV)
+    A = -torch.rand(D, 16, device=DEV)
+    _, h = la.ssm_fwd(x, torch.zeros_like(x), A, b, b, softplus=False, h0=h0)
+    dh0 = la.ssm_bwd(x, torch.zeros_like(x), A, b, torch.zeros_like(b), x, softplus=False, h0=h0, dh_T=h0)[8]
+    step = h0.clone()
+    la.ssm_step(x[:, 0], torch.zeros(1, D, device=DEV), A, b[:, 0], b[:, 0], step, softplus=False)
+    _, still = la.ssm_fwd(torch.zeros_like(x), x, torch.zeros_like(A), b, b, softplus=False, h0=h0)
+    torch.cuda.synchronize()
+    assert torch.equal(h, h0) and torch.equal(dh0, h0) and torch.equal(step, h0) and torch.equal(still, h0)
+
+
+def test_slow_decays_do_not_drift():
+    """One impulse carried through 4000 tokens at each decay: its size is e^(sum) within the mean error a
+    decay may have (1e-8 of itself, and the exponent's own rounding)."""
+    T, D, N = 4000, 16, 8
+    A = -torch.logspace(-1, 0.5, D * N, base=10.0).view(D, N).to(DEV)
+    dt = torch.full((1, T, D), 0.02, device=DEV)
+    x, b = torch.zeros(1, T, D, device=DEV), torch.ones(1, T, N, device=DEV)
+    h0 = torch.ones(1, D, N, device=DEV)
+    _, h = la.ssm_fwd(x, dt, A, b, b, softplus=False, h0=h0)
+    torch.cuda.synchronize()
+    want = np.exp(T * float(np.float32(0.02)) * ref.f64(A))
+    size = T * 0.02 * np.abs(ref.f64(A))
+    keep = want > 1e-30
+    rel = np.abs(ref.f64(h)[0] - want) / want
+    # a token's decay: 1e-8 on average and 2^-24 of its argument, twice; a product's rounding, random
+    assert (rel <= T * 1.2e-8 + 2 * size * 2.0 ** -24 + 8 * T ** 0.5 * 2.0 ** -24)[keep].all()
+
+
 def test_results_repeat():
     c = (3, 257, 48, 16, 3, "f32", True, True, True, True, True, True, False)
     s, opts, dy, dh_T = inputs(c)
