@@ -27,7 +27,7 @@ namespace {
 
 // ---- the chunks of a sequence put together ---------------------------------------------
 
-constexpr int kJoinWarps = 32;
+constexpr int kJoinWarps = 16;
 
 // The state after a run of decay P (0: dropped) from s.
 __device__ __forceinline__ float after(float P, float b, float s) { return P == 0.f ? b : fmaf(P, s, b); }
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) ssm_join_kernel(
     const int each = (chunks + warps - 1) / warps;
     const int k0 = min(w * each, chunks), k1 = min(k0 + each, chunks);
     auto at = [&](int k) { return b * chunks + (back ? chunks - 1 - k : k); };
-    constexpr int kBatch = 8;
+    constexpr int kBatch = 4;
     float sum[kBatch];
     float4 add[kBatch];
     auto load = [&](int k) {
@@ -328,7 +328,7 @@ size_t backward_workspace(const SsmArgs& a, const Plan& plan, SsmBwdParams* bp) 
 }
 
 cudaError_t join(const SsmParams& p, bool forward, bool backward, const float* dh_T, cudaStream_t s) {
-    const int warps = std::min(kJoinWarps, (p.chunks + 7) / 8);
+    const int warps = std::min(kJoinWarps, (p.chunks + 3) / 4);
     const dim3 grid((unsigned)((long long)p.D * p.N / 128), p.B, forward && backward ? 2 : 1);
     TraceScope trace("ssm_join_kernel", s);
     ssm_join_kernel<<<grid, warps * 32, 0, s>>>(forward ? p.chunk_h : nullptr, p.h0, p.chunk_g, dh_T, p.chunk_s, p.A,

@@ -250,10 +250,16 @@ __global__ void __launch_bounds__(kWarps * 32, S::MODE == kState ? 4 : 3) ssm_sc
             else if (p.h0) from = p.h0 + (b * p.D + c[q]) * N + j * NS;
         }
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            A[q][i] = __ldg(p.A + (size_t)c[q] * N + j * NS + i) * kLog2e;
-            h[q][i] = from ? from[i] : 0.f;
-            if (kBack) P[q][kBack ? i : 0] = 1.f, back[q][kBack ? i : 0] = 0.f;
+        for (int i = 0; i < NS; i += 4) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(p.A + (size_t)c[q] * N + j * NS + i));
+            const float4 s = from ? *reinterpret_cast<const float4*>(from + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float as[4] = {a.x, a.y, a.z, a.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                A[q][i + k] = as[k] * kLog2e;
+                h[q][i + k] = ss[k];
+                if (kBack) P[q][kBack ? i + k : 0] = 1.f, back[q][kBack ? i + k : 0] = 0.f;
+            }
         }
     }
     const float skip = p.skip ? p.skip[c[0]] : 0.f, bias = p.bias ? p.bias[c[0]] : 0.f;
@@ -485,17 +491,17 @@ __global__ void __launch_bounds__(kWarps * 32, S::MODE == kState ? 4 : 3) ssm_sc
 #pragma unroll
     for (int q = 0; q < CH; ++q) {
         if (!on[q]) continue;
-        if (kY) {
-            if (!p.h_out || t1 != p.T) continue;
+        auto put = [&](float* to, const float* v) {
 #pragma unroll
-            for (int i = 0; i < NS; ++i) p.h_out[(b * p.D + c[q]) * N + j * NS + i] = h[q][i];
+            for (int i = 0; i < NS; i += 4)
+                *reinterpret_cast<float4*>(to + j * NS + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        };
+        if (kY) {
+            if (p.h_out && t1 == p.T) put(p.h_out + (b * p.D + c[q]) * N, h[q]);
         } else {
             const long long at = (b * p.chunks + chunk) * p.D + c[q];
-#pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                p.chunk_h[at * N + j * NS + i] = h[q][i];
-                if (kBack) p.chunk_g[at * N + j * NS + i] = back[q][kBack ? i : 0];
-            }
+            put(p.chunk_h + at * N, h[q]);
+            if constexpr (kBack) put(p.chunk_g + at * N, back[q]);
             if (j == 0) p.chunk_s[at] = cut ? INFINITY : sum[q];
         }
     }

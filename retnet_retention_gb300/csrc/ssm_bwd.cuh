@@ -90,12 +90,20 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) ssm_gradients_kernel(const 
     for (int q = 0; q < 2; ++q) {
         const int c = on ? c0 + (q == 0 ? mine_c : other_c) : 0;
         const long long at = ((b * p.chunks + chunk) * p.D + c) * N;
-        auto state = [&](const float* from, int i) { return on ? from[4 * j + (i ^ turn)] : 0.f; };
+        // four neighbouring states, turned
+        auto states = [&](const float* from, float2 (&to)[2]) {
+            float4 f = on ? *reinterpret_cast<const float4*>(from + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (turn & 1) f = make_float4(f.y, f.x, f.w, f.z);
+            if (turn & 2) f = make_float4(f.z, f.w, f.x, f.y);
+            to[0] = make_float2(f.x, f.y);
+            to[1] = make_float2(f.z, f.w);
+        };
+        states(p.A + (size_t)c * N, A[q]);
+        states(p.chunk_h + at, hin[q]);
+        states(p.chunk_g + at, g[q]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            A[q][i] = make_float2(state(p.A + (size_t)c * N, 2 * i) * kLog2e, state(p.A + (size_t)c * N, 2 * i + 1) * kLog2e);
-            hin[q][i] = make_float2(state(p.chunk_h + at, 2 * i), state(p.chunk_h + at, 2 * i + 1));
-            g[q][i] = make_float2(state(p.chunk_g + at, 2 * i), state(p.chunk_g + at, 2 * i + 1));
+            A[q][i] = __fmul2_rn(A[q][i], both(kLog2e));
             dA[q][i] = make_float2(0.f, 0.f);
         }
     }
