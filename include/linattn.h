@@ -517,7 +517,8 @@ LA_API la_status la_scan_step(const void* x, la_dtype dtype, const float* log_a,
  *             state itself, else may not overlap it
  *   flags     LA_CONV_SILU
  * No output may overlap an input (state_out: but state itself) or another output.  Sums in
- * fp32, rounded once.  D a multiple of 16, B * T < 2^31, B * D at most 2^33, D * W < 2^31.
+ * fp32, rounded once.  D a multiple of 16, B * T at most 2^31 - 256, B * D at most 2^33,
+ * D * W < 2^31.
  * T == 0: state_out is the state.  B == 0 is a no-op.
  * Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
  */
@@ -587,8 +588,8 @@ LA_API la_status la_short_conv_step(const void* x, long long x_stride, la_dtype 
  *   workspace at least la_ssm_workspace_size(...) bytes (which may be 0); overwritten;
  *             one for each call that may run at once
  * States, decays and sums are fp32; y is rounded where it is stored.  No output may overlap an
- * input or another output.  D a multiple of 16, B < 65536, B * T < 2^31, D * N < 2^31.  T == 0:
- * h_out is the initial state.  B == 0 is a no-op.
+ * input or another output.  D a multiple of 16, B and G < 65536, B * T at most 2^31 - 256,
+ * D * N < 2^31, B * D * N at most 2^33.  T == 0: h_out is the initial state.  B == 0 is a no-op.
  * Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
  */
 #define LA_SSM_SOFTPLUS 1u
@@ -658,8 +659,8 @@ LA_API la_status la_ssm_step(const void* x, const void* dt, const float* A, cons
  *   scale, residual_scale    finite;  eps > 0, finite
  * h_out may be h itself with the same strides; else no output may overlap an input or another
  * output.  y is the norm of h' before its rounding.  Sums in fp32; a row's squares must stay
- * below its range.  D a multiple of 16 up to 8192, B < 65536, B * T < 2^31.  B or T == 0 is a
- * no-op.  Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
+ * below its range.  D a multiple of 16 up to 8192, B < 65536, B * T at most 2^31 - 256.
+ * B or T == 0 is a no-op.  Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.
  */
 #define LA_BLOCK_POST_NORM 1u
 #define LA_BLOCK_PRE_NORM 2u

@@ -64,8 +64,10 @@ struct Memory {
 
 constexpr long long kMaxChannels = 1ll << 33;  // of all sequences together
 
+constexpr long long kMaxTokens = (1ll << 31) - 256;  // a token a tile further still is an int
+
 bool rows_shape_ok(int B, int T, int D, la_dtype dtype) {
-    return B >= 0 && T >= 0 && D >= 16 && D % 16 == 0 && valid_dtype(dtype) && (long long)B * T <= INT_MAX &&
+    return B >= 0 && T >= 0 && D >= 16 && D % 16 == 0 && valid_dtype(dtype) && (long long)B * T <= kMaxTokens &&
            (B == 0 || T == 0 || (long long)B * T <= kMaxSpan / D) && (long long)B * D <= kMaxChannels;
 }
 
@@ -91,7 +93,7 @@ la_status conv_args(ShortConvArgs* a, const float* weight, const float* bias, la
 // ---- ssm -----------------------------------------------------------------------------
 
 bool ssm_shape_ok(int B, int T, int D, int N, int G, la_dtype dtype) {
-    return rows_shape_ok(B, T, D, dtype) && B <= 65535 && (N == 8 || N == 16 || N == 32 || N == 64) && G >= 1 &&
+    return rows_shape_ok(B, T, D, dtype) && B <= 65535 && (N == 8 || N == 16 || N == 32 || N == 64) && G >= 1 && G <= 65535 &&
            D % G == 0 && D / G % 8 == 0 && (long long)D * N <= INT_MAX && (long long)G * N <= INT_MAX &&
            (long long)B * D * N <= kMaxChannels;
 }

@@ -144,7 +144,7 @@ CONV_ALL = [dict(B=-1), dict(D=0), dict(D=24), dict(W=1), dict(W=5), dict(dt=2),
 CONV_FWD = CONV_ALL + [dict(T=-1), dict(y=None), dict(y=at(4) + 8), dict(y=at(0)), dict(y=at(1)), dict(y=at(2)),
                        dict(y=at(3)), dict(so=at(4) + 16), dict(so=at(3) + 16), dict(so=at(0)), dict(so=at(5) + 4),
                        dict(pos=at(6) + 4), dict(pos=at(4)), dict(xs=arr(192, 60)), dict(xs=arr(-192, 64)),
-                       dict(ys=arr(192, 32)), dict(ys=arr(0, 64)), dict(xs=arr(1 << 50, 64)), dict(B=65536, T=32768)]
+                       dict(ys=arr(192, 32)), dict(ys=arr(0, 64)), dict(xs=arr(1 << 50, 64)), dict(B=65536, T=32768), dict(B=1, T=2 ** 31 - 255)]
 CONV_BWD = CONV_ALL + [dict(T=-1), dict(dy=None), dict(dx=None), dict(dx=at(0)), dict(dx=at(6)), dict(dx=at(7)),
                        dict(dw=at(1)), dict(dw=at(10)), dict(db=at(2)), dict(ds=at(3)), dict(ds=at(7)), dict(ds=at(8)),
                        dict(ws=None), dict(wb=0), dict(ws=at(12) + 8), dict(ws=at(0)), dict(ws=at(9)), dict(dw=at(9) + 4),
@@ -185,11 +185,11 @@ def pairs(count, **over):
     return arr(*[s for p in v for s in p])
 
 
-SSM_ALL = [dict(B=-1), dict(B=65536), dict(D=0), dict(D=24), dict(N=4), dict(N=12), dict(N=128), dict(G=0), dict(G=3), dict(G=16),
+SSM_ALL = [dict(B=-1), dict(B=65536), dict(D=0), dict(D=24), dict(N=4), dict(N=12), dict(N=128), dict(G=0), dict(G=3), dict(G=16), dict(D=524288, G=65536),
            dict(ty=2), dict(flags=2), dict(x=None), dict(dt=None), dict(A=None), dict(b=None), dict(c=None),
            dict(x=at(0) + 8), dict(A=at(2) + 4), dict(b=at(3) + 2), dict(k=at(5) + 4), dict(bias=at(7) + 8),
            dict(g=at(6) + 8), dict(h0=at(8) + 4)]
-SSM_FWD = SSM_ALL + [dict(T=-1), dict(y=None), dict(y=at(0)), dict(y=at(3)), dict(y=at(2)), dict(h=at(8) + 16), dict(h=at(9)),
+SSM_FWD = SSM_ALL + [dict(T=-1), dict(B=1, T=2 ** 31 - 255), dict(y=None), dict(y=at(0)), dict(y=at(3)), dict(y=at(2)), dict(h=at(8) + 16), dict(h=at(9)),
                      dict(h=at(10) + 4), dict(y=at(9) + 2), dict(pos=at(9)), dict(pos=at(23) + 4),
                      dict(st=pairs(6, _0=(192, 60))), dict(st=pairs(6, _2=(96, -32))), dict(st=pairs(6, _5=(192, 32))),
                      dict(st=pairs(6, _5=(0, 64))), dict(st=pairs(6, _4=(1 << 50, 64)))]
@@ -226,7 +226,7 @@ BLOCK_ALL = [dict(B=-1), dict(B=65536), dict(T=-1), dict(D=0), dict(D=24), dict(
              dict(ty=0, rty=1), dict(flags=16), dict(flags=2), dict(flags=1), dict(flags=11, g=None), dict(al=float("nan")),
              dict(be=float("inf")), dict(eps=0.0), dict(eps=float("nan")), dict(o=None), dict(o=at(0) + 8),
              dict(wp=at(2) + 4), dict(g=at(3) + 8), dict(wq=at(4) + 4), dict(os=arr(192, 60)), dict(os=arr(192, -64)),
-             dict(B=32768, T=65536)]
+             dict(B=32768, T=65536), dict(B=1, T=2 ** 31 - 255)]
 BLOCK_FWD = BLOCK_ALL + [dict(y=None), dict(flags=1, wq=None, ho=None, y=None), dict(h=at(1) + 8), dict(ho=at(5) + 4),
                          dict(y=at(0)), dict(y=at(1)), dict(y=at(5)), dict(ho=at(0)), dict(ho=at(1) + 64), dict(y=at(2)),
                          dict(hos=arr(192, 32)), dict(ys=arr(0, 64)), dict(ho=at(1), hos=arr(256, 64)), dict(ho=at(3))]
