@@ -157,7 +157,7 @@ __device__ __forceinline__ float normed(float2 (&x)[P][4], const bool (&on)[P], 
 constexpr int kRing = 3;
 
 // T: o and y; R: the residual stream.  P pieces of eight entries a thread.
-template <typename T, typename R, int P, int THREADS, bool CENTER>
+template <typename T, typename R, int P, int THREADS, bool CENTER, bool WHOLE>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS) block_norm_kernel(const __grid_constant__ BlockParams p) {
     __shared__ __align__(16) float red[4][kRedFloats];
     clear_red(red, 4);
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS) b
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         e[i] = i * width + at.lane * 8;
-        on[i] = e[i] < p.D;
+        on[i] = WHOLE || e[i] < p.D;
     }
     const unsigned first = blockIdx.x * p.rows_cta + at.slot;
     Walk ahead(p.by_T, first, leap), here = ahead;
@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS) b
 #pragma unroll
     for (int i = 0; i < P; ++i) row_weights<false>(p.w_pre, on[i], e[i], e[i] + 4, w_pre[i]);
     int slot = 0;
-    for (unsigned m = first; m - at.slot < rows; m += leap) {  // the same for every slot
-        const bool row = m < rows;
+    for (unsigned m = first; (WHOLE ? m : m - at.slot) < rows; m += leap) {  // the same for every slot
+        const bool row = WHOLE || m < rows;
         const unsigned gate_now = p.gate_each && row ? here.b : 0;
         if (gate_now != gate_of) {
             gate_of = gate_now;
@@ -256,7 +256,7 @@ constexpr int bwd_ring(int threads) { return threads > 256 ? 1 : 2; }
 
 // A CTA takes rows of one sequence where each sequence has its own gate (its sums then
 // belong to that sequence's gradient), else of all.
-template <typename T, typename R, int P, int THREADS, bool CENTER>
+template <typename T, typename R, int P, int THREADS, bool CENTER, bool WHOLE>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(const __grid_constant__ BlockParams p) {
     tc::griddep_launch_dependents();  // the sums' kernel may be scheduled (it waits itself)
     __shared__ __align__(16) float red[4][kRedFloats];
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         e[i] = i * width + at.lane * 8;
-        on[i] = e[i] < p.D;
+        on[i] = WHOLE || e[i] < p.D;
 #pragma unroll
         for (int j = 0; j < 4; ++j) s_post[i][j] = s_pre[i][j] = make_float2(0.f, 0.f);
     }
@@ -333,8 +333,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
         }
     };
     int slot = 0;
-    for (unsigned m = first; m - at.slot < end; m += leap) {
-        const bool row = m < end;
+    for (unsigned m = first; (WHOLE ? m : m - at.slot) < end; m += leap) {
+        const bool row = WHOLE || m < end;
         float2 n[P][4], q[P][4], dt[P][4];  // norm(h'), p, and dy on its way to dt
         copies_wait<kBwdRing - 1>();
         auto take = [&](auto* slots, int which, int i, float2 (&to)[4]) {  // zeros where there is nothing
@@ -551,11 +551,11 @@ BlockParams params(const BlockNormArgs& a) {
     return p;
 }
 
-template <typename T, typename R, int P, int THREADS, bool CENTER>
+template <typename T, typename R, int P, int THREADS, bool CENTER, bool WHOLE>
 cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, int threads, cudaStream_t s) {
     const Shape sh = shape(p.D);
     const size_t shared = bwd ? bwd_shared(sh, sizeof(T), sizeof(R)) : fwd_shared(sh, sizeof(T), sizeof(R));
-    const auto kernel = bwd ? block_norm_bwd_kernel<T, R, P, THREADS, CENTER> : block_norm_kernel<T, R, P, THREADS, CENTER>;
+    const auto kernel = bwd ? block_norm_bwd_kernel<T, R, P, THREADS, CENTER, WHOLE> : block_norm_kernel<T, R, P, THREADS, CENTER, WHOLE>;
     if (shared > 44 * 1024) {  // less, with the static part, a kernel has without asking
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;
@@ -566,8 +566,14 @@ cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, int threads, c
 
 template <typename T, typename R, int P, int THREADS>
 cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, int threads, cudaStream_t s) {
-    return p.center ? launch<T, R, P, THREADS, true>(p, bwd, grid, threads, s)
-                    : launch<T, R, P, THREADS, false>(p, bwd, grid, threads, s);
+    // a row for the CTA's threads, none of them past its end: no entry needs asking for
+    if constexpr (P > 1) {
+        if (p.rows_cta == 1 && p.D == 8 * P * threads)
+            return p.center ? launch<T, R, P, THREADS, true, true>(p, bwd, grid, threads, s)
+                            : launch<T, R, P, THREADS, false, true>(p, bwd, grid, threads, s);
+    }
+    return p.center ? launch<T, R, P, THREADS, true, false>(p, bwd, grid, threads, s)
+                    : launch<T, R, P, THREADS, false, false>(p, bwd, grid, threads, s);
 }
 
 template <typename T, typename R>
