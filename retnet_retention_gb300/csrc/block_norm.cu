@@ -13,12 +13,15 @@
 //   do = norm'(alpha g dt w_post),  dw_post = sum alpha g dt norm(o),
 //   norm'(v) = r (v - [mean v] - n mean(v n))
 //
-// Bound by HBM: o and h in, h' and y out.  A CTA holds a row in registers (a thread eight
-// neighbouring entries, once or twice), so that both norms cost no second read, and the
-// weights of its columns.  The next rows come through a ring in shared memory, each thread's own
-// pieces, copied in the background.  dg and dw_post are one sum over the rows, of alpha dt p, times
-// w_post and g.  y is the norm of h' before its rounding; the gradients start from the rounded
-// h' that the forward call left.
+// Bound by HBM: o and h in, h' and y out; 8 x 8192 rows of 2048 in bf16 take 166 us, 0.96 of the copy
+// rate, gradients of 4 x 4093 rows of 2048 (fp32 residual, centred) 103 us and their sums 8, 0.87.  A CTA
+// holds a row in registers (a thread eight neighbouring entries, once or twice), so that both norms cost no
+// second read, and the weights of its columns.  The next row comes through a ring in shared memory, copied in
+// the background, each thread's own pieces (fp32: each warp's).  Rows are dealt out to the CTAs in turn: a run
+// of rows for each took 200 us where this takes 190.  Rows that fill their threads have a build without
+// questions after single entries (the gradients 113 us without, 102 with).  dg and dw_post are one sum over
+// the rows, of alpha dt p, times w_post and g.  y is the norm of h' before its rounding; the gradients start
+// from the rounded h' that the forward call left.
 #include <algorithm>
 
 #include "rows.cuh"
@@ -32,6 +35,7 @@ namespace {
 struct Rows {
     const void* p;
     long long b, t;  // strides
+    bool wide;       // rows of fp32 start at multiples of 32 bytes
 };
 
 struct BlockParams {
@@ -41,6 +45,7 @@ struct BlockParams {
     float *part_post, *part_gate, *part_pre;  // backward: partial rows, or null
     int B, T, D;
     int rows_cta;                  // rows a CTA holds at once
+    int ring;                      // backward: rows of it
     Divide by_T;
     int seq_blocks;                // CTAs a sequence's rows are shared out to (0: of all sequences)
     int post, pre, center, gate_each;
@@ -126,11 +131,49 @@ struct Walk {
     }
 };
 
-// A thread's eight entries into its slot in the background.
-template <typename E>
-__device__ __forceinline__ void copy8(E* slot, const E* from) {
+// A thread's eight entries from e on into its slot in the background.  fp32 entries a warp copies
+// together, 512 bytes in a row at once (a thread's own 32 bytes are two halves of a sector, fetched twice).
+// Their pieces of four lie exchanged in every second group of four lanes, which then read without a
+// bank met twice.
+template <bool WHOLE, typename E>
+__device__ __forceinline__ void copy8(E* slot, const E* row, int e, int D) {
+    if constexpr (sizeof(E) == 2) {
+        if (WHOLE || e < D) copy16(slot, row + e, true);
+    } else {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 0; k < (int)sizeof(E) / 2; ++k) copy16((char*)slot + 16 * k, (const char*)from + 16 * k, true);
+        for (int k = 0; k < 2; ++k) {
+            const int q = k * 32 + lane;
+            if (WHOLE || e - lane * 8 + q * 4 < D)
+                copy16(slot - lane * 8 + (q ^ (q >> 3 & 1)) * 4, row + e - lane * 8 + q * 4, true);
+        }
+    }
+}
+
+template <typename E>
+__device__ __forceinline__ void read8(const E* slot, float2 (&x)[4]) {
+    const int s = sizeof(E) == 2 ? 0 : threadIdx.x >> 2 & 1;
+    floats8<false>(raw8<sizeof(E) == 2>(slot, 4 * s, 4 - 4 * s), x);
+}
+
+// Around a warp's reads of what its lanes copied for one another.
+template <typename T, typename R>
+__device__ __forceinline__ void warp_slots() {
+    if constexpr (sizeof(T) == 4 || sizeof(R) == 4) __syncwarp();
+}
+
+// Eight entries to memory: fp32 ones in one 32-byte access where every row allows it.
+template <typename E>
+__device__ __forceinline__ void put8(E* to, const float2 (&x)[4], bool wide) {
+    if constexpr (sizeof(E) == 4) {
+        if (wide) {
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(x[0].x), "f"(x[0].y),
+                         "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y)
+                         : "memory");
+            return;
+        }
+    }
+    store8<true, false>(to, 0, 4, x);
 }
 
 template <bool MINUS_MEAN, int P>
@@ -154,13 +197,20 @@ __device__ __forceinline__ float normed(float2 (&x)[P][4], const bool (&on)[P], 
     return rsqrtf(q[0] * inv_d + eps);
 }
 
-constexpr int kRing = 3;
+// Rows of a ring, by a CTA's threads.  Forward: one row ahead where an SM holds three CTAs or more, whose
+// rows then keep the memory busy and no more than that: with three rows ahead 8 x 8192 rows of 2048 took 192 us,
+// with one 167 (of 512 to 4096 entries in bf16 0.80 of the copy rate against 0.86 to 0.93); the one CTA of 512 threads reaches
+// 0.83 with three and 0.58 with one.  Backward: two, but one above 128 threads, where two leave an SM
+// fewer CTAs (4096 entries: 0.60 against 0.77).
+constexpr int fwd_ring(int threads) { return threads > 256 ? 3 : 1; }
+constexpr int bwd_ring(int threads) { return threads > 128 ? 1 : 2; }
 
 // T: o and y; R: the residual stream.  P pieces of eight entries a thread.
 template <typename T, typename R, int P, int THREADS, bool CENTER, bool WHOLE>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS) block_norm_kernel(const __grid_constant__ BlockParams p) {
     __shared__ __align__(16) float red[4][kRedFloats];
     clear_red(red, 4);
+    constexpr int kRing = fwd_ring(THREADS);
     extern __shared__ __align__(16) unsigned char ring[];  // [kRing][P][threads] of T's eight, then of R's
     const Place at(p.rows_cta);
     const int width = at.warps * 32 * 8;  // entries of a piece of the row
@@ -183,11 +233,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS) b
     auto fetch = [&](int slot) {
         if (m_ahead < rows) {
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (on[i]) {
-                    copy8(slots_o + (slot * P + i) * piece, ahead.at<const T>(p.o) + e[i]);
-                    if (p.h.p) copy8(slots_h + (slot * P + i) * piece, ahead.at<const R>(p.h) + e[i]);
-                }
+            for (int i = 0; i < P; ++i) {
+                copy8<WHOLE>(slots_o + (slot * P + i) * piece, ahead.at<const T>(p.o), e[i], p.D);
+                if (p.h.p) copy8<WHOLE>(slots_h + (slot * P + i) * piece, ahead.at<const R>(p.h), e[i], p.D);
+            }
         }
         copies_commit();
         m_ahead += leap;
@@ -216,25 +265,27 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS) b
         }
         float2 v[P][4];
         copies_wait<kRing - 1>();
+        warp_slots<T, R>();
 #pragma unroll
         for (int i = 0; i < P; ++i) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.f, 0.f);
-            if (row && on[i]) floats8<false>(raw8<true>(slots_o + (slot * P + i) * piece, 0, 4), v[i]);
+            if (row && on[i]) read8(slots_o + (slot * P + i) * piece, v[i]);
         }
         float r = 1.f;
         if (p.post) r = normed<CENTER, P>(v, on, inv_d, p.eps, red[at.slot], turn, at);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             float2 h[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
-            if (row && on[i] && p.h.p) floats8<false>(raw8<true>(slots_h + (slot * P + i) * piece, 0, 4), h);
+            if (row && on[i] && p.h.p) read8(slots_h + (slot * P + i) * piece, h);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 v[i][j] = __fmul2_rn(__fmul2_rn(v[i][j], both(r)), gw[i][j]);
                 v[i][j] = __ffma2_rn(h[j], both(p.beta), v[i][j]);
             }
-            if (row && on[i] && p.h_out.p) store8<true, false>(here.at<R>(p.h_out) + e[i], 0, 4, v[i]);
+            if (row && on[i] && p.h_out.p) put8(here.at<R>(p.h_out) + e[i], v[i], p.h_out.wide);
         }
+        warp_slots<T, R>();
         fetch(slot);
         slot = slot + 1 == kRing ? 0 : slot + 1;
         if (p.pre) {
@@ -243,16 +294,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS) b
             for (int i = 0; i < P; ++i) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(__fmul2_rn(v[i][j], both(r)), w_pre[i][j]);
-                if (row && on[i]) store8<true, false>(here.at<T>(p.y) + e[i], 0, 4, v[i]);
+                if (row && on[i]) put8(here.at<T>(p.y) + e[i], v[i], p.y.wide);
             }
         }
         here.next();
     }
 }
-
-// Rows of the gradients' ring: one where a CTA has 512 threads (two of fp32 entries would not fit
-// an SM's shared memory).
-constexpr int bwd_ring(int threads) { return threads > 256 ? 1 : 2; }
 
 // A CTA takes rows of one sequence where each sequence has its own gate (its sums then
 // belong to that sequence's gradient), else of all.
@@ -262,7 +309,6 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
     __shared__ __align__(16) float red[4][kRedFloats];
     clear_red(red, 4);
     extern __shared__ __align__(16) unsigned char ring[];  // o, dy, h, dh; at the end [rows_cta][D] sums
-    constexpr int kBwdRing = bwd_ring(THREADS);
     const Place at(p.rows_cta);
     const int width = at.warps * 32 * 8;
     const unsigned begin = p.seq_blocks ? blockIdx.x / p.seq_blocks * p.by_T.T : 0;
@@ -271,16 +317,16 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
     const unsigned first = begin + (p.seq_blocks ? blockIdx.x % p.seq_blocks : blockIdx.x) * p.rows_cta + at.slot;
     const float inv_d = 1.f / (float)p.D;
     const int piece = blockDim.x * 8;
-    T* const slots_t = reinterpret_cast<T*>(ring) + threadIdx.x * 8;  // [kBwdRing][2][P]
-    R* const slots_r = reinterpret_cast<R*>(ring + (size_t)kBwdRing * 2 * P * piece * sizeof(T)) + threadIdx.x * 8;
+    T* const slots_t = reinterpret_cast<T*>(ring) + threadIdx.x * 8;  // [p.ring][2][P]
+    R* const slots_r = reinterpret_cast<R*>(ring + (size_t)p.ring * 2 * P * piece * sizeof(T)) + threadIdx.x * 8;
     int turn = 0;
     bool on[P];
     int e[P];
     float2 s_post[P][4], s_pre[P][4];  // sums of alpha dt p and dy n
     const float* gate = p.gate ? p.gate + (p.seq_blocks ? (size_t)(blockIdx.x / p.seq_blocks) * p.D : 0) : nullptr;
     // the thread's entries of alpha g w_post and of w_pre, in shared memory: two quads of each
-    float4* const gws = reinterpret_cast<float4*>(reinterpret_cast<R*>(ring + (size_t)kBwdRing * 2 * P * piece * sizeof(T)) +
-                                                  (size_t)kBwdRing * 2 * P * piece) + threadIdx.x;
+    float4* const gws = reinterpret_cast<float4*>(reinterpret_cast<R*>(ring + (size_t)p.ring * 2 * P * piece * sizeof(T)) +
+                                                  (size_t)p.ring * 2 * P * piece) + threadIdx.x;
     float4* const w_pres = gws + 2 * P * blockDim.x;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -294,22 +340,22 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
     auto fetch = [&](int slot) {
         if (m_ahead < end) {
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (on[i]) {
-                    copy8(slots_t + (slot * 2 * P + i) * piece, ahead.at<const T>(p.o) + e[i]);
-                    if (p.pre) {
-                        copy8(slots_t + (slot * 2 * P + P + i) * piece, ahead.at<const T>(p.dy) + e[i]);
-                        copy8(slots_r + (slot * 2 * P + i) * piece, ahead.at<const R>(p.h) + e[i]);
-                    }
-                    if (p.dh.p) copy8(slots_r + (slot * 2 * P + P + i) * piece, ahead.at<const R>(p.dh) + e[i]);
+            for (int i = 0; i < P; ++i) {
+                T* const t = slots_t + (slot * 2 * P + i) * piece;
+                R* const r = slots_r + (slot * 2 * P + i) * piece;
+                copy8<WHOLE>(t, ahead.at<const T>(p.o), e[i], p.D);
+                if (p.pre) {
+                    copy8<WHOLE>(t + P * piece, ahead.at<const T>(p.dy), e[i], p.D);
+                    copy8<WHOLE>(r, ahead.at<const R>(p.h), e[i], p.D);
                 }
+                if (p.dh.p) copy8<WHOLE>(r + P * piece, ahead.at<const R>(p.dh), e[i], p.D);
+            }
         }
         copies_commit();
         m_ahead += leap;
         ahead.next();
     };
-#pragma unroll
-    for (int i = 0; i < kBwdRing; ++i) fetch(i);
+    for (int i = 0; i < p.ring; ++i) fetch(i);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         float2 g[4], w[4];
@@ -336,10 +382,12 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
     for (unsigned m = first; (WHOLE ? m : m - at.slot) < end; m += leap) {
         const bool row = WHOLE || m < end;
         float2 n[P][4], q[P][4], dt[P][4];  // norm(h'), p, and dy on its way to dt
-        copies_wait<kBwdRing - 1>();
+        if (p.ring == 1) copies_wait<0>();
+        else copies_wait<1>();
+        warp_slots<T, R>();
         auto take = [&](auto* slots, int which, int i, float2 (&to)[4]) {  // zeros where there is nothing
             if (row && on[i]) {
-                floats8<false>(raw8<true>(slots + (slot * 2 * P + which * P + i) * piece, 0, 4), to);
+                read8(slots + (slot * 2 * P + which * P + i) * piece, to);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) to[j] = make_float2(0.f, 0.f);
@@ -381,6 +429,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 float2 w[4];
+                __syncwarp();
                 take(slots_t, 1, i, dt[i]);
                 weights(w_pres, i, w);
 #pragma unroll
@@ -400,6 +449,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
         for (int i = 0; i < P; ++i) {
             float2 into[4], w[4];
             if (p.dh.p) {
+                __syncwarp();
                 take(slots_r, 1, i, into);
             } else {
 #pragma unroll
@@ -414,7 +464,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
             if (row && on[i] && p.d_res.p) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) into[j] = __fmul2_rn(into[j], both(p.beta));
-                store8<true, false>(here.at<R>(p.d_res) + e[i], 0, 4, into);
+                put8(here.at<R>(p.d_res) + e[i], into, p.d_res.wide);
             }
             weights(gws, i, w);
 #pragma unroll
@@ -426,8 +476,9 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
             s[0] += dot8(dt[i], q[i]);
             if (CENTER) s[1] += sum8(dt[i]);
         }
+        warp_slots<T, R>();
         fetch(slot);
-        slot = slot + 1 == kBwdRing ? 0 : slot + 1;
+        slot = slot + 1 == p.ring ? 0 : slot + 1;
         if (p.post) {
             row_sums<2>(s, red[at.slot], turn, at.warps, at.warp);
             const float2 along = both(-s[0] * inv_d), mean = both(CENTER ? -s[1] * inv_d : 0.f);
@@ -439,7 +490,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
         }
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            if (row && on[i]) store8<true, false>(here.at<T>(p.d_o) + e[i], 0, 4, dt[i]);
+            if (row && on[i]) put8(here.at<T>(p.d_o) + e[i], dt[i], p.d_o.wide);
         here.next();
     }
     // one partial row a CTA, over its row slots
@@ -495,7 +546,7 @@ Shape shape(int D) {
 }
 
 // Bytes of a CTA's shared memory, T and R the sizes of an entry of o and of the residual.
-size_t fwd_shared(const Shape& sh, size_t T, size_t R) { return (size_t)kRing * sh.pieces * sh.threads * sh.rows * 8 * (T + R); }
+size_t fwd_shared(const Shape& sh, size_t T, size_t R) { return (size_t)fwd_ring(sh.threads * sh.rows) * sh.pieces * sh.threads * sh.rows * 8 * (T + R); }
 size_t bwd_shared(const Shape& sh, size_t T, size_t R) {
     const size_t entries = (size_t)sh.pieces * sh.threads * sh.rows * 8;
     return entries * (bwd_ring(sh.threads * sh.rows) * 2 * (T + R) + 2 * sizeof(float));  // the sums at the end fit in the ring
@@ -532,7 +583,9 @@ void bwd_blocks(const BlockNormArgs& a, int* each, long long* all) {
 }
 
 BlockParams params(const BlockNormArgs& a) {
-    auto rows = [](const void* p, const long long* s) { return Rows{p, s[0], s[1]}; };
+    auto rows = [](const void* p, const long long* s) {
+        return Rows{p, s[0], s[1], (reinterpret_cast<uintptr_t>(p) | s[0] * 4 | s[1] * 4) % 32 == 0};
+    };
     BlockParams p = {};
     p.o = rows(a.o, a.o_strides);
     p.h = rows(a.h, a.h_strides);
@@ -607,6 +660,7 @@ cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, cudaStream_t s) {
 
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, cudaStream_t s) {
     BlockParams p = params(a);
+    p.ring = bwd_ring(shape(a.D).threads * p.rows_cta);
     int each;
     long long all;
     bwd_blocks(a, &each, &all);

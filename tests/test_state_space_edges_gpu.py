@@ -210,3 +210,36 @@ def test_steps_and_reads_in_one_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, want[k])
     assert torch.equal(cs, end[0]) and torch.equal(h, end[1])
+
+
+@pytest.mark.parametrize("D", [48, 512, 528, 2048, 4096, 8192])
+@pytest.mark.parametrize("dtypes", [("f32", "f32"), ("bf16", "f32")], ids="-".join)
+def test_rows_at_any_multiple_of_16_bytes(D, dtypes):
+    """Rows of every width that begin 16 bytes behind a multiple of 32 give what dense ones give."""
+    B, T = 2, 5
+    to, th = ({"f32": torch.float32, "bf16": torch.bfloat16}[d] for d in dtypes)
+    g = torch.Generator().manual_seed(D)
+    dense = [torch.randn(B, T, D, generator=g).to(t).to(DEV) for t in (to, th, to, th)]
+    pre, post, gate = (torch.randn(D, generator=g).to(DEV) for _ in range(3))
+    opts = dict(post_norm=True, post_weight=post, pre_weight=pre, gate=gate, scale=0.5, residual_scale=0.75, center=True)
+
+    def moved(t):
+        e = 16 // t.element_size()
+        buf = torch.zeros(B, T, D + 2 * e + e, dtype=t.dtype, device=DEV)
+        return buf[:, :, e:e + D]
+
+    def run(place):
+        o, h, dy, dh = (place(t).copy_(t) for t in dense)
+        h_out, y, d_o, d_h = (place(t) for t in (h, o, o, h))
+        la.block_norm_fwd(o, h, h_out=h_out, out=y, **opts)
+        grads = la.block_norm_bwd(o, h_out, dy, dh, d_o=d_o, dh=d_h, **opts)
+        return h_out, y, *grads
+
+    want, got = run(torch.empty_like), run(moved)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    f64 = [ref.f64(t) for t in dense]
+    p = bref.block(f64[0], f64[1], True, ref.f64(post), ref.f64(gate), 0.5, 0.75, True, ref.f64(pre), True,
+                   float(np.float32(1e-6)))
+    ref.check("h'", got[0], p[0], p[1], th)
+    ref.check("y", got[1], p[2], p[3], to)
