@@ -197,13 +197,11 @@ __device__ __forceinline__ float normed(float2 (&x)[P][4], const bool (&on)[P], 
     return rsqrtf(q[0] * inv_d + eps);
 }
 
-// Rows of a ring, by a CTA's threads.  Forward: one row ahead where an SM holds three CTAs or more, whose
-// rows then keep the memory busy and no more than that: with three rows ahead 8 x 8192 rows of 2048 took 192 us,
-// with one 167 (of 512 to 4096 entries in bf16 0.80 of the copy rate against 0.86 to 0.93); the one CTA of 512 threads reaches
-// 0.83 with three and 0.58 with one.  Backward: two, but one above 128 threads, where two leave an SM
-// fewer CTAs (4096 entries: 0.60 against 0.77).
+// Rows of the forward ring, by a CTA's threads: one row ahead where an SM holds three CTAs or more, whose
+// rows then keep the memory busy and no more than that (8 x 8192 rows of 2048: 192 us with three rows ahead,
+// 166 with one; rows of 512 to 4096 entries in bf16 0.80 of the copy rate against 0.86 to 0.93); the one
+// CTA of 512 threads reaches 0.83 with three and 0.58 with one.
 constexpr int fwd_ring(int threads) { return threads > 256 ? 3 : 1; }
-constexpr int bwd_ring(int threads) { return threads > 128 ? 1 : 2; }
 
 // T: o and y; R: the residual stream.  P pieces of eight entries a thread.
 template <typename T, typename R, int P, int THREADS, bool CENTER, bool WHOLE>
@@ -547,10 +545,12 @@ Shape shape(int D) {
 
 // Bytes of a CTA's shared memory, T and R the sizes of an entry of o and of the residual.
 size_t fwd_shared(const Shape& sh, size_t T, size_t R) { return (size_t)fwd_ring(sh.threads * sh.rows) * sh.pieces * sh.threads * sh.rows * 8 * (T + R); }
-size_t bwd_shared(const Shape& sh, size_t T, size_t R) {
+size_t bwd_shared(const Shape& sh, size_t T, size_t R, int ring) {
     const size_t entries = (size_t)sh.pieces * sh.threads * sh.rows * 8;
-    return entries * (bwd_ring(sh.threads * sh.rows) * 2 * (T + R) + 2 * sizeof(float));  // the sums at the end fit in the ring
+    return entries * (ring * 2 * (T + R) + 2 * sizeof(float));  // the sums at the end fit in the ring
 }
+
+constexpr size_t kMostShared = 222 << 10;  // of a CTA, beside its static part
 
 // CTAs an SM holds: by the registers the launch bounds leave a thread, and by shared memory.
 long long resident(const Shape& sh, int threads_per_sm, size_t shared) {
@@ -559,6 +559,15 @@ long long resident(const Shape& sh, int threads_per_sm, size_t shared) {
 }
 
 size_t entry_size(bool bf16) { return bf16 ? 2 : 4; }
+
+// Rows of the gradients' ring: two up to 128 threads (4 x 4093 rows of 2048, fp32 residual, centred: 104 us, with one
+// 117), above where the second costs an SM no CTA (4096 entries in bf16 0.82 of the copy rate with two CTAs
+// and rows, 0.77 with one row, 0.60 with one CTA and two rows; 5120 0.59, with one row 0.49).
+int bwd_ring(const Shape& sh, size_t T, size_t R) {
+    if (sh.threads * sh.rows <= 128) return 2;
+    const size_t two = bwd_shared(sh, T, R, 2);
+    return two <= kMostShared && resident(sh, 512, two) == resident(sh, 512, bwd_shared(sh, T, R, 1)) ? 2 : 1;
+}
 
 long long fwd_blocks(const BlockNormArgs& a) {
     const Shape sh = shape(a.D);
@@ -571,7 +580,7 @@ long long fwd_blocks(const BlockNormArgs& a) {
 void bwd_blocks(const BlockNormArgs& a, int* each, long long* all) {
     const Shape sh = shape(a.D);
     // as many for either type of the residual: the workspace's size is asked for without it
-    const long long most = sm_count() * resident(sh, 512, bwd_shared(sh, entry_size(a.bf16), 4));
+    const long long most = sm_count() * resident(sh, 512, bwd_shared(sh, entry_size(a.bf16), 4, bwd_ring(sh, entry_size(a.bf16), 4)));
     if (a.gate && a.gate_each) {
         const long long rows = ((long long)a.T + sh.rows - 1) / sh.rows;
         *each = (int)std::max(1ll, std::min(rows, most / a.B));
@@ -607,7 +616,7 @@ BlockParams params(const BlockNormArgs& a) {
 template <typename T, typename R, int P, int THREADS, bool CENTER, bool WHOLE>
 cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, int threads, cudaStream_t s) {
     const Shape sh = shape(p.D);
-    const size_t shared = bwd ? bwd_shared(sh, sizeof(T), sizeof(R)) : fwd_shared(sh, sizeof(T), sizeof(R));
+    const size_t shared = bwd ? bwd_shared(sh, sizeof(T), sizeof(R), p.ring) : fwd_shared(sh, sizeof(T), sizeof(R));
     const auto kernel = bwd ? block_norm_bwd_kernel<T, R, P, THREADS, CENTER, WHOLE> : block_norm_kernel<T, R, P, THREADS, CENTER, WHOLE>;
     if (shared > 44 * 1024) {  // less, with the static part, a kernel has without asking
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
@@ -660,7 +669,7 @@ cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, cudaStream_t s) {
 
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, cudaStream_t s) {
     BlockParams p = params(a);
-    p.ring = bwd_ring(shape(a.D).threads * p.rows_cta);
+    p.ring = bwd_ring(shape(a.D), entry_size(a.bf16), entry_size(a.residual_bf16));
     int each;
     long long all;
     bwd_blocks(a, &each, &all);

@@ -15,6 +15,11 @@
 // in registers, so that x is read once but for the W - 1 rows before a run (and backward
 // behind it).  The next eight rows come through a ring in shared memory, each thread's own
 // pieces, copied in the background: loads in flight cost no registers and there is no barrier.
+//
+// 8 x 8192 tokens of 4096 channels in bf16: 168 us, 6.4 TB/s, 0.95 of the copy rate.  The gradients
+// (4 x 4093 tokens of 4096 channels: 96 us, 4.2 TB/s) are bound by their instructions, 122 for a token of
+// a warp's 128 channels, a third of them packed and two turns long; eight channels a thread did not fit the
+// registers (182 us).  A step of 256 sequences takes 3 us beside its launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -135,7 +140,7 @@ __device__ __forceinline__ void convolve(const float2 (&w)[W][V / 2], const floa
 }
 
 // Tokens of the unrolled loop, a multiple of the W - 1 rows kept (a long loop does not stay in
-// the instruction cache: nine tokens of the gradients took 119 us where three take 100), and
+// the instruction cache: nine tokens of the gradients took 119 us where three take 96), and
 // rows of the ring, a multiple of those.
 template <int W>
 constexpr int kUnrollOf = W == 4 ? 3 : 4;

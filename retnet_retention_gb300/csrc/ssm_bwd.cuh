@@ -13,6 +13,10 @@
 // is walked backward: the first half's are computed twice, which costs less than the warps
 // that the registers of a whole block would.
 //
+// 4 x 4096 tokens of 2048 channels of 16 states: 643 us of this walk, after 231 of the summary walk and
+// 21 of the join, before 31 of the sums; bound by issue slots, 233 instructions for a token of a warp's 16
+// channels, 58 of them packed, at 3 warps a scheduler (what 168 registers leave); HBM is at 16 %.
+//
 // A lane holds four states of two channels.  Sums over n cross L = N / 4 lanes, sums over
 // channels (for db, dc) the other 32 / L: both give away half of what they hold at each
 // step.  Which state a register holds is turned with the lane (n = 4 j + (i ^ turn)), and
