@@ -14,12 +14,12 @@
 //   norm'(v) = r (v - [mean v] - n mean(v n))
 //
 // Bound by HBM: o and h in, h' and y out; 8 x 8192 rows of 2048 in bf16 take 166 us, 0.96 of the copy
-// rate, gradients of 4 x 4093 rows of 2048 (fp32 residual, centred) 103 us and their sums 8, 0.87.  A CTA
+// rate, gradients of 4 x 4093 rows of 2048 (fp32 residual, centred) 103 us, 0.87, and their sums 8.  A CTA
 // holds a row in registers (a thread eight neighbouring entries, once or twice), so that both norms cost no
 // second read, and the weights of its columns.  The next row comes through a ring in shared memory, copied in
 // the background, each thread's own pieces (fp32: each warp's).  Rows are dealt out to the CTAs in turn: a run
 // of rows for each took 200 us where this takes 190.  Rows that fill their threads have a build without
-// questions after single entries (the gradients 113 us without, 102 with).  dg and dw_post are one sum over
+// questions after single entries (the gradients 113 us without, 103 with).  dg and dw_post are one sum over
 // the rows, of alpha dt p, times w_post and g.  y is the norm of h' before its rounding; the gradients start
 // from the rounded h' that the forward call left.
 #include <algorithm>
@@ -104,9 +104,10 @@ __device__ __forceinline__ float sum8(const float2 (&x)[4]) {
 // A thread's place: row slot, its warp in the row, its first entry.
 struct Place {
     int slot, warp, warps, lane;
-    __device__ Place(int rows_cta) {
-        const int per = blockDim.x / rows_cta;
-        slot = threadIdx.x / per;
+    // one row a CTA: slot 0 known to all, so that its rows' addresses are the CTA's, not each thread's
+    __device__ Place(int rows_cta, bool one) {
+        const int per = one ? blockDim.x : blockDim.x / rows_cta;
+        slot = one ? 0 : threadIdx.x / per;
         lane = threadIdx.x - slot * per;
         warps = per / 32;
         warp = lane / 32;
@@ -210,9 +211,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS) b
     clear_red(red, 4);
     constexpr int kRing = fwd_ring(THREADS);
     extern __shared__ __align__(16) unsigned char ring[];  // [kRing][P][threads] of T's eight, then of R's
-    const Place at(p.rows_cta);
+    const Place at(p.rows_cta, WHOLE);
     const int width = at.warps * 32 * 8;  // entries of a piece of the row
-    const unsigned rows = p.by_T.T * (unsigned)p.B, leap = gridDim.x * p.rows_cta;
+    const unsigned rows = p.by_T.T * (unsigned)p.B, leap = gridDim.x * (WHOLE ? 1 : p.rows_cta);
     const float inv_d = 1.f / (float)p.D;
     T* const slots_o = reinterpret_cast<T*>(ring) + threadIdx.x * 8;
     R* const slots_h = reinterpret_cast<R*>(ring + (size_t)kRing * P * blockDim.x * 8 * sizeof(T)) + threadIdx.x * 8;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
     __shared__ __align__(16) float red[4][kRedFloats];
     clear_red(red, 4);
     extern __shared__ __align__(16) unsigned char ring[];  // o, dy, h, dh; at the end [rows_cta][D] sums
-    const Place at(p.rows_cta);
+    const Place at(p.rows_cta, WHOLE);
     const int width = at.warps * 32 * 8;
     const unsigned begin = p.seq_blocks ? blockIdx.x / p.seq_blocks * p.by_T.T : 0;
     const unsigned end = p.seq_blocks ? begin + p.by_T.T : p.by_T.T * (unsigned)p.B;
@@ -560,11 +561,10 @@ long long resident(const Shape& sh, int threads_per_sm, size_t shared) {
 
 size_t entry_size(bool bf16) { return bf16 ? 2 : 4; }
 
-// Rows of the gradients' ring: two up to 128 threads (4 x 4093 rows of 2048, fp32 residual, centred: 104 us, with one
-// 117), above where the second costs an SM no CTA (4096 entries in bf16 0.82 of the copy rate with two CTAs
-// and rows, 0.77 with one row, 0.60 with one CTA and two rows; 5120 0.59, with one row 0.49).
+// Rows of the gradients' ring: two where the second costs an SM no CTA (rows of 2048 in bf16 0.89 of the copy rate,
+// with one row 0.83; 5120 0.59 and 0.49), else one (2048 beside an fp32 residual 0.96, with two rows and a CTA
+// fewer 0.84; 4096 in bf16 0.77 and 0.60).
 int bwd_ring(const Shape& sh, size_t T, size_t R) {
-    if (sh.threads * sh.rows <= 128) return 2;
     const size_t two = bwd_shared(sh, T, R, 2);
     return two <= kMostShared && resident(sh, 512, two) == resident(sh, 512, bwd_shared(sh, T, R, 1)) ? 2 : 1;
 }
