@@ -17,9 +17,10 @@
 // pieces, copied in the background: loads in flight cost no registers and there is no barrier.
 //
 // 8 x 8192 tokens of 4096 channels in bf16: 168 us, 6.4 TB/s, 0.95 of the copy rate.  The gradients
-// (4 x 4093 tokens of 4096 channels: 96 us, 4.2 TB/s) are bound by their instructions, 122 for a token of
-// a warp's 128 channels, a third of them packed and two turns long; eight channels a thread did not fit the
-// registers (182 us).  A step of 256 sequences takes 3 us beside its launch.
+// (4 x 4093 tokens of 4096 channels: 92 us, 4.4 TB/s) are bound by their instructions, 112 for a token of
+// a warp's 128 channels, 38 of them packed and two turns long; a ring of W - 1 rows in registers beside the
+// token's own took 10 more, to move them (96 us); eight channels a thread did not fit the registers (182 us).
+// A step of 256 sequences of 4096 channels takes 4.8 us in a graph.
 #include <algorithm>
 #include <type_traits>
 
@@ -120,32 +121,31 @@ __device__ __forceinline__ Pack<T, V> row_before(const ConvParams& p, long long 
     return r;
 }
 
-// u of a token from its row `cur` and those before it: row k back is before[(from - k) mod
-// (W - 1)], a place known when the loop is unrolled, so that the rows never move.
-template <int W, int V, int FROM>
+// u of a token from the last W rows, its own at rows[AT]: row k back is rows[(AT - k) mod W], a
+// place known when the loop is unrolled, so that the rows never move.
+template <int W, int V, int AT>
 __device__ __forceinline__ void convolve(const float2 (&w)[W][V / 2], const float2 (&bias)[V / 2],
-                                         const float2 (&before)[W - 1][V / 2], const float2 (&cur)[V / 2], int reach,
-                                         float2 (&u)[V / 2]) {
+                                         const float2 (&rows)[W][V / 2], int reach, float2 (&u)[V / 2]) {
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) u[i] = __ffma2_rn(w[W - 1][i], cur[i], bias[i]);
+    for (int i = 0; i < V / 2; ++i) u[i] = __ffma2_rn(w[W - 1][i], rows[AT][i], bias[i]);
 #pragma unroll
     for (int k = W - 1; k > 0; --k) {
         if (k <= reach) {
-            constexpr int kMod = W - 1;
-            const int at = ((FROM - k) % kMod + kMod) % kMod;
+            constexpr int kWrap = AT + W;
+            const int at = (kWrap - k) % W;
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) u[i] = __ffma2_rn(w[W - 1 - k][i], before[at][i], u[i]);
+            for (int i = 0; i < V / 2; ++i) u[i] = __ffma2_rn(w[W - 1 - k][i], rows[at][i], u[i]);
         }
     }
 }
 
-// Tokens of the unrolled loop, a multiple of the W - 1 rows kept (a long loop does not stay in
-// the instruction cache: nine tokens of the gradients took 119 us where three take 96), and
-// rows of the ring, a multiple of those.
+// Tokens of the unrolled loop, a multiple of the W rows kept (a long loop does not stay in the
+// instruction cache: nine tokens of the gradients took 119 us where three took 96, four 92), and rows of the
+// ring, a multiple of those.
 template <int W>
-constexpr int kUnrollOf = W == 4 ? 3 : 4;
+constexpr int kUnrollOf = W == 3 ? 3 : 4;
 template <int W>
-constexpr int kAheadOf = W == 4 ? 9 : 8;
+constexpr int kAheadOf = W == 3 ? 9 : 8;
 
 // How far the taps of the next tokens reach, loaded a turn of the loop before it is looked at.
 template <int W>
@@ -212,10 +212,10 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const __grid_co
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(i, i);
-    float2 w[W][V / 2], bias[V / 2], before[W - 1][V / 2];
+    float2 w[W][V / 2], bias[V / 2], rows[W][V / 2];  // the token's and those before it
     load_weights<W, V>(p, c, w, bias);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) row_before<T, W, V>(p, b, t0 - (W - 1) + j, c).floats(before[j]);
+    for (int j = 0; j < W - 1; ++j) row_before<T, W, V>(p, b, t0 - (W - 1) + j, c).floats(rows[j + 1]);
     if (t0 == 0 && p.state_out) {
         // the sequence's first thread has read the state and may write it in place: row j
         // is row T - W + 1 + j of the tokens behind it
@@ -234,13 +234,11 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_kernel(const __grid_co
             constexpr int i = decltype(index)::value;
             copies_wait<kAhead - 1>();
             Pack<T, V> r;
-            float2 cur[V / 2], u[V / 2];
+            float2 u[V / 2];
             r.load(reinterpret_cast<const T*>(&ring[slot + i][threadIdx.x]));
-            r.floats(cur);
+            r.floats(rows[i % W]);
             fetch(i0 + i + kAhead, slot + i);
-            convolve<W, V, i>(w, bias, before, cur, reach, u);
-#pragma unroll
-            for (int k = 0; k < V / 2; ++k) before[i % (W - 1)][k] = cur[k];
+            convolve<W, V, i % W>(w, bias, rows, reach, u);
             if (p.silu) {
 #pragma unroll
                 for (int k = 0; k < V / 2; ++k) u[k] = __fmul2_rn(u[k], sigmoid2<T>(u[k]));
@@ -301,12 +299,11 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __gri
             };
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) fetch(i, i);
-            float2 before[W - 1][V / 2], dus[W - 1][V / 2];  // the last rows, the last du
-            int reached[W - 1];                              // and how far their taps reached
+            float2 rows[W][V / 2], dus[W][V / 2];  // the token's row and the last ones, their du
+            int reached[W];                        // and, where not all, how far their taps reached
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) {
-                row_before<T, W, V>(p, b, t0 - (W - 1) + j, c).floats(before[j]);
-                reached[j] = W - 1;
+            for (int j = 0; j < W; ++j) {
+                if (j > 0) row_before<T, W, V>(p, b, t0 - W + j, c).floats(rows[j]);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) dus[j][e] = make_float2(0.f, 0.f);
             }
@@ -322,11 +319,14 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __gri
                     constexpr int i = decltype(index)::value;
                     constexpr bool kWhole = decltype(whole)::value;
                     const int m = i0 + i;  // token t0 + m
-                    float2 cur[V / 2], du[V / 2];
+                    constexpr int kAt = i % W;
+                    float2(&cur)[V / 2] = rows[kAt], (&du)[V / 2] = dus[kAt];
                     int reach = W - 1;
                     copies_wait<kAhead - 1>();
+                    if (!kWhole) {
 #pragma unroll
-                    for (int e = 0; e < V / 2; ++e) cur[e] = du[e] = make_float2(0.f, 0.f);
+                        for (int e = 0; e < V / 2; ++e) cur[e] = du[e] = make_float2(0.f, 0.f);
+                    }
                     if (kWhole || m < there) {
                         Pack<T, V> in;
                         in.load(reinterpret_cast<const T*>(&ring[slot + i][0][threadIdx.x]));
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __gri
                     fetch(m + kAhead, slot + i);
                     if (p.silu && (kWhole || m < there)) {
                         float2 u[V / 2];
-                        convolve<W, V, i>(w, bias, before, cur, reach, u);
+                        convolve<W, V, kAt>(w, bias, rows, reach, u);
 #pragma unroll
                         for (int e = 0; e < V / 2; ++e) {
                             // the slope: sigma + u sigma (1 - sigma)
@@ -346,15 +346,14 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __gri
                             du[e] = __fmul2_rn(du[e], __ffma2_rn(a, __ffma2_rn(s, both(-1.f), both(1.f)), s));
                         }
                     }
-                    constexpr int kMod = W - 1;
                     if (kWhole || m < n) {
 #pragma unroll
                         for (int k = 0; k < W; ++k) {
                             if (kWhole || k == 0 || k <= reach) {
-                                const int from = ((i - k) % kMod + kMod) % kMod;
+                                const int from = (kAt + W - k) % W;
 #pragma unroll
                                 for (int e = 0; e < V / 2; ++e)
-                                    dw[W - 1 - k][e] = __ffma2_rn(du[e], k == 0 ? cur[e] : before[from][e], dw[W - 1 - k][e]);
+                                    dw[W - 1 - k][e] = __ffma2_rn(du[e], rows[from][e], dw[W - 1 - k][e]);
                             }
                         }
 #pragma unroll
@@ -373,12 +372,12 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __gri
                         }
 #pragma unroll
                         for (int k = 0; k < W; ++k) {  // du of token s + k, which lies W - 1 - k back
-                            const int from = ((i + k) % kMod + kMod) % kMod;
+                            const int from = (kAt + k + 1) % W;
                             const int far = k == W - 1 ? reach : reached[from];
                             if (kWhole || k == 0 || far >= k) {
 #pragma unroll
                                 for (int e = 0; e < V / 2; ++e)
-                                    sum[e] = __ffma2_rn(w[W - 1 - k][e], k == W - 1 ? du[e] : dus[from][e], sum[e]);
+                                    sum[e] = __ffma2_rn(w[W - 1 - k][e], dus[from][e], sum[e]);
                             }
                         }
                         Pack<T, V> r;
@@ -387,17 +386,18 @@ __global__ void __launch_bounds__(kThreads, 4) short_conv_bwd_kernel(const __gri
                         else if (p.dstate) r.store((T*)p.dstate + (b * (W - 1) + m) * p.D + c);
                     }
                     if (kWhole || s >= 0) dx += p.dt;
-                    reached[i % kMod] = reach;
-#pragma unroll
-                    for (int e = 0; e < V / 2; ++e) {
-                        before[i % kMod][e] = cur[e];
-                        dus[i % kMod][e] = du[e];
-                    }
+                    if (!kWhole) reached[kAt] = reach;
                 };
                 if (reaches.full && clean && i0 >= W - 1 && i0 + U <= n) {
                     each<U>([&](auto index) { token(index, std::true_type()); });
                 } else {
-                    each<U>([&](auto index) { token(index, std::false_type()); });
+                    if (clean) {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) reached[j] = W - 1;
+                    }
+                    each<U>([&](auto index) {
+                        if (i0 + decltype(index)::value < n + W - 1) token(index, std::false_type());
+                    });
                 }
                 clean = reaches.full;  // U is at least W - 1
             }
@@ -448,13 +448,12 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const __grid_
     load_weights<W, V>(p, c, w, bias);
     for (long long b = blockIdx.y; b < p.B; b += gridDim.y) {
         if (b + gridDim.y < p.B) load(next, b + gridDim.y);
-        float2 u[V / 2], before[W - 1][V / 2], x[V / 2];
+        float2 u[V / 2], x[W][V / 2];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) rows[j].floats(before[j]);
-        rows[W - 1].floats(x);
+        for (int j = 0; j < W; ++j) rows[j].floats(x[j]);
 #pragma unroll
         for (int j = 1; j < W; ++j) rows[j].store((T*)p.state_out + (b * (W - 1) + j - 1) * p.D + c);
-        convolve<W, V, 0>(w, bias, before, x, W - 1, u);
+        convolve<W, V, W - 1>(w, bias, x, W - 1, u);
         if (p.silu) {
 #pragma unroll
             for (int k = 0; k < V / 2; ++k) u[k] = __fmul2_rn(u[k], sigmoid2<T>(u[k]));
