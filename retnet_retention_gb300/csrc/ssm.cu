@@ -29,8 +29,10 @@ namespace {
 
 constexpr int kJoinWarps = 16;
 
-// The state after a run of decay P (0: dropped) from s.
-__device__ __forceinline__ float after(float P, float b, float s) { return P == 0.f ? b : fmaf(P, s, b); }
+// The state after a run of decay P (below 0: a document starts in it, s is dropped) from s.  A decay
+// that underflows to 0 drops nothing: what is not a number stays so, as in an uncut walk.
+__device__ __forceinline__ float after(float P, float b, float s) { return P < 0.f ? b : fmaf(P, s, b); }
+__device__ __forceinline__ float behind(float P, float e) { return P < 0.f || e < 0.f ? -1.f : P * e; }
 
 struct Run4 {
     float4 P, b;
@@ -68,8 +70,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) ssm_join_kernel(
             }
         }
     };
-    auto decay = [&](float s) {  // of a chunk: 0 where a document starts in it
-        if (s == INFINITY) return make_float4(0.f, 0.f, 0.f, 0.f);
+    auto decay = [&](float s) {  // of a chunk: below 0 where a document starts in it
+        if (s == INFINITY) return make_float4(-1.f, -1.f, -1.f, -1.f);
         return make_float4(exp2_fast(s * a.x), exp2_fast(s * a.y), exp2_fast(s * a.z), exp2_fast(s * a.w));
     };
     auto step = [&](const float4& e, const float4& b4, const float4& s) {
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) ssm_join_kernel(
             for (int i = 0; i < kBatch; ++i) {
                 const float4 e = decay(sum[i]);
                 run.b = step(e, add[i], run.b);
-                run.P.x *= e.x; run.P.y *= e.y; run.P.z *= e.z; run.P.w *= e.w;
+                run.P = make_float4(behind(run.P.x, e.x), behind(run.P.y, e.y), behind(run.P.z, e.z), behind(run.P.w, e.w));
             }
         }
         runs[w][lane] = run;

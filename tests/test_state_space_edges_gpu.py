@@ -243,3 +243,36 @@ def test_rows_at_any_multiple_of_16_bytes(D, dtypes):
                    float(np.float32(1e-6)))
     ref.check("h'", got[0], p[0], p[1], th)
     ref.check("y", got[1], p[2], p[3], to)
+
+
+def test_a_decay_of_zero_drops_nothing():
+    """An infinite state times a decay that underflows is not a number, in a sequence cut into
+    chunks (T at least 512) as in two calls that are not; a document's start drops it in both."""
+    B, T, D, N = 1, 1000, 32, 16
+    g = torch.Generator().manual_seed(3)
+    x, b = torch.randn(B, T, D, generator=g).to(DEV), torch.randn(B, T, N, generator=g).to(DEV)
+    dt, A = torch.full((B, T, D), 40.0, device=DEV), torch.full((D, N), -50.0, device=DEV)
+    h0 = torch.zeros(B, D, N, device=DEV)
+    h0[0, 3] = float("inf")
+    dh = torch.zeros(B, D, N, device=DEV)
+    dh[0, 5] = float("inf")
+    for start in (None, 700):
+        pos = None
+        if start is not None:
+            pos = torch.ones(B, T, dtype=torch.int32, device=DEV)
+            pos[0, start] = 0
+        cut = lambda t, lo, hi: None if t is None else t[:, lo:hi].contiguous()
+        y, hT = la.ssm_fwd(x, dt, A, b, b, h0=h0, positions=pos)
+        parts, h = [], h0
+        for lo, hi in ((0, 400), (400, T - 200), (T - 200, T)):
+            p, h = la.ssm_fwd(*(cut(t, lo, hi) for t in (x, dt)), A, *(cut(t, lo, hi) for t in (b, b)), h0=h,
+                              positions=cut(pos, lo, hi))
+            parts.append(p)
+        dh0 = la.ssm_bwd(x, dt, A, b, b, torch.zeros_like(x), h0=torch.zeros_like(h0), positions=pos, dh_T=dh)[8]
+        torch.cuda.synchronize()
+        whole = torch.cat(parts, 1)
+        assert torch.equal(torch.isnan(y), torch.isnan(whole)) and torch.equal(torch.isnan(hT), torch.isnan(h))
+        there = torch.isnan(y)[0].any(0)
+        assert bool(there[3]) and int(there.sum()) == 1
+        assert bool(torch.isnan(y[0, -1, 3])) == (start is None)
+        assert bool(torch.isnan(dh0[0, 5]).all()) == (start is None) and not bool(torch.isnan(dh0[0, 4]).any())
