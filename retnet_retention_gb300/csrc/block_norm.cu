@@ -45,7 +45,7 @@ struct BlockParams {
     float *part_post, *part_gate, *part_pre;  // backward: partial rows, or null
     int B, T, D;
     int rows_cta;                  // rows a CTA holds at once
-    int ring;                      // backward: rows of it
+    int ring;                      // backward: rows of the ring in shared memory
     Divide by_T;
     int seq_blocks;                // CTAs a sequence's rows are shared out to (0: of all sequences)
     int post, pre, center, gate_each;
@@ -206,7 +206,8 @@ constexpr int fwd_ring(int threads) { return threads > 256 ? 3 : 1; }
 
 // T: o and y; R: the residual stream.  P pieces of eight entries a thread.
 template <typename T, typename R, int P, int THREADS, bool CENTER, bool WHOLE>
-__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS) block_norm_kernel(const __grid_constant__ BlockParams p) {
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 768 / THREADS)
+    block_norm_kernel(const __grid_constant__ BlockParams p) {
     __shared__ __align__(16) float red[4][kRedFloats];
     clear_red(red, 4);
     constexpr int kRing = fwd_ring(THREADS);
@@ -545,7 +546,10 @@ Shape shape(int D) {
 }
 
 // Bytes of a CTA's shared memory, T and R the sizes of an entry of o and of the residual.
-size_t fwd_shared(const Shape& sh, size_t T, size_t R) { return (size_t)fwd_ring(sh.threads * sh.rows) * sh.pieces * sh.threads * sh.rows * 8 * (T + R); }
+size_t fwd_shared(const Shape& sh, size_t T, size_t R) {
+    const size_t entries = (size_t)sh.pieces * sh.threads * sh.rows * 8;
+    return entries * fwd_ring(sh.threads * sh.rows) * (T + R);
+}
 size_t bwd_shared(const Shape& sh, size_t T, size_t R, int ring) {
     const size_t entries = (size_t)sh.pieces * sh.threads * sh.rows * 8;
     return entries * (ring * 2 * (T + R) + 2 * sizeof(float));  // the sums at the end fit in the ring
@@ -555,7 +559,8 @@ constexpr size_t kMostShared = 222 << 10;  // of a CTA, beside its static part
 
 // CTAs an SM holds: by the registers the launch bounds leave a thread, and by shared memory.
 long long resident(const Shape& sh, int threads_per_sm, size_t shared) {
-    const long long by_threads = threads_per_sm / (sh.threads * sh.rows), by_shared = (long long)((224u << 10) / (shared + 2048));
+    const long long by_threads = threads_per_sm / (sh.threads * sh.rows);
+    const long long by_shared = (long long)((224u << 10) / (shared + 2048));
     return std::max(1ll, std::min(by_threads, by_shared));
 }
 
@@ -580,7 +585,8 @@ long long fwd_blocks(const BlockNormArgs& a) {
 void bwd_blocks(const BlockNormArgs& a, int* each, long long* all) {
     const Shape sh = shape(a.D);
     // as many for either type of the residual: the workspace's size is asked for without it
-    const long long most = sm_count() * resident(sh, 512, bwd_shared(sh, entry_size(a.bf16), 4, bwd_ring(sh, entry_size(a.bf16), 4)));
+    const size_t entry = entry_size(a.bf16);
+    const long long most = sm_count() * resident(sh, 512, bwd_shared(sh, entry, 4, bwd_ring(sh, entry, 4)));
     if (a.gate && a.gate_each) {
         const long long rows = ((long long)a.T + sh.rows - 1) / sh.rows;
         *each = (int)std::max(1ll, std::min(rows, most / a.B));
@@ -617,7 +623,8 @@ template <typename T, typename R, int P, int THREADS, bool CENTER, bool WHOLE>
 cudaError_t launch(const BlockParams& p, bool bwd, unsigned grid, int threads, cudaStream_t s) {
     const Shape sh = shape(p.D);
     const size_t shared = bwd ? bwd_shared(sh, sizeof(T), sizeof(R), p.ring) : fwd_shared(sh, sizeof(T), sizeof(R));
-    const auto kernel = bwd ? block_norm_bwd_kernel<T, R, P, THREADS, CENTER, WHOLE> : block_norm_kernel<T, R, P, THREADS, CENTER, WHOLE>;
+    const auto kernel = bwd ? block_norm_bwd_kernel<T, R, P, THREADS, CENTER, WHOLE>
+                            : block_norm_kernel<T, R, P, THREADS, CENTER, WHOLE>;
     if (shared > 44 * 1024) {  // less, with the static part, a kernel has without asking
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;

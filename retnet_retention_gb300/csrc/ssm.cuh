@@ -7,9 +7,9 @@
 // The walk is bound by issue slots: for a token of a warp's 32 channels of 16 states 92 instructions, 32 of
 // them packed products that take two, so 124 of the 152 cycles it takes where a scheduler has two warps.  8 x 8192
 // tokens of 4096 channels: 1268 us (the 2^x alone 444, HBM 318); there 104 of 152 SMs hold two CTAs and
-// the others one, since a sequence's tokens come one after another.  Not kept, at that size: more lanes a channel (1615 to 1810
-// us), products one by one (slower beside the 2^x), loops of 4 or 16 tokens (1681, 1630), more CTAs an SM
-// by fewer registers.
+// the others one, since a sequence's tokens come one after another.  Not kept, at that size: more lanes a
+// channel (1615 to 1810 us), products one by one (slower beside the 2^x), loops of 4 or 16 tokens (1681,
+// 1630), more CTAs an SM by fewer registers.
 #pragma once
 
 #include <type_traits>
@@ -215,12 +215,13 @@ __device__ __forceinline__ void copy_piece(void* to, const void* from, bool vali
 // local states every kBlock tokens.
 //
 // A warp copies the next tile's rows in the background, those of its channels and b and c (which
-// it brings to fp32 itself: 1.5 instructions a token, and no barrier among warps).  The elementwise work of a token and channel is
-// done by one lane: register 0 of CH = 2 is the lane's own channel (2 cl + (j & 1)), and its own
+// it brings to fp32 itself: 1.5 instructions a token, and no barrier among warps).  The elementwise work
+// of a token and channel is done by one lane: register 0 of CH = 2 is the lane's own channel (2 cl + (j & 1)), and its own
 // tokens are every M-th.  Tiles in which a document starts or the chunk ends, and for the summary those
 // behind a start, take the careful form of the loop.
 template <typename S>
-__global__ void __launch_bounds__(kWarps * 32, S::MODE == kState ? 4 : 3) ssm_scan_kernel(const __grid_constant__ SsmParams p) {
+__global__ void __launch_bounds__(kWarps * 32, S::MODE == kState ? 4 : 3)
+    ssm_scan_kernel(const __grid_constant__ SsmParams p) {
     using T = typename S::Elem;
     constexpr int CH = S::CH, NS = S::NS, N = S::N, CL = S::CL, WC = S::WC, U = S::U, M = S::M, K = S::K;
     constexpr bool kY = S::MODE == kForward, kBack = S::MODE == kSummary, kGate = S::MODE != kState;
