@@ -511,10 +511,12 @@ LA_API la_status la_scan_step(const void* x, la_dtype dtype, const float* log_a,
  *   positions DEVICE int32 [B][T], each token's place in its document, or NULL: a tap k
  *             tokens back counts only where k <= positions[b][t] (documents packed one
  *             behind another, or padding before a sequence).  What does not count is not
- *             read into the sum, infinities and NaN included.  The taps of a token below
- *             W - 1 of no other document reach into the state.
- *   state_out [B][W-1][D] dtype: the last W - 1 rows of state and x, or NULL; may be
- *             state itself, else may not overlap it
+ *             read into the sum, infinities and NaN included.  Taps that count and lie
+ *             before token 0 read the state.
+ *   state_out [B][W-1][D] dtype: the last W - 1 rows of state and x as they are, those of
+ *             another document or of padding among them, or NULL; may be state itself,
+ *             else may not overlap it.  A call that goes on from there gives its tokens'
+ *             positions (la_short_conv_step_at for single ones).
  *   flags     LA_CONV_SILU
  * No output may overlap an input (state_out: but state itself) or another output.  Sums in
  * fp32, rounded once.  D a multiple of 16, B * T at most 2^31 - 256, B * D at most 2^33,
@@ -554,13 +556,25 @@ LA_API size_t la_short_conv_bwd_workspace_size(int B, int T, int D, int W, la_dt
 
 /*
  * One token of la_short_conv_fwd: x [B][D] dtype with x_stride elements from sequence to
- * sequence, y [B][D] dense.  state [B][W-1][D] and state_out as there (state_out may be
- * state itself).  Errors as la_short_conv_fwd.
+ * sequence, y [B][D] dense.  state [B][W-1][D], every row of which counts, and state_out as
+ * there (state_out may be state itself).  Errors as la_short_conv_fwd.
  */
 LA_API la_status la_short_conv_step(const void* x, long long x_stride, la_dtype dtype,
                                     const float* weight, const float* bias, int B, int D, int W,
                                     unsigned flags, const void* state, void* state_out, void* y,
                                     la_stream_t stream);
+
+/*
+ * la_short_conv_step of tokens at their places in their documents: positions DEVICE int32 [B],
+ * as la_short_conv_fwd's, or NULL: a tap k tokens back counts only where k <= positions[b].
+ * The state behind a packed or padded prompt holds its last W - 1 rows whatever they belong
+ * to, and la_short_conv_step counts them all: tokens at positions below W - 1 need this
+ * call.  The state moves up all the same.
+ */
+LA_API la_status la_short_conv_step_at(const void* x, long long x_stride, la_dtype dtype,
+                                       const float* weight, const float* bias, int B, int D, int W,
+                                       unsigned flags, const void* state, const int* positions,
+                                       void* state_out, void* y, la_stream_t stream);
 
 /*
  * The selective scan: "decay the old state, add, read out" with N numbers of state a
@@ -632,7 +646,8 @@ LA_API size_t la_ssm_bwd_workspace_size(int B, int T, int D, int N, int G, la_dt
 /*
  * One token of la_ssm_fwd: x, dt, gate [B][D], b, c [B][G][N] dtype; strides: HOST array
  * of 5 strides from sequence to sequence, for x, dt, b, c and gate, or NULL (dense);
- * h_in, h_out [B][D][N] fp32, h_out may be h_in itself; y [B][D] dense.
+ * h_in, h_out [B][D][N] fp32, h_out may be h_in itself (a sequence that starts here begins
+ * from zeros); y [B][D] dense.
  * Errors as la_ssm_fwd.
  */
 LA_API la_status la_ssm_step(const void* x, const void* dt, const float* A, const void* b,

@@ -149,6 +149,8 @@ def _load() -> ctypes.CDLL:
     lib.la_short_conv_bwd_workspace_size.restype = sz
     lib.la_short_conv_step.argtypes = [vp, ll, i, vp, vp, i, i, i, u, vp, vp, vp, vp]
     lib.la_short_conv_step.restype = i
+    lib.la_short_conv_step_at.argtypes = [vp, ll, i, vp, vp, i, i, i, u, vp, vp, vp, vp, vp]
+    lib.la_short_conv_step_at.restype = i
     lib.la_ssm_fwd.argtypes = [vp] * 9 + [i, i, i, i, i, i, u, vp, vp, vp, vp, vp, sz, vp]
     lib.la_ssm_fwd.restype = i
     lib.la_ssm_workspace_size.argtypes = [i, i, i, i, i, i]
@@ -995,8 +997,8 @@ def short_conv_fwd(x, weight, *, bias=None, silu=True, state=None, positions=Non
     bias fp32 [D], then u * sigmoid(u) with silu.  state [B,W-1,D]: the rows before token 0
     (None: zeros).  positions int32 [B,T]: a tap k tokens back counts only where
     k <= positions (packed documents, padding in front).  Returns (y [B,T,D], the state
-    behind the last token); the state is None when return_state is False and no state_out was
-    given.  state_out may be state."""
+    behind the last token: the last W-1 rows, whatever document they belong to); the state is
+    None when return_state is False and no state_out was given.  state_out may be state."""
     W, dev, code, w, b = _conv_shape(x, weight, bias, 3)
     B, T, D = x.shape
     dt, held = x.dtype, (B, W - 1, D)
@@ -1043,9 +1045,11 @@ def short_conv_bwd(x, weight, dy, *, bias=None, silu=True, state=None, positions
     return dx, dw, db, d0
 
 
-def short_conv_step(x, weight, state, *, bias=None, silu=True, out=None, state_out=None, stream=None):
+def short_conv_step(x, weight, state, *, bias=None, silu=True, positions=None, out=None, state_out=None, stream=None):
     """One token of short_conv_fwd: x [B,D] (rows dense); state [B,W-1,D] moves up by one
-    row, in place or into state_out.  Returns y [B,D]."""
+    row, in place or into state_out.  positions int32 [B]: a tap k tokens back counts only
+    where k <= positions, as in short_conv_fwd; without them every row of the state counts,
+    which is wrong behind a padded or packed prompt of fewer than W-1 tokens.  Returns y [B,D]."""
     W, dev, code, w, b = _conv_shape(x, weight, bias, 2)
     B, D = x.shape
     dt, held = x.dtype, (B, W - 1, D)
@@ -1055,8 +1059,10 @@ def short_conv_step(x, weight, state, *, bias=None, silu=True, out=None, state_o
         out, y = _output(out, "out", (B, D), dt, dev)
         old = _dense(state, "state", held, dt, dev)
         new = old if state_out is None else _dense(state_out, "state_out", held, dt, dev)
-        st = _load().la_short_conv_step(x.data_ptr(), x.stride(0), code, w, b, B, D, W, LA_CONV_SILU if silu else 0,
-                                        old, new, y, s)
+        positions = _aligned(positions)
+        st = _load().la_short_conv_step_at(x.data_ptr(), x.stride(0), code, w, b, B, D, W,
+                                           LA_CONV_SILU if silu else 0, old,
+                                           _dense(positions, "positions", (B,), torch.int32, dev), new, y, s)
     _check(st, "la_short_conv_step")
     return out
 

@@ -274,13 +274,13 @@ la_status la_short_conv_bwd(const void* x, const long long* x_strides, const voi
     return cuda_status(launch_short_conv_bwd(a, s));
 }
 
-la_status la_short_conv_step(const void* x, long long x_stride, la_dtype dtype, const float* weight,
-                             const float* bias, int B, int D, int W, unsigned flags, const void* state,
-                             void* state_out, void* y, la_stream_t stream) {
+la_status la_short_conv_step_at(const void* x, long long x_stride, la_dtype dtype, const float* weight,
+                                const float* bias, int B, int D, int W, unsigned flags, const void* state,
+                                const int* positions, void* state_out, void* y, la_stream_t stream) {
     ShortConvArgs a;
     const la_status st = conv_args(&a, weight, bias, dtype, B, 1, D, W, flags);
     if (st != LA_OK || B == 0) return st;
-    if (!state || !state_out || !y || any_misaligned({state, state_out, y})) return LA_ERR_INVALID_ARG;
+    if (!state || !state_out || !y || any_misaligned({state, positions, state_out, y})) return LA_ERR_INVALID_ARG;
     const size_t es = elem_size(dtype), held = (size_t)B * (W - 1) * D * es;
     const long long xs[2] = {x_stride, 0};
     View vx;
@@ -290,13 +290,21 @@ la_status la_short_conv_step(const void* x, long long x_stride, la_dtype dtype, 
     m.input(vx);
     m.input(weight, (size_t)D * W * 4);
     m.input(bias, (size_t)D * 4);
+    m.input(positions, (size_t)B * 4);
     if (state != state_out) m.input(state, held);
     m.output(state_out, held);
     m.output(y, (size_t)B * D * es);
     if (!m.ok()) return LA_ERR_INVALID_ARG;
-    a.x = x; a.y = y; a.state = state; a.state_out = state_out;
+    a.x = x; a.y = y; a.state = state; a.state_out = state_out; a.positions = positions;
     keep(a.x_strides, vx);
     return cuda_status(launch_short_conv_step(a, (cudaStream_t)stream));
+}
+
+la_status la_short_conv_step(const void* x, long long x_stride, la_dtype dtype, const float* weight,
+                             const float* bias, int B, int D, int W, unsigned flags, const void* state,
+                             void* state_out, void* y, la_stream_t stream) {
+    return la_short_conv_step_at(x, x_stride, dtype, weight, bias, B, D, W, flags, state, nullptr, state_out, y,
+                                 stream);
 }
 
 la_status la_ssm_fwd(const void* x, const void* dt, const float* A, const void* b, const void* c,
