@@ -591,8 +591,8 @@ LA_API la_status la_short_conv_step_at(const void* x, long long x_stride, la_dty
  *             c, gate and y in this order, or NULL (all dense): rows (of D or G N entries)
  *             dense, strides >= 0 and multiples of 16 bytes, y's rows apart.  The stride of a
  *             dimension of size 1 is not read.
- *   A         DEVICE fp32 [D][N], finite (as a rule below 0);  skip, dt_bias DEVICE fp32
- *             [D] or NULL (zero)
+ *   A         DEVICE fp32 [D][N], finite (as a rule below 0; each token's exp(delta A)
+ *             inside the fp32 range);  skip, dt_bias DEVICE fp32 [D] or NULL (zero)
  *   h0        [B][D][N] fp32 initial state or NULL for zero; may be h_out itself, else may
  *             not overlap it
  *   positions DEVICE int32 [B][T] or NULL: a token with position 0 starts a document: the old state

@@ -29,13 +29,11 @@ namespace {
 
 constexpr int kJoinWarps = 16;
 
-// The state after a run of decay P (below 0: a document starts in it, s is dropped) from s.  A decay
-// that underflows to 0 drops nothing: what is not a number stays so, as in an uncut walk.
-__device__ __forceinline__ float after(float P, float b, float s) { return P < 0.f ? b : fmaf(P, s, b); }
-__device__ __forceinline__ float behind(float P, float e) { return P < 0.f || e < 0.f ? -1.f : P * e; }
-
+// A run of chunks: the sum of its delta (infinity: a document starts in it, what enters is
+// dropped) and the state it reaches from zero.
 struct Run4 {
-    float4 P, b;
+    float4 b;
+    float sum;
 };
 
 // v[b][chunk][D][N]: what a chunk adds becomes what enters it, in place; from the first
@@ -70,29 +68,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) ssm_join_kernel(
             }
         }
     };
-    auto decay = [&](float s) {  // of a chunk: below 0 where a document starts in it
-        if (s == INFINITY) return make_float4(-1.f, -1.f, -1.f, -1.f);
-        return make_float4(exp2_fast(s * a.x), exp2_fast(s * a.y), exp2_fast(s * a.z), exp2_fast(s * a.w));
-    };
-    auto step = [&](const float4& e, const float4& b4, const float4& s) {
-        return make_float4(after(e.x, b4.x, s.x), after(e.y, b4.y, s.y), after(e.z, b4.z, s.z), after(e.w, b4.w, s.w));
+    // The state behind a chunk or run from s.  A decay that underflows drops nothing: what is not a number
+    // stays so, as in an uncut walk.
+    auto step = [&](float d_sum, const float4& b4, const float4& s) {
+        if (d_sum == INFINITY) return b4;
+        return make_float4(carry(d_sum * a.x, s.x, b4.x), carry(d_sum * a.y, s.y, b4.y), carry(d_sum * a.z, s.z, b4.z),
+                           carry(d_sum * a.w, s.w, b4.w));
     };
     load(k0);
     float4 s = s0 ? s0[b * quads + quad] : make_float4(0.f, 0.f, 0.f, 0.f);
     if (warps > 1) {
-        Run4 run = {make_float4(1.f, 1.f, 1.f, 1.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        Run4 run = {make_float4(0.f, 0.f, 0.f, 0.f), 0.f};
         for (int k = k0; k < k1; k += kBatch) {
             if (k > k0) load(k);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const float4 e = decay(sum[i]);
-                run.b = step(e, add[i], run.b);
-                run.P = make_float4(behind(run.P.x, e.x), behind(run.P.y, e.y), behind(run.P.z, e.z), behind(run.P.w, e.w));
+                run.b = step(sum[i], add[i], run.b);
+                run.sum += sum[i];
             }
         }
         runs[w][lane] = run;
         __syncthreads();
-        for (int k = 0; k < w; ++k) s = step(runs[k][lane].P, runs[k][lane].b, s);
+        for (int k = 0; k < w; ++k) s = step(runs[k][lane].sum, runs[k][lane].b, s);
     }
     for (int k = k0; k < k1; k += kBatch) {
         if (k > k0 || k1 - k0 > kBatch) load(k);
@@ -100,7 +97,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) ssm_join_kernel(
         for (int i = 0; i < kBatch; ++i)
             if (k + i < k1) {
                 v[at(k + i) * quads + quad] = s;
-                s = step(decay(sum[i]), add[i], s);
+                s = step(sum[i], add[i], s);
             }
     }
 }

@@ -75,6 +75,23 @@ constexpr float kLog2e = 1.4426950408889634f;
 // applied a thousand times: raised, the mean error is below 0.8e-8 there.  2^kRaise is 1.
 constexpr float kRaise = 2e-8f;
 
+// 2^(x / 2), finite: what is carried over many tokens is multiplied by it twice, so that a decay past the
+// fp32 range, above 2^128 or below 2^-126, meets a small or large number as token by token, and
+// 0 stays 0.  Bounded at 2^127.5, it brings every normal number past the range at x = 255.
+__device__ __forceinline__ float half_decay(float x) { return exp2_fast(fminf(fmaf(0.5f, x, kRaise), 127.5f)); }
+
+// The same of two states' sum A.
+__device__ __forceinline__ float2 half_decay2(float sum, float2 A) {
+    const float2 x = __ffma2_rn(both(0.5f * sum), A, both(kRaise));
+    return make_float2(exp2_fast(fminf(x.x, 127.5f)), exp2_fast(fminf(x.y, 127.5f)));
+}
+
+// 2^x s + b
+__device__ __forceinline__ float carry(float x, float s, float b) {
+    const float e = half_decay(x);
+    return fmaf(e, e * s, b);
+}
+
 // log(1 + p) for p in [0, 1], 1.7e-7 relative (p = 0 included): p times a polynomial of
 // degree 8 fitted to log(1 + p) / p in the relative maximum norm.  No logarithm, so that
 // small steps keep all their digits.
@@ -207,6 +224,28 @@ __device__ __forceinline__ void copy_piece(void* to, const void* from, bool vali
                      "l"(from), "n"(BYTES), "r"(valid ? BYTES : 0)
                      : "memory");
     }
+}
+
+// What a chunk passes back to one state, sum_t exp(A sum_(s <= t) delta_s) c_t du_t, each decay by its
+// exponent: where decays grow, their product P leaves the fp32 range although what it meets is 0 or
+// small.
+template <typename T>
+__device__ __noinline__ float passed_back(const SsmParams& p, long long b, int t0, int t1, int c, int g, int n) {
+    const float bias = p.bias ? p.bias[c] : 0.f, A = p.A[(size_t)c * p.N + n] * kLog2e;
+    float sum = 0.f, back = 0.f;
+    for (int t = t0; t < t1; ++t) {
+        if (p.positions && p.positions[b * p.T + t] == 0) break;
+        auto at = [&](const SsmRows& r, int e) { return load_elem((const T*)r.p + b * r.b + t * r.t, e); };
+        const float v = at(p.dt, c) + bias;
+        sum += p.softplus ? softplus<T>(v) : v;
+        float du = at(p.dy, c);
+        if (p.gate.p) {
+            const float z = at(p.gate, c);
+            du *= z * sigmoid<T>(z);
+        }
+        back = carry(sum * A, du * at(p.cm, g * p.N + n), back);
+    }
+    return back;
 }
 
 // One walk over a chunk of tokens for a tile of channels: kForward writes y from the state
@@ -509,6 +548,15 @@ __global__ void __launch_bounds__(kWarps * 32, S::MODE == kState ? 4 : 3)
         } else {
             const long long at = (b * p.chunks + chunk) * p.D + c[q];
             put(p.chunk_h + at * N, h[q]);
+            if constexpr (kBack) {
+                bool finite = true;  // an infinite P leaves no finite sum
+#pragma unroll
+                for (int i = 0; i < NS; ++i) finite = finite && fabsf(back[q][i]) < INFINITY;
+                if (!finite) {
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) back[q][i] = passed_back<T>(p, b, t0, t1, c[q], g, j * NS + i);
+                }
+            }
             if constexpr (kBack) put(p.chunk_g + at * N, back[q]);
             if (j == 0) p.chunk_s[at] = cut ? INFINITY : sum[q];
         }

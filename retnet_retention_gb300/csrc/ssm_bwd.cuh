@@ -268,9 +268,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) ssm_gradients_kernel(const 
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float2 local = i == 0 ? make_float2(f.x, f.y) : make_float2(f.z, f.w);
-                    const float2 e = __fmul2_rn(both(sum), A[q][i]);
-                    enter[q][i] = sum == INFINITY ? local
-                                                  : __ffma2_rn(make_float2(exp2_fast(e.x), exp2_fast(e.y)), hin[q][i], local);
+                    const float2 e = half_decay2(sum, A[q][i]);
+                    enter[q][i] = sum == INFINITY ? local : __ffma2_rn(e, __fmul2_rn(e, hin[q][i]), local);
                 }
             }
         }
