@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) ssm_join_kernel(
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 run.b = step(sum[i], add[i], run.b);
-                run.sum += sum[i];
+                run.sum = run.sum == INFINITY || sum[i] == INFINITY ? INFINITY : run.sum + sum[i];  // NaN too ends there
             }
         }
         runs[w][lane] = run;

@@ -77,13 +77,18 @@ constexpr float kRaise = 2e-8f;
 
 // 2^(x / 2), finite: what is carried over many tokens is multiplied by it twice, so that a decay past the
 // fp32 range, above 2^128 or below 2^-126, meets a small or large number as token by token, and
-// 0 stays 0.  Bounded at 2^127.5, it brings every normal number past the range at x = 255.
-__device__ __forceinline__ float half_decay(float x) { return exp2_fast(fminf(fmaf(0.5f, x, kRaise), 127.5f)); }
+// 0 stays 0.  Bounded at 2^127.5, it brings every normal number past the range at x = 255.  What is
+// not a number stays so.
+__device__ __forceinline__ float bounded_exp2(float v) {
+    asm("min.NaN.f32 %0, %0, 0f42ff0000;" : "+f"(v));  // 127.5
+    return exp2_fast(v);
+}
+__device__ __forceinline__ float half_decay(float x) { return bounded_exp2(fmaf(0.5f, x, kRaise)); }
 
 // The same of two states' sum A.
 __device__ __forceinline__ float2 half_decay2(float sum, float2 A) {
     const float2 x = __ffma2_rn(both(0.5f * sum), A, both(kRaise));
-    return make_float2(exp2_fast(fminf(x.x, 127.5f)), exp2_fast(fminf(x.y, 127.5f)));
+    return make_float2(bounded_exp2(x.x), bounded_exp2(x.y));
 }
 
 // 2^x s + b

@@ -95,3 +95,43 @@ def test_a_small_state_grows_and_a_small_gradient(sign):
     dy[:, 50, grows] = 1e-30
     h0 = torch.where(grows[:, None], 1e-30, 1.0).expand(D, N)[None].contiguous()
     check(s, options(h0=h0), dy, torch.zeros_like(h0))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,at,start", [(300, 150, None), (300, 150, 200), (300, 150, 120), (700, 640, 660), (700, 600, 660),
+                                        (5000, 2500, None), (5000, 2500, 2600)])
+def test_a_step_that_is_not_a_number_stays_so(T, at, start, dtype):
+    """A NaN step: its channel's states behind it and gradients before it are NaN up to a document's
+    start, where no gradient comes in behind it too; the other channels keep their bits."""
+    D, N, ch = 32, 16, 5
+    s, dy, _ = sequence(T, D, N, 1, 0.01)
+    s["A"] = -s["A"].abs()
+    dy[:, at - 10:, ch] = 0.0
+    s, dy = {n: t if n == "A" else t.to(dtype) for n, t in s.items()}, dy.to(dtype)
+    pos = None
+    if start is not None:
+        pos = torch.ones(1, T, dtype=torch.int32, device=DEV)
+        pos[0, start] = 0
+    h0 = torch.ones(1, D, N, device=DEV)
+    opts, grad = options(h0=h0, positions=pos), options(h0=h0, positions=pos, dh_T=torch.zeros_like(h0))
+    y, hT = la.ssm_fwd(**s, **opts)
+    want = la.ssm_bwd(*s.values(), dy, **grad)
+    s["dt"] = s["dt"].clone()
+    s["dt"][0, at, ch] = float("nan")
+    y2, hT2 = la.ssm_fwd(**s, **opts)
+    got = la.ssm_bwd(*s.values(), dy, **grad)
+    torch.cuda.synchronize()
+    others = [k for k in range(D) if k != ch]
+    end = T if start is None or start < at else start
+    begin = 0 if start is None or start > at else start  # gradients pass back to here
+    nan = torch.isnan(y2[0, :, ch])
+    assert bool(nan[at:end].all()) and not bool(nan[:at].any()) and not bool(nan[end:].any())
+    assert torch.equal(y2[..., others], y[..., others]) and torch.equal(hT2[:, others], hT[:, others])
+    assert bool(torch.isnan(hT2[0, ch]).all()) == (end == T)
+    dx, ddt, dh0 = got[0], got[1], got[8]
+    for v, w in ((dx, want[0]), (ddt, want[1])):
+        nan = torch.isnan(v[0, :, ch])
+        assert bool(nan[begin:at + 1].all()) and not bool(nan[:begin].any())
+        assert torch.equal(v[..., others], w[..., others])
+    assert bool(torch.isnan(dh0[0, ch]).all()) == (begin == 0)
+    assert torch.equal(dh0[:, others], want[8][:, others])
