@@ -523,7 +523,6 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_bwd_kernel(
 // d(gate) of each sequence: its CTAs' partial rows, added in order.
 __global__ void __launch_bounds__(128) block_gate_sum_kernel(const float* part, int blocks, int D, float* out) {
     const int c = blockIdx.x * 128 + threadIdx.x;
-    tc::griddep_wait();
     if (c >= D) return;
     const float* from = part + (size_t)blockIdx.y * blocks * D + c;
     float v = 0.f;

@@ -163,38 +163,6 @@ __device__ __forceinline__ float share_sums(float (&v)[L], int j, int gap) {
     return v[0];
 }
 
-// The rows of b and c of a tile of tokens, as fp32 [token][2 N]: loads into registers
-// ahead of time, then into shared memory.
-template <typename T, int N, int THREADS, int TOKENS>
-struct SharedRows {
-    static constexpr int kPieces = TOKENS * 2 * N / 8, kEach = (kPieces + THREADS - 1) / THREADS;
-    Raw8<T> raw[kEach];
-
-    __device__ __forceinline__ void load(const SsmParams& p, long long b, int g, int t0, int t1) {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int q = i * THREADS + threadIdx.x, row = q / (2 * N / 8), part = q % (2 * N / 8);
-            const bool c = part >= N / 8;
-            const SsmRows& from = c ? p.cm : p.bm;
-            raw[i] = Raw8<T>();
-            if (q < kPieces && t0 + row < t1)
-                raw[i] = raw8<true>((const T*)from.p + b * from.b + (long long)(t0 + row) * from.t + g * N +
-                                        (part - (c ? N / 8 : 0)) * 8, 0, 4);
-        }
-    }
-    __device__ __forceinline__ void store(float* to) const {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int q = i * THREADS + threadIdx.x;
-            if (q < kPieces) {
-                float2 x[4];
-                floats8<false>(raw[i], x);
-                store8<true, false>(to + q * 8, 0, 4, x);
-            }
-        }
-    }
-};
-
 enum Mode { kForward, kState, kSummary };  // kState: a chunk's state alone; kSummary: for the gradients
 
 // A walk's shape: a channel's N states lie with L lanes, NS = N / L each; a lane holds CH
