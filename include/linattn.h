@@ -601,7 +601,9 @@ LA_API la_status la_short_conv_step_at(const void* x, long long x_stride, la_dty
  *   flags     LA_SSM_SOFTPLUS
  *   workspace at least la_ssm_workspace_size(...) bytes (which may be 0); overwritten;
  *             one for each call that may run at once
- * States, decays and sums are fp32; y is rounded where it is stored.  No output may overlap an
+ * States, decays and sums are fp32; y is rounded where it is stored.  A decay is one hardware 2^x (2 ulp);
+ * with dtype bf16 the softplus and the gate's sigmoid take theirs too, off by 2^-22 |v| of
+ * themselves, which h_out and the fp32 gradients inherit.  No output may overlap an
  * input or another output.  D a multiple of 16, B and G < 65536, B * T at most 2^31 - 256,
  * D * N < 2^31, B * D * N at most 2^33.  T == 0: h_out is the initial state.  B == 0 is a no-op.
  * Errors: LA_ERR_INVALID_ARG, LA_ERR_CUDA.

@@ -10,6 +10,9 @@ namespace la {
 
 namespace {
 
+// From kQuadColumns columns on a lane adds four: a quarter of the CTAs, of 1024 threads each (the scan's
+// gradients, 64 to 256 rows: 65536 columns 15 us, one a lane 27; 32768 12 and 17; 16384 11 and 12: there and
+// below the sums stay with one).
 constexpr int kSumWarps = 32, kQuadColumns = 32768;
 
 struct Sums {

@@ -519,8 +519,9 @@ ConvParams fwd_params(const ShortConvArgs& a) {
     return p;
 }
 
-// Backward: the CTAs that fit at once, each as many runs of about kRun tokens as the others
-// (4 x 4093 tokens of 4096 channels: 304 runs of 54 for 304 places; 256 of 64 took a sixth longer).
+// Backward: the CTAs that fit at once, each as many runs of about kRun tokens as the others (4 x 4093
+// tokens of 4096 channels: 228 runs of 72 tokens, three for each of 76 places; with 256 of 64 some
+// places would take four).
 ConvParams bwd_params(const ShortConvArgs& a) {
     ConvParams p = params(a);
     tile(&p, 4);

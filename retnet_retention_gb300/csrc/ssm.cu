@@ -261,11 +261,14 @@ Plan plan_of(const SsmArgs& a, Split split, int channels_cta, long long chunks) 
     return p;
 }
 
-// One walk where the channels give a scheduler nearly a warp: a warp alone takes 230 cycles
-// a token, two together 350.  With fewer the sequences are cut, down to chunks of 32 tokens, which
-// costs a second walk (8 x 2048 tokens of 16 states: 1024 channels 150 us cut, 222 not; 1536
-// 222 either way; 2048 271 cut, 223 not).  Where even that leaves few warps, four states a lane
-// (3 x 512 tokens of 208 channels: 14 us, with sixteen 19).
+// One walk where the channels give a scheduler more than half a warp: a warp alone takes 203 cycles
+// a token, two together 322.  With fewer the sequences are cut, down to chunks of 32 tokens, which
+// costs a second walk (8 x 2048 tokens of 16 states: 1024 channels 144 us cut, 169 not; 1280 175 and 202;
+// 1536 205 and 202; 2048 271 and 203; 5 x 8192 of 4096 channels 1296 and 1258, although eight SMs hold
+// two CTAs and the others one; 8 x 8192 of 1536, at the border, 755 and 800).  Below 512 tokens one launch
+// instead of three (3 x 256 of 208 channels 17 us, cut 12 in a graph, where the caller's two more
+// launches do not count).  Where even that leaves few warps, four states a lane (3 x 512 tokens of 208
+// channels: 13.6 us, with sixteen 14.4).
 Plan forward_plan(const SsmArgs& a) {
     const long long sms = sm_count();
     Split split = wide_split(a.N);
@@ -277,6 +280,11 @@ Plan forward_plan(const SsmArgs& a) {
     return plan_of(a, split, split.cta(), chunks);
 }
 
+// As many chunks as give an SM 28 CTAs of the gradients' walk, of 64 tokens at least: more chunks fill
+// the last turn of the card better and cost the join (4 x 4096 tokens of 2048 channels: 28 CTAs an SM 916 us,
+// 14 950, 8 1001, 56 954).  Chunks of 32 tokens would shorten small calls (1 x 512 of 1024 channels 40 us, with
+// 64 52, 128 86; 1 x 2048 of 512 channels 56, 59, 85; 4 x 512 of 2048 152, 154, 174) and take their part of the
+// workspace twice.
 Plan backward_plan(const SsmArgs& a, int channels) {
     const long long tiles = (a.D / a.G + channels - 1) / channels;
     const long long ctas = (long long)a.B * a.G * tiles, want = (long long)sm_count() * 28;

@@ -5,7 +5,8 @@
 //   h_t = exp(delta A) h_(t-1) + delta x b_t,   y_t = (c_t . h_t + skip x) gate sigmoid(gate)
 //
 // The walk is bound by issue slots: for a token of a warp's 32 channels of 16 states 92 instructions, 32 of
-// them packed products that take two, so 124 of the 152 cycles it takes where a scheduler has two warps.  8 x 8192
+// them packed products that take two, so 124 of the 161 cycles it takes where every scheduler has two warps
+// (16 x 4096 tokens of 2432 channels: 638 us; with one warp each, 8 sequences, 402).  8 x 8192
 // tokens of 4096 channels: 1268 us (the 2^x alone 444, HBM 318); there 104 of 152 SMs hold two CTAs and
 // the others one, since a sequence's tokens come one after another.  Not kept, at that size: more lanes a
 // channel (1615 to 1810 us), products one by one (slower beside the 2^x), loops of 4 or 16 tokens (1681,

@@ -13,8 +13,8 @@
 // is walked backward: the first half's are computed twice, which costs less than the warps
 // that the registers of a whole block would.
 //
-// 4 x 4096 tokens of 2048 channels of 16 states: 643 us of this walk, after 231 of the summary walk and
-// 21 of the join, before 31 of the sums; bound by issue slots, 233 instructions for a token of a warp's 16
+// 4 x 4096 tokens of 2048 channels of 16 states: 646 us of this walk, after 234 of the summary walk and
+// 23 of the join, before 33 of the sums; bound by issue slots, 233 instructions for a token of a warp's 16
 // channels, 58 of them packed, at 3 warps a scheduler (what 168 registers leave); HBM is at 16 %.
 //
 // A lane holds four states of two channels.  Sums over n cross L = N / 4 lanes, sums over
