@@ -1063,7 +1063,7 @@ def short_conv_step(x, weight, state, *, bias=None, silu=True, positions=None, o
         st = _load().la_short_conv_step_at(x.data_ptr(), x.stride(0), code, w, b, B, D, W,
                                            LA_CONV_SILU if silu else 0, old,
                                            _dense(positions, "positions", (B,), torch.int32, dev), new, y, s)
-    _check(st, "la_short_conv_step")
+    _check(st, "la_short_conv_step_at")
     return out
 
 
@@ -1281,9 +1281,11 @@ def block_norm_bwd(o, h_out, dy, dh_out=None, *, post_norm=False, post_weight=No
     None with pre_norm False) and dh_out (that of h_out, or None): (d_o [B,T,D], dh [B,T,D]
     of h_out's type, dpost_weight [D], dgate like gate, dpre_weight [D]).  A gradient is None
     where its input is; the last three with weight_grads False, dh with residual_grad False (a
-    call that had no residual).  d_o and dh may be given, with strides; dh may be dh_out."""
-    code, rcode, rty, flags, (wp, g, wq) = _block_args(o, h_out, post_norm, post_weight, gate, pre_norm, pre_weight,
-                                                       center)
+    call that had no residual).  h_out may be None with pre_norm False, which does not read it
+    (the residual is of dh_out's type then).  d_o and dh may be given, with strides; dh may be
+    dh_out."""
+    code, rcode, rty, flags, (wp, g, wq) = _block_args(o, dh_out if h_out is None else h_out, post_norm, post_weight,
+                                                       gate, pre_norm, pre_weight, center)
     B, T, D = o.shape
     ty, dev, shape, f32 = o.dtype, o.device, (B, T, D), torch.float32
     if (dy is not None) != bool(pre_norm):
